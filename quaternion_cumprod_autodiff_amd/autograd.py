@@ -222,3 +222,65 @@ def gated_deltanet2(query, key, value, erase, write, log_decay, initial_state, *
         return GatedDeltaNet2Function.apply(*ins, chunk)
     context, state, _ = capi.gdn2_fwd(*[t.contiguous() for t in ins], chunk=chunk, want_boundary=not low_memory)
     return context, state
+
+
+# ---------------------------------------------------------------------------
+# Language-model operators (include/gated_delta.h, include/qk_norm.h).
+
+def _grads_wanted(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def gated_delta_step(query, key, value, log_decay, beta, state, *, slots=None, scale=None):
+    """One or a few new tokens of the gated delta rule (:func:`gated_delta_rule`)
+    for each batch row, for decoding: query, key [B, T, Hk, K], value
+    [B, T, Hv, V], log_decay and beta [B, T, Hv] float32.  ``state``, a pool
+    [slots, Hv, K, V] float32, is updated in place; row n uses state slots[n]
+    (int32; without ``slots`` state n).  Returns out [B, T, Hv, V].  A row
+    whose slot is outside the pool (-1 for padding) or named by an earlier row
+    is not run: its out is zero.  Not differentiable."""
+    if _grads_wanted(query, key, value, log_decay, beta, state):
+        raise ValueError("gated_delta_step updates its states in place and has no gradient: use gated_delta_rule")
+    return capi.gdr_step(query, key, value, log_decay, beta, state, slots, scale=scale)
+
+
+class QkNormRotateFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, query, key, query_weight, key_weight, cos, sin, positions, kind, eps, interleaved):
+        ctx.how = {"kind": kind, "eps": eps, "interleaved": interleaved}
+        ctx.save_for_backward(query, key, query_weight, key_weight, cos, sin, positions)
+        return capi.qkn_fwd(query, key, query_weight, key_weight, cos, sin, positions, **ctx.how)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_query, d_key):
+        saved = ctx.saved_tensors
+        want = ctx.needs_input_grad[:4]
+        grads = capi.qkn_bwd(*saved, d_query.contiguous(), d_key.contiguous(), want=want, **ctx.how)
+        return (*grads, None, None, None, None, None, None)
+
+
+def _last_dense(t):
+    return t if t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+def qk_norm_rotate(query, key, query_weight=None, key_weight=None, cos=None, sin=None, positions=None, *, kind: str = "rms",
+                   eps: float = 1e-6, interleaved: bool = False):
+    """(query, key) with every head normed, weighted and turned by its token's
+    position in one pass, differentiable in the first four.
+
+    query [B, T, Hq, D], key [B, T, Hk, D]: float32, bfloat16 or float16, any
+    strides (views of a fused projection are read in place); weights [D] of the
+    same dtype or None.  kind "rms": x / sqrt(mean x^2 + eps); "l2":
+    x / sqrt(sum x^2 + eps), unit heads as the gated delta rule wants its keys.
+    cos, sin [P, R / 2] float32 turn the first R elements (None: no rotation):
+    pairs (i, i + R / 2), or (2i, 2i + 1) with ``interleaved``.  Token (b, t)
+    takes table row positions[b, t] (int32 or int64), or row t without
+    positions; a position outside the table makes its heads NaN.  Gradients of
+    cos and sin are refused."""
+    if _grads_wanted(cos, sin):
+        raise ValueError("qk_norm_rotate has no gradient of cos and sin: detach them")
+    query, key = _last_dense(query), _last_dense(key)
+    if _grads_wanted(query, key, query_weight, key_weight):
+        return QkNormRotateFunction.apply(query, key, query_weight, key_weight, cos, sin, positions, kind, eps, interleaved)
+    return capi.qkn_fwd(query, key, query_weight, key_weight, cos, sin, positions, kind=kind, eps=eps, interleaved=interleaved)

@@ -47,6 +47,8 @@ EXPORTS = (
     # include/qc_bench.h
     "qc_stream_copy",
 )
+# Of the language-model operators: include/gated_delta.h and include/qk_norm.h.
+LM_EXPORTS = ("gdr_step", "qkn_fwd", "qkn_workspace_bytes", "qkn_bwd")
 
 
 class QcOptions(ctypes.Structure):
@@ -57,6 +59,19 @@ class QcOptions(ctypes.Structure):
 class QcScanPlan(ctypes.Structure):
     _fields_ = [("n_actions", ctypes.c_int64), ("bwd_start", ctypes.c_int64),
                 ("forward_steps", ctypes.c_int64), ("prefix_steps", ctypes.c_int64)]
+
+
+class GdrDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "Hk", "Hv", "K", "V", "N")] + [
+        ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class QknDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "Hq", "Hk", "D", "R", "P")] + [
+        ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
+        ("dtype", ctypes.c_int32), ("kind", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("positions64", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 class QuatCumprodError(RuntimeError):
@@ -137,6 +152,15 @@ def load(path: str | None = None):
         lib.gdn2_bwd.restype = ctypes.c_int
         lib.qc_stream_copy.argtypes = [vp, vp, sz, i32, vp]
         lib.qc_stream_copy.restype = ctypes.c_int
+        gdr, qkn = ctypes.POINTER(GdrDims), ctypes.POINTER(QknDims)
+        lib.gdr_step.argtypes = [gdr] + [vp] * 6 + [i64, i64] + [vp] * 3
+        lib.gdr_step.restype = ctypes.c_int
+        lib.qkn_fwd.argtypes = [qkn] + [vp] * 10
+        lib.qkn_fwd.restype = ctypes.c_int
+        lib.qkn_workspace_bytes.argtypes = [qkn]
+        lib.qkn_workspace_bytes.restype = sz
+        lib.qkn_bwd.argtypes = [qkn] + [vp] * 14 + [sz, vp]
+        lib.qkn_bwd.restype = ctypes.c_int
         if path is None:
             _lib = lib
         return lib
@@ -683,3 +707,231 @@ def gdn2_bwd(query, key, value, erase, write, log_decay, boundary, d_context, d_
                       _stream(stream))
     _check(rc, "gdn2_bwd")
     return tuple(outs[n] for n in GDN2_INPUTS)
+
+
+# ---------------------------------------------------------------------------
+# Language-model operators: the gated delta rule (include/gated_delta.h) and
+# the norms of query and key heads with the position rotation
+# (include/qk_norm.h).  query, key [B, T, Hk, K] and value [B, T, Hv, V] are
+# read through their strides (last axis dense), in float32, bfloat16 or
+# float16; gates and states are float32.
+
+_LM_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+# Checked shapes and strides, with the sizes structure the library takes: a
+# decoding loop makes the same call for every token.
+_lm_plans: dict = {}
+_LM_PLANS_KEPT = 512
+
+
+def _lm_plan(key, make):
+    plan = _lm_plans.get(key)
+    if plan is None:
+        plan = make()
+        if len(_lm_plans) >= _LM_PLANS_KEPT:
+            _lm_plans.clear()
+        _lm_plans[key] = plan
+    return plan
+
+
+def _lm_elsewhere(device, stream):
+    """Whether a call on ``device`` needs another current device or stream."""
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+def _lm_there(device, stream, call, *args, **kw):
+    """``call`` with ``device`` and ``stream`` current, so that what it allocates belongs to that stream."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+
+
+def _lm_heads(name, t, like=None):
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [batch, tokens, heads, elements], got {tuple(t.shape)}")
+    if t.dtype not in _LM_DTYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name} must be dense along its last axis")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU: there is no CPU path")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise TypeError(f"{name} must have dtype {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+
+
+def _lm_dense(name, t, shape, dtype, device):
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _gdr_dims(query, key, value, n, scale):
+    _lm_heads("query", query)
+    _lm_heads("key", key, query)
+    _lm_heads("value", value, query)
+    B, T, Hk, K = query.shape
+    if key.shape != query.shape:
+        raise ValueError(f"key must have query's shape {tuple(query.shape)}, got {tuple(key.shape)}")
+    if value.shape[0] != B or value.shape[1] != T:
+        raise ValueError(f"value must share query's batch and tokens {(B, T)}, got {tuple(value.shape)}")
+    Hv, V = value.shape[2], value.shape[3]
+    if Hk < 1 or Hv < 1 or Hv % Hk:
+        raise ValueError(f"value's heads ({Hv}) must be a multiple of query's and key's ({Hk})")
+    if not 1 <= K <= 128 or not 1 <= V <= 1024:
+        raise ValueError(f"head sizes must be 1..128 for query and key and 1..1024 for value, got {K} and {V}")
+    d = GdrDims(B, T, Hk, Hv, K, V, B if n is None else n)
+    for st, t in ((d.q_stride, query), (d.k_stride, key), (d.v_stride, value)):
+        st[:] = t.stride()[:3]
+    d.dtype = _LM_DTYPES[query.dtype]
+    d.scale = K ** -0.5 if scale is None else scale
+    return d
+
+
+def _gdr_plan(query, key, value, n, scale):
+    return _lm_plan((0, query.shape, key.shape, value.shape, query.stride(), key.stride(), value.stride(), query.dtype,
+                     key.dtype, value.dtype, query.device, key.device, value.device, n, scale),
+                    lambda: _gdr_dims(query, key, value, n, scale))
+
+
+def gdr_step(query, key, value, log_decay, beta, state, slots=None, *, scale=None, out=None, stream=None):
+    """One or a few tokens of the gated delta rule for each batch row, on a
+    pool of states [slots, Hv, K, V] float32 that is updated in place; returns
+    out [B, T, Hv, V].  Row n uses state slots[n] (int32), or state n without
+    ``slots``.  A row whose slot is outside the pool, or named by an earlier
+    row, is not run: zeros in out, no state touched.  The pool's slots may lie
+    apart (a view of a larger pool); each must be dense.  scale defaults to
+    K ** -0.5."""
+    device = query.device
+    if query.is_cuda and _lm_elsewhere(device, stream):
+        return _lm_there(device, stream, gdr_step, query, key, value, log_decay, beta, state, slots, scale=scale, out=out)
+    d = _gdr_plan(query, key, value, None, scale)
+    gates = (d.B, d.T, d.Hv)
+    _lm_dense("log_decay", log_decay, gates, torch.float32, device)
+    _lm_dense("beta", beta, gates, torch.float32, device)
+    if (state.dim() != 4 or state.shape[1:] != (d.Hv, d.K, d.V) or state.dtype != torch.float32 or state.device != device
+            or not (state.is_contiguous() or (state.shape[0] > 0 and state[0].is_contiguous()))):
+        raise ValueError(f"state must be float32 [slots, {d.Hv}, {d.K}, {d.V}] on {device} with dense slots, "
+                         f"got {state.dtype} {tuple(state.shape)} on {state.device}")
+    if slots is not None:
+        _lm_dense("slots", slots, (d.B,), torch.int32, device)
+    elif state.shape[0] < d.B:
+        raise ValueError(f"state must have a slot for each of {d.B} rows, got {state.shape[0]}")
+    shape = (d.B, d.T, d.Hv, d.V)
+    if out is None:
+        out = torch.empty(shape, dtype=query.dtype, device=device)
+    else:
+        _lm_dense("out", out, shape, query.dtype, device)
+    rc = load().gdr_step(d, query.data_ptr(), key.data_ptr(), value.data_ptr(), log_decay.data_ptr(), beta.data_ptr(),
+                         state.data_ptr(), state.shape[0], state.stride(0) if state.shape[0] > 1 else d.Hv * d.K * d.V,
+                         None if slots is None else slots.data_ptr(), out.data_ptr(),
+                         torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, "gdr_step")
+    return out
+
+
+QKN_KINDS = {"rms": 0, "l2": 1}
+
+
+def _qkn_dims(query, key, cos, positions, kind, eps, interleaved):
+    _lm_heads("query", query)
+    _lm_heads("key", key, query)
+    B, T, Hq, D = query.shape
+    if key.shape[0] != B or key.shape[1] != T or key.shape[3] != D:
+        raise ValueError(f"key must be [{B}, {T}, heads, {D}] as query, got {tuple(key.shape)}")
+    if not 1 <= D <= 1024:
+        raise ValueError(f"head size must be 1..1024, got {D}")
+    if kind not in QKN_KINDS:
+        raise ValueError(f"kind must be one of {tuple(QKN_KINDS)}, got {kind!r}")
+    if not eps >= 0:
+        raise ValueError(f"eps must be >= 0, got {eps}")
+    d = QknDims(B, T, Hq, key.shape[2], D)
+    for st, t in ((d.q_stride, query), (d.k_stride, key)):
+        st[:] = t.stride()[:3]
+    if cos is not None:
+        if cos.dim() != 2 or 2 * cos.shape[1] > D:
+            raise ValueError(f"cos and sin must be [positions, R / 2] with R <= {D}, got {tuple(cos.shape)}")
+        d.P, d.R = cos.shape[0], 2 * cos.shape[1]
+        if positions is None and d.P < T:
+            raise ValueError(f"cos and sin need a row for each of {T} tokens where no positions are given, got {d.P}")
+        if d.P < 1 and d.R and B * T:
+            raise ValueError("cos and sin must have a row")
+    d.dtype, d.kind, d.interleaved = _LM_DTYPES[query.dtype], QKN_KINDS[kind], int(interleaved)
+    d.positions64 = int(positions is not None and positions.dtype == torch.int64)
+    d.eps = eps
+    return d
+
+
+def _qkn_plan(query, key, query_weight, key_weight, cos, sin, positions, kind, eps, interleaved):
+    device = query.device
+    d = _lm_plan((1, query.shape, key.shape, query.stride(), key.stride(), query.dtype, key.dtype, device, key.device,
+                  None if cos is None else cos.shape, None if positions is None else positions.dtype, kind, eps,
+                  bool(interleaved)),
+                 lambda: _qkn_dims(query, key, cos, positions, kind, eps, interleaved))
+    for name, w in (("query_weight", query_weight), ("key_weight", key_weight)):
+        if w is not None:
+            _lm_dense(name, w, (d.D,), query.dtype, device)
+    if (cos is None) != (sin is None) or (cos is None and positions is not None):
+        raise ValueError("cos and sin must be given together, and positions only with them")
+    if cos is not None:
+        _lm_dense("cos", cos, (d.P, d.R // 2), torch.float32, device)
+        _lm_dense("sin", sin, (d.P, d.R // 2), torch.float32, device)
+    if positions is not None:
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+        _lm_dense("positions", positions, (d.B, d.T), positions.dtype, device)
+    return d
+
+
+def _data_ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def qkn_fwd(query, key, query_weight=None, key_weight=None, cos=None, sin=None, positions=None, *, kind="rms", eps=1e-6,
+            interleaved=False, query_out=None, key_out=None, stream=None):
+    """(query, key) with every head normed, weighted and turned; see
+    include/qk_norm.h.  Outputs are contiguous."""
+    device = query.device
+    if query.is_cuda and _lm_elsewhere(device, stream):
+        return _lm_there(device, stream, qkn_fwd, query, key, query_weight, key_weight, cos, sin, positions, kind=kind,
+                         eps=eps, interleaved=interleaved, query_out=query_out, key_out=key_out)
+    d = _qkn_plan(query, key, query_weight, key_weight, cos, sin, positions, kind, eps, interleaved)
+    if query_out is None:
+        query_out = torch.empty(query.shape, dtype=query.dtype, device=device)
+    else:
+        _lm_dense("query_out", query_out, query.shape, query.dtype, device)
+    if key_out is None:
+        key_out = torch.empty(key.shape, dtype=key.dtype, device=device)
+    else:
+        _lm_dense("key_out", key_out, key.shape, key.dtype, device)
+    rc = load().qkn_fwd(d, query.data_ptr(), key.data_ptr(), _data_ptr(query_weight), _data_ptr(key_weight), _data_ptr(cos),
+                        _data_ptr(sin), _data_ptr(positions), query_out.data_ptr(), key_out.data_ptr(),
+                        torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, "qkn_fwd")
+    return query_out, key_out
+
+
+def qkn_bwd(query, key, query_weight, key_weight, cos, sin, positions, d_query_out, d_key_out, *, kind="rms", eps=1e-6,
+            interleaved=False, want=(True, True, True, True), stream=None):
+    """Gradients (query, key, query_weight, key_weight) of qkn_fwd; those not
+    wanted, and those of absent weights, are None."""
+    device = query.device
+    if query.is_cuda and _lm_elsewhere(device, stream):
+        return _lm_there(device, stream, qkn_bwd, query, key, query_weight, key_weight, cos, sin, positions, d_query_out,
+                         d_key_out, kind=kind, eps=eps, interleaved=interleaved, want=want)
+    d = _qkn_plan(query, key, query_weight, key_weight, cos, sin, positions, kind, eps, interleaved)
+    _lm_dense("d_query_out", d_query_out, query.shape, query.dtype, device)
+    _lm_dense("d_key_out", d_key_out, key.shape, key.dtype, device)
+    like = (query, key, query_weight, key_weight)
+    grads = [torch.empty(t.shape, dtype=t.dtype, device=device) if t is not None and w else None for t, w in zip(like, want)]
+    ws, nbytes = None, 0
+    if grads[2] is not None or grads[3] is not None:
+        nbytes = int(load().qkn_workspace_bytes(d))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    rc = load().qkn_bwd(d, query.data_ptr(), key.data_ptr(), _data_ptr(query_weight), _data_ptr(key_weight), _data_ptr(cos),
+                        _data_ptr(sin), _data_ptr(positions), d_query_out.data_ptr(), d_key_out.data_ptr(),
+                        *[_data_ptr(g) for g in grads], _data_ptr(ws), nbytes, torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, "qkn_bwd")
+    return tuple(grads)

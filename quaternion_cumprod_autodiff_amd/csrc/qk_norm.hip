@@ -1,0 +1,504 @@
+// qk_norm.hip -- norms of query and key heads with the position rotation in
+// the same pass, and their VJP (include/qk_norm.h).
+//
+// Forward, per head x [D] with r = 1 / sqrt(sum x^2 / size + eps) (size D or
+// 1): n = x r w, y = turn(n).  VJP, with the cotangent g of y:
+//     dn = turn^-1(g),   dh = dn w,   c = sum dh x
+//     dx = r dh - x r^3 c / size,     dw = sum over tokens and heads of dn x r
+// The statistics, the products and the weights' sums are float32.
+//
+// Bound by memory: every element is read once (twice as x and g in the VJP)
+// and written once, so a group of lanes holds a head in registers between the
+// sum and the product.  A lane holds W pairs of elements, chosen so that a
+// pair that turns together is in one lane: with 16-byte rows (D, R / 2
+// multiples of 8 and every row on 16 bytes) W = 8, else W = 1.
+#include "lm_common.hpp"
+#include "qc_internal.hpp"
+#include "qk_norm.h"
+#include "quat_cumprod.h"
+
+#include <type_traits>
+
+namespace qc {
+namespace {
+
+constexpr int kThreads = 256;
+// Blocks that share a weight gradient's sum: enough to fill 256 CUs several
+// times, few enough that the second pass over their partial sums is short.
+constexpr int kMaxPartials = 1024;
+
+struct QknArgs {
+    const void *q, *k, *wq, *wk;
+    const float *cos, *sin;
+    const void* pos;
+    void *yq, *yk;                 // forward: outputs; VJP: dx (may be null)
+    const void *gq, *gk;           // VJP: cotangents
+    float *pq, *pk;                // VJP: partial sums [blocks][D] (null: no gradient of that weight)
+    int64_t qs[3], ks[3];
+    int64_t T, rows_q, rows_k, D, R, P;
+    int hq, hk, blocks_q, blocks_k;
+    int pos64, interleaved;
+    float eps, inv_size;
+};
+
+// Elements of the pair slot p (W pairs) of a head: those that turn, (first,
+// first + step * i) and (second, ...), then the others in two runs.
+template <int W>
+struct Slot {
+    int64_t a, b;
+    bool turns, has_a, has_b;
+};
+
+template <int W>
+__device__ __forceinline__ Slot<W> slot_of(int p, int D, int R, bool interleaved) {
+    const int turning = R / (2 * W);
+    Slot<W> s;
+    s.turns = p < turning;
+    if (s.turns) {
+        s.a = interleaved ? 2 * p * W : p * W;
+        s.b = interleaved ? (2 * p + 1) * W : R / 2 + p * W;
+    } else {
+        s.a = R + 2 * (p - turning) * W;
+        s.b = s.a + W;
+    }
+    s.has_a = s.a < D;
+    s.has_b = s.b < D;
+    return s;
+}
+
+template <int W, class E>
+__device__ __forceinline__ void load_pair(const E* row, const Slot<W>& s, float (&a)[W], float (&b)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) a[i] = b[i] = 0.f;
+    if (s.has_a) load_floats<W>(row + s.a, a);
+    if (s.has_b) load_floats<W>(row + s.b, b);
+}
+
+// (a, b) as pairs that turn together: as loaded for halves, unzipped for
+// neighbours (a then b hold 2W consecutive elements).
+template <int W>
+__device__ __forceinline__ void turn(float (&a)[W], float (&b)[W], const float* c, const float* s, bool interleaved, float sign) {
+    if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            float& x = 2 * i < W ? a[2 * i % W] : b[(2 * i) % W];
+            float& y = 2 * i + 1 < W ? a[(2 * i + 1) % W] : b[(2 * i + 1) % W];
+            const float u = x * c[i] - sign * (y * s[i]);
+            y = y * c[i] + sign * (x * s[i]);
+            x = u;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const float u = a[i] * c[i] - sign * (b[i] * s[i]);
+            b[i] = b[i] * c[i] + sign * (a[i] * s[i]);
+            a[i] = u;
+        }
+    }
+}
+
+template <int G>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+    for (int m = 1; m < G; m *= 2) x += __shfl_xor(x, m, 64);
+    return x;
+}
+
+__device__ __forceinline__ int64_t table_row(const QknArgs& a, int64_t token) {
+    if (!a.pos) return token % a.T;
+    const int64_t p = a.pos64 ? static_cast<const int64_t*>(a.pos)[token] : int64_t(static_cast<const int32_t*>(a.pos)[token]);
+    return p;
+}
+
+struct Row {
+    int64_t offset, token;
+};
+
+__device__ __forceinline__ Row row_of(int64_t i, int heads, const int64_t (&st)[3], int64_t T) {
+    const int64_t token = i / heads;
+    const int64_t h = i - token * heads, b = token / T, t = token - b * T;
+    return {b * st[0] + t * st[1] + h * st[2], token};
+}
+
+// One head per group of G lanes; S slots of W pairs per lane.  DT: storage
+// type; BWD: the VJP.
+template <int DT, int W, int G, int S, bool BWD>
+__global__ void __launch_bounds__(kThreads) qkn_kernel(QknArgs a) {
+    using E = typename Storage<DT>::type;
+    const int lane = threadIdx.x % G, group = threadIdx.x / G;
+    const bool is_q = int(blockIdx.x) < a.blocks_q;
+    const int64_t rows = is_q ? a.rows_q : a.rows_k;
+    const int heads = is_q ? a.hq : a.hk;
+    const int block = is_q ? blockIdx.x : blockIdx.x - a.blocks_q, blocks = is_q ? a.blocks_q : a.blocks_k;
+    const E* x = static_cast<const E*>(is_q ? a.q : a.k);
+    const E* wt = static_cast<const E*>(is_q ? a.wq : a.wk);
+    E* y = static_cast<E*>(is_q ? a.yq : a.yk);
+    const E* g = static_cast<const E*>(is_q ? a.gq : a.gk);
+    float* part = is_q ? a.pq : a.pk;
+    const int D = int(a.D), R = int(a.R);
+    const bool inter = a.interleaved != 0;
+    Slot<W> slot[S];
+    float wa[S][W], wb[S][W], sa[S][W], sb[S][W];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        slot[s] = slot_of<W>(lane + G * s, D, R, inter);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            wa[s][i] = wb[s][i] = 1.f;
+            sa[s][i] = sb[s][i] = 0.f;
+        }
+        if (wt) load_pair<W>(wt, slot[s], wa[s], wb[s]);
+    }
+    constexpr int kGroups = kThreads / G;
+    for (int64_t i = int64_t(block) * kGroups + group; i < rows; i += int64_t(blocks) * kGroups) {
+        const Row at = is_q ? row_of(i, heads, a.qs, a.T) : row_of(i, heads, a.ks, a.T);
+        float xa[S][W], xb[S][W], ga[S][W], gb[S][W];
+        float sum = 0.f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            load_pair<W>(x + at.offset, slot[s], xa[s], xb[s]);
+            if constexpr (BWD) load_pair<W>(g + i * D, slot[s], ga[s], gb[s]);
+        }
+        int64_t row = 0;
+        float poison = 0.f;
+        if (R) {
+            row = table_row(a, at.token);
+            if (row < 0 || row >= a.P) {
+                row = 0;
+                poison = __builtin_nanf("");
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int j = 0; j < W; ++j) sum += xa[s][j] * xa[s][j] + xb[s][j] * xb[s][j];
+        sum = group_sum<G>(sum);
+        const float r = 1.f / sqrtf(sum * a.inv_size + a.eps) + poison;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            float c[W], sn[W];
+            if (slot[s].turns) {
+                const int64_t t = row * (R / 2) + int64_t(lane + G * s) * W;
+                load_floats<W>(a.cos + t, c);
+                load_floats<W>(a.sin + t, sn);
+            }
+            if constexpr (!BWD) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    xa[s][j] = xa[s][j] * r * wa[s][j];
+                    xb[s][j] = xb[s][j] * r * wb[s][j];
+                }
+                if (slot[s].turns) turn<W>(xa[s], xb[s], c, sn, inter, 1.f);
+                if (slot[s].has_a) store_floats<W>(y + i * D + slot[s].a, xa[s]);
+                if (slot[s].has_b) store_floats<W>(y + i * D + slot[s].b, xb[s]);
+            } else if (slot[s].turns) {
+                turn<W>(ga[s], gb[s], c, sn, inter, -1.f);
+            }
+        }
+        if constexpr (BWD) {
+            float dot = 0.f;
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    sa[s][j] += ga[s][j] * (xa[s][j] * r);
+                    sb[s][j] += gb[s][j] * (xb[s][j] * r);
+                    ga[s][j] *= wa[s][j];
+                    gb[s][j] *= wb[s][j];
+                    dot += ga[s][j] * xa[s][j] + gb[s][j] * xb[s][j];
+                }
+            dot = group_sum<G>(dot);
+            const float f = r * r * r * dot * a.inv_size;
+            if (y) {
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        xa[s][j] = r * ga[s][j] - xa[s][j] * f;
+                        xb[s][j] = r * gb[s][j] - xb[s][j] * f;
+                    }
+                    if (slot[s].has_a) store_floats<W>(y + i * D + slot[s].a, xa[s]);
+                    if (slot[s].has_b) store_floats<W>(y + i * D + slot[s].b, xb[s]);
+                }
+            }
+        }
+    }
+    if constexpr (BWD) {
+        if (!part) return;
+        // The block's sum in a fixed order: groups of a wave by shuffles, waves through LDS.
+        __shared__ float red[kThreads / 64][G * S * W * 2];
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+#pragma unroll
+                for (int m = G; m < 64; m *= 2) {
+                    sa[s][j] += __shfl_xor(sa[s][j], m, 64);
+                    sb[s][j] += __shfl_xor(sb[s][j], m, 64);
+                }
+            }
+        const int wave = threadIdx.x / 64;
+        if (threadIdx.x % 64 < G) {
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    red[wave][(s * W + j) * 2 * G + lane] = sa[s][j];
+                    red[wave][((s * W + j) * 2 + 1) * G + lane] = sb[s][j];
+                }
+        }
+        __syncthreads();
+        if (threadIdx.x < G) {
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    float ta = 0.f, tb = 0.f;
+                    for (int w = 0; w < kThreads / 64; ++w) {
+                        ta += red[w][(s * W + j) * 2 * G + lane];
+                        tb += red[w][((s * W + j) * 2 + 1) * G + lane];
+                    }
+                    if (slot[s].has_a) part[int64_t(block) * D + slot[s].a + j] = ta;
+                    if (slot[s].has_b) part[int64_t(block) * D + slot[s].b + j] = tb;
+                }
+        }
+    }
+}
+
+// dw[d] = sum of the blocks' partial sums, 16 columns and 16 runs of blocks to
+// a block of threads, the runs joined in order.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) qkn_weight_kernel(const float* pq, const float* pk, int nq, int nk, void* dq, void* dk, int D) {
+    using E = typename Storage<DT>::type;
+    const float* part = blockIdx.y ? pk : pq;
+    const int n = blockIdx.y ? nk : nq;
+    E* out = static_cast<E*>(blockIdx.y ? dk : dq);
+    if (!out) return;
+    const int col = blockIdx.x * 16 + threadIdx.x % 16, run = threadIdx.x / 16;
+    __shared__ float red[16][17];
+    float s = 0.f;
+    if (col < D)
+        for (int i = run; i < n; i += 16) s += part[int64_t(i) * D + col];
+    red[run][threadIdx.x % 16] = s;
+    __syncthreads();
+    if (threadIdx.x < 16 && col < D) {
+        float t = 0.f;
+        for (int i = 0; i < 16; ++i) t += red[i][threadIdx.x];
+        out[col] = E(t);
+    }
+}
+
+int pow2_at_least(int64_t n) {
+    int p = 1;
+    while (p < n) p *= 2;
+    return p;
+}
+
+struct Shape {
+    bool wide;          // W = 8
+    int g, s;           // lanes per head, slots per lane
+};
+
+Shape shape_of(const qkn_dims& d, bool wide) {
+    Shape sh;
+    sh.wide = wide;
+    const int64_t slots = (d.D + (wide ? 15 : 1)) / (wide ? 16 : 2);
+    sh.g = wide ? pow2_at_least(slots) : 64;
+    if (wide && sh.g < 4) sh.g = 4;
+    sh.s = wide ? 1 : pow2_at_least((slots + 63) / 64);
+    return sh;
+}
+
+// Blocks for so many heads; past 2^20 blocks the blocks loop.
+int64_t blocks_for(int64_t rows, int g) {
+    const int64_t n = (rows * g + kThreads - 1) / kThreads;
+    return n < (int64_t(1) << 20) ? n : int64_t(1) << 20;
+}
+
+template <class F>
+hipError_t by_dtype(int dt, F&& f) {
+    if (dt == 0) return f(std::integral_constant<int, 0>{});
+    if (dt == 1) return f(std::integral_constant<int, 1>{});
+    return f(std::integral_constant<int, 2>{});
+}
+
+template <bool BWD>
+hipError_t launch(int dt, Shape sh, const QknArgs& a, hipStream_t st) {
+    return by_dtype(dt, [&](auto t) {
+        constexpr int DT = decltype(t)::value;
+        const void* fn;
+        if (sh.wide)
+            fn = sh.g == 4    ? reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 4, 1, BWD>)
+                 : sh.g == 8  ? reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 8, 1, BWD>)
+                 : sh.g == 16 ? reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 16, 1, BWD>)
+                 : sh.g == 32 ? reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 32, 1, BWD>)
+                              : reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 64, 1, BWD>);
+        else
+            fn = sh.s == 1   ? reinterpret_cast<const void*>(&qkn_kernel<DT, 1, 64, 1, BWD>)
+                 : sh.s == 2 ? reinterpret_cast<const void*>(&qkn_kernel<DT, 1, 64, 2, BWD>)
+                 : sh.s == 4 ? reinterpret_cast<const void*>(&qkn_kernel<DT, 1, 64, 4, BWD>)
+                             : reinterpret_cast<const void*>(&qkn_kernel<DT, 1, 64, 8, BWD>);
+        QknArgs args = a;
+        void* params[] = {&args};
+        return hipLaunchKernel(fn, dim3(unsigned(a.blocks_q + a.blocks_k)), dim3(kThreads), params, 0, st);
+    });
+}
+
+int check_dims(const qkn_dims* d) {
+    if (!d) return QC_ERR_NULL;
+    if (d->B < 0 || d->T < 0 || d->Hq < 0 || d->Hk < 0 || d->P < 0) return QC_ERR_SHAPE;
+    if (d->D < 1 || d->D > 1024 || d->R < 0 || d->R > d->D || d->R % 2) return QC_ERR_SHAPE;
+    const int64_t tokens = count(d->B, d->T);
+    if (tokens < 0 || count(tokens, count(d->Hq, d->D)) < 0 || count(tokens, count(d->Hk, d->D)) < 0) return QC_ERR_SHAPE;
+    if (d->Hq > (1 << 20) || d->Hk > (1 << 20) || count(d->P, d->R) < 0) return QC_ERR_SHAPE;
+    if (d->dtype < 0 || d->dtype > 2) return QC_ERR_DTYPE;
+    if (d->kind < 0 || d->kind > 1 || !(d->eps >= 0.f)) return QC_ERR_OPTION;
+    return QC_OK;
+}
+
+struct Common {
+    int rc;
+    QknArgs a;
+    Shape sh;
+    int64_t q_bytes, k_bytes, q_out, k_out;
+};
+
+Common common(const qkn_dims* d, const void* q, const void* k, const void* wq, const void* wk, const float* cos, const float* sin,
+              const void* pos) {
+    Common c{};
+    c.rc = check_dims(d);
+    if (c.rc != QC_OK) return c;
+    const size_t e = dtype_bytes(d->dtype);
+    const int64_t tokens = d->B * d->T;
+    c.q_out = tokens * d->Hq * d->D * e;
+    c.k_out = tokens * d->Hk * d->D * e;
+    c.q_bytes = strided_bytes(d->B, d->T, d->Hq, d->D, d->q_stride, e);
+    c.k_bytes = strided_bytes(d->B, d->T, d->Hk, d->D, d->k_stride, e);
+    if (c.q_bytes < 0 || c.k_bytes < 0) {
+        c.rc = QC_ERR_SHAPE;
+        return c;
+    }
+    if ((c.q_out && !q) || (c.k_out && !k) || (d->R && tokens && (!cos || !sin))) {
+        c.rc = QC_ERR_NULL;
+        return c;
+    }
+    if (d->R && tokens && (d->P < 1 || (!pos && d->P < d->T))) {
+        c.rc = QC_ERR_SHAPE;
+        return c;
+    }
+    for (const void* p : {q, k, wq, wk})
+        if (p && !aligned_to(p, e)) c.rc = QC_ERR_ALIGN;
+    for (const void* p : {static_cast<const void*>(cos), static_cast<const void*>(sin)})
+        if (p && !aligned_to(p, 4)) c.rc = QC_ERR_ALIGN;
+    if (pos && !aligned_to(pos, d->positions64 ? 8 : 4)) c.rc = QC_ERR_ALIGN;
+    if (c.rc != QC_OK) return c;
+    const bool wide = d->D % 8 == 0 && d->R % 16 == 0 && rows_on_16(q, d->q_stride, e) && rows_on_16(k, d->k_stride, e) &&
+                      (!wq || aligned_to(wq, 16)) && (!wk || aligned_to(wk, 16)) &&
+                      (!d->R || (aligned_to(cos, 16) && aligned_to(sin, 16)));
+    c.sh = shape_of(*d, wide);
+    QknArgs& a = c.a;
+    a.q = q; a.k = k; a.wq = wq; a.wk = wk; a.cos = cos; a.sin = sin; a.pos = pos;
+    for (int i = 0; i < 3; ++i) {
+        a.qs[i] = d->q_stride[i];
+        a.ks[i] = d->k_stride[i];
+    }
+    a.T = d->T; a.rows_q = tokens * d->Hq; a.rows_k = tokens * d->Hk; a.D = d->D; a.R = d->R; a.P = d->P;
+    a.hq = int(d->Hq); a.hk = int(d->Hk);
+    a.pos64 = d->positions64; a.interleaved = d->interleaved;
+    a.eps = d->eps;
+    a.inv_size = d->kind == QKN_RMS ? 1.f / float(d->D) : 1.f;
+    return c;
+}
+
+int64_t partials(int64_t rows) { return rows < kMaxPartials ? rows : kMaxPartials; }
+
+}  // namespace
+}  // namespace qc
+
+extern "C" {
+
+int qkn_fwd(const qkn_dims* dims, const void* query, const void* key, const void* query_weight, const void* key_weight,
+            const float* cos, const float* sin, const void* positions, void* query_out, void* key_out, void* stream) {
+    qc::Common c = qc::common(dims, query, key, query_weight, key_weight, cos, sin, positions);
+    if (c.rc != QC_OK) return c.rc;
+    if ((c.q_out && !query_out) || (c.k_out && !key_out)) return QC_ERR_NULL;
+    const size_t e = qc::dtype_bytes(dims->dtype), w = size_t(dims->D) * e, table = size_t(dims->P * (dims->R / 2)) * 4;
+    if ((query_out && !qc::aligned_to(query_out, c.sh.wide ? 16 : e)) || (key_out && !qc::aligned_to(key_out, c.sh.wide ? 16 : e))) {
+        if ((query_out && !qc::aligned_to(query_out, e)) || (key_out && !qc::aligned_to(key_out, e))) return QC_ERR_ALIGN;
+        c.sh = qc::shape_of(*dims, false);
+    }
+    const qc::ByteSpan sp[] = {{query_out, size_t(c.q_out)}, {key_out, size_t(c.k_out)}, {query, size_t(c.q_bytes)},
+                               {key, size_t(c.k_bytes)}, {query_weight, w}, {key_weight, w}, {cos, table}, {sin, table},
+                               {positions, size_t(dims->B * dims->T) * (dims->positions64 ? 8 : 4)}};
+    if (qc::outputs_overlap(sp, 2, 9)) return QC_ERR_ALIAS;
+    c.a.yq = query_out;
+    c.a.yk = key_out;
+    c.a.blocks_q = int(qc::blocks_for(c.a.rows_q, c.sh.g));
+    c.a.blocks_k = int(qc::blocks_for(c.a.rows_k, c.sh.g));
+    if (c.a.blocks_q + c.a.blocks_k == 0) return QC_OK;
+    const hipError_t err = qc::launch<false>(dims->dtype, c.sh, c.a, static_cast<hipStream_t>(stream));
+    return err == hipSuccess ? QC_OK : qc::record_hip_error(err);
+}
+
+size_t qkn_workspace_bytes(const qkn_dims* dims) {
+    if (qc::check_dims(dims) != QC_OK) return 0;
+    const int64_t tokens = dims->B * dims->T;
+    return size_t(qc::partials(tokens * dims->Hq) + qc::partials(tokens * dims->Hk)) * size_t(dims->D) * 4 + 16;
+}
+
+int qkn_bwd(const qkn_dims* dims, const void* query, const void* key, const void* query_weight, const void* key_weight,
+            const float* cos, const float* sin, const void* positions, const void* d_query_out, const void* d_key_out,
+            void* d_query, void* d_key, void* d_query_weight, void* d_key_weight, void* workspace,
+            size_t workspace_bytes, void* stream) {
+    qc::Common c = qc::common(dims, query, key, query_weight, key_weight, cos, sin, positions);
+    if (c.rc != QC_OK) return c.rc;
+    if (!d_query && !d_key && !d_query_weight && !d_key_weight) return QC_OK;
+    const bool any_q = d_query || d_query_weight, any_k = d_key || d_key_weight;
+    if ((c.q_out && any_q && !d_query_out) || (c.k_out && any_k && !d_key_out)) return QC_ERR_NULL;
+    if ((d_query_weight && !query_weight) || (d_key_weight && !key_weight)) return QC_ERR_NULL;
+    const size_t e = qc::dtype_bytes(dims->dtype), w = size_t(dims->D) * e, table = size_t(dims->P * (dims->R / 2)) * 4;
+    const size_t need = qkn_workspace_bytes(dims);
+    const bool weights = d_query_weight || d_key_weight;
+    if (weights && (!workspace || workspace_bytes < need)) return QC_ERR_WORKSPACE;
+    if (weights && !qc::aligned_to(workspace, 16)) return QC_ERR_ALIGN;
+    bool wide = c.sh.wide;
+    for (const void* p : {d_query_out, d_key_out, static_cast<const void*>(d_query), static_cast<const void*>(d_key)}) {
+        if (p && !qc::aligned_to(p, e)) return QC_ERR_ALIGN;
+        if (p && !qc::aligned_to(p, 16)) wide = false;
+    }
+    for (const void* p : {d_query_weight, d_key_weight})
+        if (p && !qc::aligned_to(p, e)) return QC_ERR_ALIGN;
+    c.sh = qc::shape_of(*dims, wide);
+    const qc::ByteSpan sp[] = {{d_query, size_t(c.q_out)}, {d_key, size_t(c.k_out)}, {d_query_weight, w}, {d_key_weight, w},
+                               {weights ? workspace : nullptr, need}, {query, size_t(c.q_bytes)}, {key, size_t(c.k_bytes)},
+                               {query_weight, w}, {key_weight, w}, {cos, table}, {sin, table},
+                               {positions, size_t(dims->B * dims->T) * (dims->positions64 ? 8 : 4)},
+                               {d_query_out, size_t(c.q_out)}, {d_key_out, size_t(c.k_out)}};
+    if (qc::outputs_overlap(sp, 5, 14)) return QC_ERR_ALIAS;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    auto blocks = [&](bool any, const void* dw, int64_t rows) -> int {
+        if (!any) return 0;
+        const int64_t n = qc::blocks_for(rows, c.sh.g), most = qc::partials(rows);
+        return int(dw && n > most ? most : n);
+    };
+    c.a.blocks_q = blocks(any_q, d_query_weight, c.a.rows_q);
+    c.a.blocks_k = blocks(any_k, d_key_weight, c.a.rows_k);
+    c.a.yq = d_query; c.a.yk = d_key; c.a.gq = d_query_out; c.a.gk = d_key_out;
+    c.a.pq = d_query_weight ? static_cast<float*>(workspace) : nullptr;
+    c.a.pk = d_key_weight ? static_cast<float*>(workspace) + (d_query_weight ? int64_t(c.a.blocks_q) * dims->D : 0) : nullptr;
+    hipError_t err = hipSuccess;
+    if (c.a.blocks_q + c.a.blocks_k) err = qc::launch<true>(dims->dtype, c.sh, c.a, st);
+    if (err == hipSuccess && weights) {
+        err = qc::by_dtype(dims->dtype, [&](auto t) {
+            const float *pq = c.a.pq, *pk = c.a.pk;
+            int nq = c.a.blocks_q, nk = c.a.blocks_k, D = int(dims->D);
+            void *dq = d_query_weight, *dk = d_key_weight;
+            void* params[] = {&pq, &pk, &nq, &nk, &dq, &dk, &D};
+            return hipLaunchKernel(reinterpret_cast<const void*>(&qc::qkn_weight_kernel<decltype(t)::value>),
+                                   dim3(unsigned((D + 15) / 16), 2), dim3(qc::kThreads), params, 0, st);
+        });
+    }
+    return err == hipSuccess ? QC_OK : qc::record_hip_error(err);
+}
+
+}  // extern "C"
