@@ -70,7 +70,28 @@ typedef struct {
     int64_t v_stride[3];
     int32_t dtype;
     float scale;
+    int32_t packed;            /* 1: offsets delimit the sequences, B is 1    */
+    int32_t reserved;
 } gdr_dims;
+
+/* Bytes of the state a forward saves for its backward, and of the workspace
+ * of a forward (backward 0) or a backward (1); 0 if out of range. */
+size_t gdr_saved_bytes(const gdr_dims* dims);
+size_t gdr_workspace_bytes(const gdr_dims* dims, int32_t backward);
+
+/* initial_state NULL: zeros.  final_state may be NULL, and saved if no
+ * backward follows. */
+int gdr_fwd(const gdr_dims* dims, const void* query, const void* key, const void* value, const float* log_decay,
+            const float* beta, const int32_t* offsets, const float* initial_state, void* out, float* final_state,
+            void* saved, void* workspace, size_t workspace_bytes, void* stream);
+
+/* VJP.  `saved` is what gdr_fwd wrote for the same inputs; d_out is dense
+ * [B, T, Hv, V], d_final_state may be NULL (zero).  Each of the six gradients,
+ * dense, may be NULL; if all are, the call does nothing. */
+int gdr_bwd(const gdr_dims* dims, const void* query, const void* key, const void* value, const float* log_decay,
+            const float* beta, const int32_t* offsets, const void* saved, const void* d_out, const float* d_final_state,
+            void* d_query, void* d_key, void* d_value, float* d_log_decay, float* d_beta, float* d_initial_state,
+            void* workspace, size_t workspace_bytes, void* stream);
 
 /* One or a few tokens (dims.T) for each of dims.N = dims.B rows, on states
  * that are updated in place: row n reads and writes state slots[n] of the pool

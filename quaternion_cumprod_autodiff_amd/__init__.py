@@ -14,7 +14,8 @@ def __getattr__(name):
         from . import capi
         return getattr(capi, name)
     if name in ("quat_cumprod", "quat_cumprod_with_final", "QuatCumprodFunction", "scan", "ScanFunction",
-                "gated_deltanet2", "GatedDeltaNet2Function", "gated_delta_step", "qk_norm_rotate",
+                "gated_deltanet2", "GatedDeltaNet2Function", "gated_delta_rule", "GatedDeltaRuleFunction",
+                "gated_delta_step", "qk_norm_rotate",
                 "QkNormRotateFunction"):
         from . import autograd
         return getattr(autograd, name)

@@ -231,6 +231,59 @@ def _grads_wanted(*tensors) -> bool:
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
+def _last_dense(t):
+    return t if t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+class GatedDeltaRuleFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, query, key, value, log_decay, beta, initial_state, scale, offsets):
+        out, state, saved = capi.gdr_fwd(query, key, value, log_decay, beta, initial_state, scale=scale, offsets=offsets,
+                                         want_saved=True)
+        ctx.scale = scale
+        ctx.save_for_backward(query, key, value, log_decay, beta, offsets, saved)
+        ctx.set_materialize_grads(False)
+        return out, state
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_out, d_state):
+        query, key, value, log_decay, beta, offsets, saved = ctx.saved_tensors
+        if d_out is None and d_state is None:
+            return (None,) * 8
+        d_out = torch.zeros(value.shape, dtype=value.dtype, device=value.device) if d_out is None else d_out.contiguous()
+        grads = capi.gdr_bwd(query, key, value, log_decay, beta, saved, d_out,
+                             None if d_state is None else d_state.contiguous(), scale=ctx.scale, offsets=offsets,
+                             want=ctx.needs_input_grad[:6])
+        return (*grads, None, None)
+
+
+def gated_delta_rule(query, key, value, log_decay, beta, initial_state=None, *, scale=None, offsets=None):
+    """(out [B, T, Hv, V], final states [N, Hv, K, V]) of the gated delta rule,
+    differentiable in its six tensors.  Per sequence and value head h, which
+    reads query and key head h // (Hv / Hk):
+
+        S = exp(log_decay_t) S;  u = beta_t (value_t - S^T key_t);  S = S + key_t u^T;  out_t = scale S^T query_t
+
+    query, key [B, T, Hk, K] and value [B, T, Hv, V]: float32, bfloat16 or
+    float16, any strides; log_decay (at most zero; -inf clears the state) and
+    beta [B, T, Hv], initial_state [N, Hv, K, V] (None: zeros) and the final
+    states float32; K <= 128, V <= 1024.  scale defaults to K ** -0.5.
+
+    Without ``offsets`` N = B.  With them (int32 [N + 1] on the GPU, ascending,
+    within 0 .. T), B is 1 and sequence n is rows offsets[n] .. offsets[n + 1]
+    - 1, of any length down to zero; rows of no sequence have zero out and zero
+    gradients.  A non-finite input spreads at most through its own sequence
+    from its chunk of 64 tokens on."""
+    query, key, value = _last_dense(query), _last_dense(key), _last_dense(value)
+    log_decay, beta = log_decay.contiguous(), beta.contiguous()
+    if initial_state is not None:
+        initial_state = initial_state.contiguous()
+    if _grads_wanted(query, key, value, log_decay, beta, initial_state):
+        return GatedDeltaRuleFunction.apply(query, key, value, log_decay, beta, initial_state, scale, offsets)
+    return capi.gdr_fwd(query, key, value, log_decay, beta, initial_state, scale=scale, offsets=offsets)[:2]
+
+
 def gated_delta_step(query, key, value, log_decay, beta, state, *, slots=None, scale=None):
     """One or a few new tokens of the gated delta rule (:func:`gated_delta_rule`)
     for each batch row, for decoding: query, key [B, T, Hk, K], value
@@ -258,10 +311,6 @@ class QkNormRotateFunction(torch.autograd.Function):
         want = ctx.needs_input_grad[:4]
         grads = capi.qkn_bwd(*saved, d_query.contiguous(), d_key.contiguous(), want=want, **ctx.how)
         return (*grads, None, None, None, None, None, None)
-
-
-def _last_dense(t):
-    return t if t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
 
 
 def qk_norm_rotate(query, key, query_weight=None, key_weight=None, cos=None, sin=None, positions=None, *, kind: str = "rms",

@@ -48,7 +48,7 @@ EXPORTS = (
     "qc_stream_copy",
 )
 # Of the language-model operators: include/gated_delta.h and include/qk_norm.h.
-LM_EXPORTS = ("gdr_step", "qkn_fwd", "qkn_workspace_bytes", "qkn_bwd")
+LM_EXPORTS = ("gdr_saved_bytes", "gdr_workspace_bytes", "gdr_fwd", "gdr_bwd", "gdr_step", "qkn_fwd", "qkn_workspace_bytes", "qkn_bwd")
 
 
 class QcOptions(ctypes.Structure):
@@ -64,7 +64,7 @@ class QcScanPlan(ctypes.Structure):
 class GdrDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "Hk", "Hv", "K", "V", "N")] + [
         ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
-        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("packed", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class QknDims(ctypes.Structure):
@@ -153,6 +153,14 @@ def load(path: str | None = None):
         lib.qc_stream_copy.argtypes = [vp, vp, sz, i32, vp]
         lib.qc_stream_copy.restype = ctypes.c_int
         gdr, qkn = ctypes.POINTER(GdrDims), ctypes.POINTER(QknDims)
+        lib.gdr_saved_bytes.argtypes = [gdr]
+        lib.gdr_saved_bytes.restype = sz
+        lib.gdr_workspace_bytes.argtypes = [gdr, i32]
+        lib.gdr_workspace_bytes.restype = sz
+        lib.gdr_fwd.argtypes = [gdr] + [vp] * 11 + [sz, vp]
+        lib.gdr_fwd.restype = ctypes.c_int
+        lib.gdr_bwd.argtypes = [gdr] + [vp] * 16 + [sz, vp]
+        lib.gdr_bwd.restype = ctypes.c_int
         lib.gdr_step.argtypes = [gdr] + [vp] * 6 + [i64, i64] + [vp] * 3
         lib.gdr_step.restype = ctypes.c_int
         lib.qkn_fwd.argtypes = [qkn] + [vp] * 10
@@ -787,6 +795,9 @@ def _gdr_dims(query, key, value, n, scale):
         st[:] = t.stride()[:3]
     d.dtype = _LM_DTYPES[query.dtype]
     d.scale = K ** -0.5 if scale is None else scale
+    d.packed = int(n is not None)
+    if d.packed and B != 1:
+        raise ValueError(f"packed sequences lie in a batch of one, got {B}")
     return d
 
 
@@ -794,6 +805,80 @@ def _gdr_plan(query, key, value, n, scale):
     return _lm_plan((0, query.shape, key.shape, value.shape, query.stride(), key.stride(), value.stride(), query.dtype,
                      key.dtype, value.dtype, query.device, key.device, value.device, n, scale),
                     lambda: _gdr_dims(query, key, value, n, scale))
+
+
+def _gdr_whole(query, key, value, log_decay, beta, offsets, scale):
+    """The plan of a whole-sequence call, its gates and offsets checked."""
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.numel() < 1:
+            raise ValueError(f"offsets must hold a number more than there are sequences, got {tuple(offsets.shape)}")
+        _lm_dense("offsets", offsets, (offsets.numel(),), torch.int32, query.device)
+    d = _gdr_plan(query, key, value, None if offsets is None else offsets.numel() - 1, scale)
+    _lm_dense("log_decay", log_decay, (d.B, d.T, d.Hv), torch.float32, query.device)
+    _lm_dense("beta", beta, (d.B, d.T, d.Hv), torch.float32, query.device)
+    return d
+
+
+def gdr_fwd(query, key, value, log_decay, beta, initial_state=None, *, scale=None, offsets=None, want_saved=False, out=None,
+            stream=None):
+    """(out, final states [N, Hv, K, V], saved state for gdr_bwd or None) of
+    the gated delta rule.  With ``offsets`` (int32 [N + 1]) B is 1 and the rows
+    are packed sequences; rows of none are left as they were in a given
+    ``out``, and zero in a new one."""
+    device = query.device
+    if query.is_cuda and _lm_elsewhere(device, stream):
+        return _lm_there(device, stream, gdr_fwd, query, key, value, log_decay, beta, initial_state, scale=scale,
+                         offsets=offsets, want_saved=want_saved, out=out)
+    d = _gdr_whole(query, key, value, log_decay, beta, offsets, scale)
+    states = (d.N, d.Hv, d.K, d.V)
+    if initial_state is not None:
+        _lm_dense("initial_state", initial_state, states, torch.float32, device)
+    lib = load()
+    ws_bytes = lib.gdr_workspace_bytes(d, 0)
+    if ws_bytes == 0:
+        raise QuatCumprodError(-2, "gdr_fwd")
+    shape = (d.B, d.T, d.Hv, d.V)
+    if out is None:
+        out = (torch.empty if offsets is None else torch.zeros)(shape, dtype=query.dtype, device=device)
+    else:
+        _lm_dense("out", out, shape, query.dtype, device)
+    fin = torch.empty(states, dtype=torch.float32, device=device)
+    saved = torch.empty(lib.gdr_saved_bytes(d), dtype=torch.uint8, device=device) if want_saved else None
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    rc = lib.gdr_fwd(d, query.data_ptr(), key.data_ptr(), value.data_ptr(), log_decay.data_ptr(), beta.data_ptr(),
+                     _data_ptr(offsets), _data_ptr(initial_state), out.data_ptr(), fin.data_ptr(), _data_ptr(saved),
+                     ws.data_ptr(), ws_bytes, torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, "gdr_fwd")
+    return out, fin, saved
+
+
+def gdr_bwd(query, key, value, log_decay, beta, saved, d_out, d_final_state=None, *, scale=None, offsets=None,
+            want=(True,) * 6, stream=None):
+    """Gradients (query, key, value, log_decay, beta, initial_state); those not
+    wanted are None.  ``saved`` is gdr_fwd's third output for the same inputs.
+    Rows of no sequence have zero gradients."""
+    device = query.device
+    if query.is_cuda and _lm_elsewhere(device, stream):
+        return _lm_there(device, stream, gdr_bwd, query, key, value, log_decay, beta, saved, d_out, d_final_state,
+                         scale=scale, offsets=offsets, want=want)
+    d = _gdr_whole(query, key, value, log_decay, beta, offsets, scale)
+    states = (d.N, d.Hv, d.K, d.V)
+    _lm_dense("d_out", d_out, (d.B, d.T, d.Hv, d.V), query.dtype, device)
+    if d_final_state is not None:
+        _lm_dense("d_final_state", d_final_state, states, torch.float32, device)
+    lib = load()
+    _lm_dense("saved", saved, (lib.gdr_saved_bytes(d),), torch.uint8, device)
+    new = torch.empty if offsets is None else torch.zeros
+    grads = [new(t.shape, dtype=t.dtype, device=device) if w else None
+             for t, w in zip((query, key, value, log_decay, beta), want)]
+    grads.append(torch.empty(states, dtype=torch.float32, device=device) if want[5] else None)
+    ws_bytes = lib.gdr_workspace_bytes(d, 1)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    rc = lib.gdr_bwd(d, query.data_ptr(), key.data_ptr(), value.data_ptr(), log_decay.data_ptr(), beta.data_ptr(),
+                     _data_ptr(offsets), saved.data_ptr(), d_out.data_ptr(), _data_ptr(d_final_state),
+                     *[_data_ptr(g) for g in grads], ws.data_ptr(), ws_bytes, torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, "gdr_bwd")
+    return tuple(grads)
 
 
 def gdr_step(query, key, value, log_decay, beta, state, slots=None, *, scale=None, out=None, stream=None):

@@ -1,0 +1,247 @@
+// gdr_chunk.hpp -- the chunked form of the gated delta rule
+// (include/gated_delta.h): its mathematics, its internal formats and the
+// device helpers that its kernels share.  Not installed.
+//
+// Chunks of C = 64 tokens.  With G_i the log decays cumulated from the chunk's
+// start, gamma_i = exp(G_i), Gam_ij = exp(G_i - G_j), S0 the state before the
+// chunk, and q, k, v, b the chunk's rows, the updates u_i = b_i (v_i - ...) of
+// the recurrence solve a unit lower triangular system, so that
+//     L_ij = Gam_ij k_i.k_j (i > j),   T = (I + diag(b) L)^-1,   P_ij = Gam_ij q_i.k_j (i >= j)
+//     U   = T diag(b) (V - gamma (K S0))                       the updates u, [C, V]
+//     out = scale (gamma (Q S0) + P U)
+//     S1  = gamma_last S0 + K^T (eta U),   eta_i = exp(G_last - G_i)
+// and, for cotangents dO of out (O = scale dO) and dS1 of S1,
+//     dU  = P^T O + eta (K dS1),   X = T^T dU,   dV = b X
+//     dS0 = gamma_last dS1 + Q^T (gamma O) - K^T (gamma b X)
+//     Phi_ij = Gam_ij O_i.U_j (i >= j),   Psi_ij = -b_i Gam_ij X_i.U_j (i > j)
+//     dQ  = gamma (O S0^T) + Phi K
+//     dKr = -gamma b (X S0^T) + Psi K         (k as the reader of the state)
+//     dKw = eta (U dS1^T) + Phi^T Q + Psi^T K   (k as its writer),   dK = dKr + dKw
+//     db_i = X_i.v_i - gamma_i k_i.(X S0^T)_i - sum_j (X_i.U_j) L_ij
+//     dG_i = q_i.dQ_i + k_i.dKr_i - k_i.dKw_i,   dG_last += gamma_last <S0, dS1> + sum_i eta_i k_i.(U dS1^T)_i
+//     dg_t = sum of dG_i over i >= t
+// All exponents are of differences that decays keep at or below zero.
+//
+// Kernels: gdr_factor (T, P and the operands' layouts, every chunk at once),
+// gdr_fwd and gdr_bwd_state (the states pass from chunk to chunk: one block per
+// 16 or 32 columns of V, everything else of a chunk in the same pass),
+// gdr_grad (the gradients of q, k, gates, every chunk at once).
+//
+// Arithmetic.  All products are v_mfma_f32_16x16x32_bf16 on operands split
+// into bfloat16 parts: bfloat16 inputs are one part, float16 two, float32 and
+// every computed operand three, all exact to 24 bits; of two operands' parts
+// i and j the products with i + j < 3 are summed, in float32.  So float32
+// accuracy costs 3 to 6 of these instructions, against 16 times one for the
+// float32 MFMA.
+//
+// Layouts.  A lane l = 16 g + m holds of an operand fragment (64 lanes x 8
+// bfloat16, 1 KiB, stored lane by lane): row m (A) or column m (B), and the 8
+// consecutive indices 32 b + 8 g + .. of the contracted axis' block b.  A
+// product's accumulators hold column m and rows 4 g + 0..3.  Rows of tile r of
+// an axis stand for the indices 32 (r / 2) + 8 (m / 4) + 4 (r % 2) + m % 4 of
+// it, so that the accumulators of tiles 2b and 2b + 1 are, in place, the 8
+// consecutive indices of a B fragment's block b: results become operands
+// without a transpose.
+#pragma once
+
+#include "gdr_internal.hpp"
+
+#include <type_traits>
+
+namespace qc {
+
+constexpr int kChunk = 64;
+constexpr int kParts = 3;
+
+constexpr int parts_of(int dt) { return dt == 0 ? 3 : dt == 1 ? 1 : 2; }
+
+// Fragments of one operand set of a chunk: 4 row tiles x KB blocks of K (or
+// 2 KB tiles of K x 2 blocks of tokens) x parts.
+constexpr int64_t kFrag = 512;                                        // bfloat16 of a fragment
+constexpr int64_t set_frags(int kb, int npi) { return int64_t(4) * kb * npi; }
+// Per chunk and key head: three sets (forward K rows, Q rows, K transposed;
+// backward K rows, Q transposed, K transposed).
+constexpr int64_t krec_bytes(int kb, int npi) { return 3 * set_frags(kb, npi) * kFrag * 2; }
+// Per chunk and value head: T and P (backward: transposed), 6 fragments of
+// non-zero 16 x 32 blocks x 3 parts each; gates.
+constexpr int64_t kTriFrags = 6 * kParts;
+struct Gates {
+    float gamma[kChunk], eta[kChunk], beta[kChunk];
+    double cum[kChunk];
+};
+constexpr int64_t kGateOffset = 2 * kTriFrags * kFrag * 2;
+constexpr int64_t kHrecBytes = (kGateOffset + int64_t(sizeof(Gates)) + 255) / 256 * 256;
+
+struct GdrArgs {
+    const void *q, *k, *v;
+    const float *g, *b, *s0;
+    const int32_t* offsets;
+    void* out;
+    float* fin;
+    char *krec, *hrec;                 // workspace: [slots][Hk] and [slots][Hv] records
+    float *save_s, *save_u;            // saved: [slots][Hv][KP][VP] and [slots][Hv][64][VP] (or null)
+    const void* d_out;
+    const float* d_fin;
+    void *dq, *dk, *dv;
+    float *dg, *db, *ds0;
+    float *x, *ds;                     // workspace: [slots][Hv][64][VP] and [slots][Hv][KP][VP]
+    int64_t qs[3], ks[3], vs[3];
+    int64_t T, slots, N, chunks;       // chunks: per sequence, without offsets
+    int Hk, Hv, group, K, V, VP;
+    int vec_qk, vec_v;                 // query and key rows, value and out rows: on 16 bytes, sizes multiples of 8
+    float scale;
+};
+
+hipError_t launch_gdr_factor(int dt, int kb, bool bwd, const GdrArgs& a, hipStream_t st);
+hipError_t launch_gdr_fwd(int dt, int kb, bool save, const GdrArgs& a, hipStream_t st);
+hipError_t launch_gdr_bwd_state(int dt, int kb, const GdrArgs& a, hipStream_t st);
+hipError_t launch_gdr_grad(int dt, int kb, const GdrArgs& a, hipStream_t st);
+
+// Calls f(dtype, blocks of K) with both as constants.
+template <class F>
+hipError_t by_dtype_kb(int dt, int kb, F&& f) {
+    auto with = [&](auto d) {
+        if (kb == 1) return f(d, std::integral_constant<int, 1>{});
+        if (kb == 2) return f(d, std::integral_constant<int, 2>{});
+        return f(d, std::integral_constant<int, 4>{});
+    };
+    if (dt == 0) return with(std::integral_constant<int, 0>{});
+    if (dt == 1) return with(std::integral_constant<int, 1>{});
+    return with(std::integral_constant<int, 2>{});
+}
+
+// Device helpers ----------------------------------------------------------------
+
+// Index within an axis of row m of tile r (see Layouts).
+__device__ __forceinline__ int tile_index(int r, int m) { return 32 * (r >> 1) + 8 * (m >> 2) + 4 * (r & 1) + (m & 3); }
+// First of the four consecutive indices that a lane's accumulators of tile r hold.
+__device__ __forceinline__ int acc_index(int r, int g) { return 32 * (r >> 1) + 8 * g + 4 * (r & 1); }
+
+struct Sequence {
+    int64_t b, t0, slot;
+    int len;
+};
+
+__device__ __forceinline__ Sequence sequence(const GdrArgs& a, int64_t n) {
+    if (!a.offsets) return {n, 0, n * a.chunks, int(a.T)};
+    int64_t lo = a.offsets[n], hi = a.offsets[n + 1];
+    lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
+    hi = hi < lo ? lo : hi > a.T ? a.T : hi;
+    // Sequence n's chunks take the slots from lo / 64 + n: consecutive sequences cannot meet, since
+    // floor((lo + len) / 64) + 1 >= floor(lo / 64) + ceil(len / 64); the last slot is below T / 64 + N.
+    return {0, lo, lo / kChunk + n, int(hi - lo)};
+}
+
+// The sequence a chunk slot belongs to (-1: none), and its chunk there.
+__device__ __forceinline__ int64_t slot_sequence(const GdrArgs& a, int64_t slot, Sequence& s, int& chunk) {
+    int64_t n;
+    if (!a.offsets) {
+        n = slot / a.chunks;
+    } else {
+        int64_t lo = 0, hi = a.N - 1;       // the last n whose first slot is at or before this one
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) / 2;
+            if (sequence(a, mid).slot <= slot) lo = mid;
+            else hi = mid - 1;
+        }
+        n = lo;
+    }
+    s = sequence(a, n);
+    if (slot < s.slot || (slot - s.slot) * kChunk >= s.len) return -1;
+    chunk = int(slot - s.slot);
+    return n;
+}
+
+// x as NP bfloat16 parts, each the rounding of what the ones before leave.
+template <int NP, int W, class Vec>
+__device__ __forceinline__ void split(const float (&x)[W], Vec (&p)[NP]) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        float r = x[j];
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const __bf16 h = __bf16(r);
+            p[n][j] = h;
+            if (n + 1 < NP) r -= float(h);
+        }
+    }
+}
+
+template <int NP>
+__device__ __forceinline__ void split4(const f32x4& x, bf16x4 (&p)[NP]) {
+    const float v[4] = {x[0], x[1], x[2], x[3]};
+    split<NP, 4>(v, p);
+}
+
+// acc += A B over one block of 32, the smallest products first.
+template <int NA, int NB>
+__device__ __forceinline__ void mma(f32x4& acc, const bf16x8 (&a)[NA], const bf16x8 (&b)[NB]) {
+#pragma unroll
+    for (int s = NA + NB - 2; s >= 0; --s) {
+        if (s >= kParts) continue;
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = s - i;
+            if (j >= 0 && j < NB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc, 0, 0, 0);
+        }
+    }
+}
+
+__device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+
+// Eight elements from p on, those past `left` as zero, as exact parts.
+template <int DT>
+__device__ __forceinline__ void load_parts(const typename Storage<DT>::type* p, int left, bool vec, bf16x8 (&x)[parts_of(DT)]) {
+    if constexpr (DT == 1) {
+        bf16x8 v;
+        if (vec) {
+            if (left >= 8) v = *reinterpret_cast<const bf16x8*>(p);
+            else
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __bf16(0.f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = j < left ? p[j] : __bf16(0.f);
+        }
+        x[0] = v;
+    } else {
+        float v[8];
+        if (vec && left >= 8) {
+            load_floats<8>(p, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = !vec && j < left ? float(p[j]) : 0.f;
+        }
+        split<parts_of(DT), 8>(v, x);
+    }
+}
+
+// Fragments of T or P before row tile r in its record, and its blocks of
+// tokens: those at or before the rows (forward), at or behind them (backward).
+template <bool BWD> __device__ __forceinline__ int tri_first(int r) {
+    return BWD ? (r < 2 ? 2 * r : r + 2) : (r < 2 ? r : 2 * r - 2);
+}
+template <bool BWD> __device__ __forceinline__ bool tri_has(int r, int b) { return BWD ? b >= (r >> 1) : b <= (r >> 1); }
+template <bool BWD> __device__ __forceinline__ int tri_index(int r, int b) { return tri_first<BWD>(r) + (BWD ? b - (r >> 1) : b); }
+
+// The passes over a sequence: blocks of all the columns and heads that share a
+// key head run on one XCD (block % 8), where they share its fragments in L2.
+__device__ __forceinline__ bool unit_of(const GdrArgs& a, int strips, int64_t& n, int& hv, int& strip) {
+    const int per = strips * a.group;
+    const int64_t u = blockIdx.x / (8 * int64_t(per)) * 8 + blockIdx.x % 8;
+    const int s = int(blockIdx.x / 8 % per);
+    if (u >= a.N * a.Hk) return false;
+    n = u / a.Hk;
+    hv = int(u % a.Hk) * a.group + s / strips;
+    strip = s % strips;
+    return true;
+}
+
+// Four indices' parts into one half of a lane's place in a fragment (stride: between the parts' fragments, in lanes).
+template <int NP>
+__device__ __forceinline__ void put_parts(bf16x8* frag, int stride, int lane, int half, const bf16x4 (&p)[NP]) {
+#pragma unroll
+    for (int n = 0; n < NP; ++n) reinterpret_cast<bf16x4*>(frag + n * stride + lane)[half] = p[n];
+}
+
+}  // namespace qc

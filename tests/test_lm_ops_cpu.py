@@ -131,6 +131,56 @@ def test_step_refusals(lib):
     assert step(lib, dims(T=0), p=(None,) * 6, out=None) == OK
 
 
+def whole(lib, d, p=tuple(range(1, 12)), ws_bytes=None):
+    """gdr_fwd: query, key, value, log_decay, beta, offsets, initial_state, out, final_state, saved, workspace."""
+    ptr = [None if x is None else (x if isinstance(x, ctypes.c_void_p) else P(x)) for x in p]
+    return lib.gdr_fwd(d, *ptr, lib.gdr_workspace_bytes(d, 0) if ws_bytes is None else ws_bytes, None)
+
+
+def whole_bwd(lib, d, p=tuple(range(1, 17)), ws_bytes=None):
+    """gdr_bwd: query .. beta, offsets, saved, d_out, d_final, six gradients, workspace."""
+    ptr = [None if x is None else (x if isinstance(x, ctypes.c_void_p) else P(x)) for x in p]
+    return lib.gdr_bwd(d, *ptr, lib.gdr_workspace_bytes(d, 1) if ws_bytes is None else ws_bytes, None)
+
+
+def but(i, x, n=11):
+    return tuple(x if j == i else j + 1 for j in range(n))
+
+
+def test_rule_refusals(lib):
+    assert whole(lib, None) == E_NULL and whole_bwd(lib, None) == E_NULL
+    for i in (0, 1, 2, 3, 4, 7):
+        assert whole(lib, dims(), p=but(i, None)) == E_NULL, i
+    packed = dims(B=1, T=9, N=3)
+    packed.packed = 1
+    assert whole(lib, packed, p=but(5, None)) == E_NULL
+    for bad in (dict(B=-1), dict(T=-1), dict(Hv=3), dict(K=0), dict(K=129), dict(V=1025), dict(N=3), dict(k=(1, 1, -1)),
+                dict(B=1 << 30, T=1 << 30), dict(T=1 << 31)):
+        assert whole(lib, dims(**bad)) == E_SHAPE, bad
+        assert lib.gdr_saved_bytes(dims(**bad)) == 0 and lib.gdr_workspace_bytes(dims(**bad), 1) == 0
+    two = dims(B=2, N=3)
+    two.packed = 1
+    assert whole(lib, two) == E_SHAPE                                   # packed rows lie in a batch of one
+    assert whole(lib, dims(dtype=-1)) == E_DTYPE
+    assert whole(lib, dims(), p=but(10, None)) == E_WS
+    assert whole(lib, dims(), ws_bytes=lib.gdr_workspace_bytes(dims(), 0) - 1) == E_WS
+    off = lambda n, by: ctypes.c_void_p(P(n).value + by)
+    for i, by in ((0, 1), (3, 2), (5, 2), (6, 2), (7, 1), (8, 2), (9, 64), (10, 128)):
+        assert whole(lib, dims(), p=but(i, off(i + 1, by))) == E_ALIGN, i
+    assert whole(lib, dims(), p=but(7, 3)) == E_ALIAS                   # out over value
+    assert whole(lib, dims(), p=but(8, 7)) == E_ALIAS                   # final over initial state
+    assert whole(lib, dims(), p=but(9, 11)) == E_ALIAS                  # saved over the workspace
+    assert whole(lib, dims(B=0), p=(None,) * 10 + (11,)) == OK
+    assert whole_bwd(lib, dims(), p=tuple(range(1, 10)) + (None,) * 6 + (16,)) == OK    # nothing wanted
+    for i in (0, 6, 7):
+        assert whole_bwd(lib, dims(), p=but(i, None, 16)) == E_NULL, i
+    assert whole_bwd(lib, dims(), p=but(15, None, 16)) == E_WS
+    assert whole_bwd(lib, dims(), ws_bytes=lib.gdr_workspace_bytes(dims(), 1) - 1) == E_WS
+    assert whole_bwd(lib, dims(), p=but(9, 8, 16)) == E_ALIAS           # d_query over d_out
+    assert whole_bwd(lib, dims(), p=but(14, 7, 16)) == E_ALIAS          # d_initial over saved
+    assert whole_bwd(lib, dims(), p=but(6, off(7, 16), 16)) == E_ALIGN
+
+
 def qdims(B=2, T=3, Hq=4, Hk=2, D=32, R=16, Pn=64, dtype=1, kind=0, eps=1e-6, **strides):
     d = capi.QknDims(B, T, Hq, Hk, D, R, Pn)
     d.q_stride[:] = strides.get("q", (T * Hq * D, Hq * D, D))
@@ -187,6 +237,8 @@ def test_python_refuses_host_tensors_and_gradients():
         autograd.gated_delta_step(q, q, v, g, g, s)
     with pytest.raises(ValueError, match="GPU"):
         autograd.qk_norm_rotate(q, q)
+    with pytest.raises(ValueError, match="GPU"):
+        autograd.gated_delta_rule(q, q, v, g, g, s)
     with pytest.raises(ValueError, match="no gradient"):
         autograd.gated_delta_step(q.clone().requires_grad_(), q, v, g, g, s)
     with pytest.raises(ValueError, match="detach"):
