@@ -34,9 +34,9 @@ __global__ void __launch_bounds__(512) gdr_bwd_kernel(GdrArgs a, int strips) {
     const int col = strip * 16 + m;
     const int i0 = acc_index(w, g);
     const int64_t krec = krec_bytes(KB, NPI);
-    const char* kr = a.krec + (s.slot * a.Hk + hk) * krec;
-    const char* hr = a.hrec + (s.slot * a.Hv + hv) * kHrecBytes;
-    const int64_t kstep = a.Hk * krec, hstep = a.Hv * kHrecBytes;
+    const char* kr = a.krec + (hk * a.slots + s.slot) * krec;
+    const char* hr = a.hrec + (hv * a.slots + s.slot) * kHrecBytes;
+    const int64_t kstep = krec, hstep = kHrecBytes;
     const int64_t row0 = (s.b * a.T + s.t0) * a.Hv + hv;      // this head's row of the sequence's first token
 
     if (wave < 4) {
@@ -62,8 +62,10 @@ __global__ void __launch_bounds__(512) gdr_bwd_kernel(GdrArgs a, int strips) {
             }
         put_state();
         bf16x8 ka[KB][NPI], kt[ST][2][NPI], ta[2][kParts];
-        f32x4 gamma, eta, beta;
-        float last;
+        // The gates of the next chunk are loaded a whole chunk ahead: the first of them is needed at the end of phase 1.
+        f32x4 gamma, eta, beta, gamma_next, eta_next, beta_next;
+        float last, last_next;
+        const int zero = lane_zero();
         auto load_k = [&](int c) {
             const bf16x8* p = reinterpret_cast<const bf16x8*>(kr + c * kstep) + int64_t(w) * KB * NPI * 64 + lane;
 #pragma unroll
@@ -73,10 +75,10 @@ __global__ void __launch_bounds__(512) gdr_bwd_kernel(GdrArgs a, int strips) {
         };
         auto load_gates = [&](int c) {
             const Gates* p = reinterpret_cast<const Gates*>(hr + c * hstep + kGateOffset);
-            gamma = *reinterpret_cast<const f32x4*>(&p->gamma[i0]);
-            eta = *reinterpret_cast<const f32x4*>(&p->eta[i0]);
-            beta = *reinterpret_cast<const f32x4*>(&p->beta[i0]);
-            last = p->gamma[kChunk - 1];
+            gamma_next = *reinterpret_cast<const f32x4*>(&p->gamma[i0]);
+            eta_next = *reinterpret_cast<const f32x4*>(&p->eta[i0]);
+            beta_next = *reinterpret_cast<const f32x4*>(&p->beta[i0]);
+            last_next = p->gamma[kChunk - 1 + zero];
         };
         auto load_t = [&](int c) {
             const bf16x8* p = reinterpret_cast<const bf16x8*>(hr + c * hstep) + lane;
@@ -107,23 +109,29 @@ __global__ void __launch_bounds__(512) gdr_bwd_kernel(GdrArgs a, int strips) {
         __syncthreads();      // its Q^T (gamma O)
         for (int c = chunks - 1; c >= 0; --c) {
             const int next = c > 0 ? c - 1 : 0;
+            gamma = gamma_next;
+            eta = eta_next;
+            beta = beta_next;
+            last = last_next;
+            load_gates(next);
             {
-                float* p = a.ds + ((s.slot + c) * a.Hv + hv) * int64_t(32 * KB) * a.VP + col;
+                float* p = a.ds + (hv * a.slots + s.slot + c) * int64_t(32 * KB) * a.VP + col;
 #pragma unroll
                 for (int x = 0; x < ST; ++x)
                     if (w + 4 * x < 2 * KB)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) p[int64_t(acc_index(w + 4 * x, g) + r) * a.VP] = st[x][r];
             }
-            f32x4 acc = zero4();
+            f32x4 acc = zero4(), odd = zero4();       // two sums, so that products need not wait for each other
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
                 bf16x8 x[kParts];
 #pragma unroll
                 for (int i = 0; i < kParts; ++i) x[i] = sf[b][i][lane];
-                mma(acc, ka[b], x);
+                mma(b & 1 ? odd : acc, ka[b], x);
             }
             load_k(next);
+            acc += odd;
             {
                 const f32x4 y = po[w][lane];
                 f32x4 x;
@@ -152,7 +160,7 @@ __global__ void __launch_bounds__(512) gdr_bwd_kernel(GdrArgs a, int strips) {
                 split4(x, p);
                 put_parts(&xf[w >> 1][0][0], 64, lane, w & 1, p);
             }
-            float* xs = a.x + ((s.slot + c) * a.Hv + hv) * int64_t(kChunk) * a.VP + col;
+            float* xs = a.x + (hv * a.slots + s.slot + c) * int64_t(kChunk) * a.VP + col;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = c * kChunk + i0 + r;
@@ -177,7 +185,6 @@ __global__ void __launch_bounds__(512) gdr_bwd_kernel(GdrArgs a, int strips) {
                     if (w + 4 * x < 2 * KB) mma(st[x], kt[x][b], y);
             }
             load_kt(next);
-            load_gates(next);
             put_state();
             __syncthreads();
         }
@@ -192,14 +199,15 @@ __global__ void __launch_bounds__(512) gdr_bwd_kernel(GdrArgs a, int strips) {
         }
     } else {
         bf16x8 pa[2][kParts], qt[ST][2][NPI];
-        float dr[4];
+        E dr[4];          // as loaded
         f32x4 gamma;
         auto load_do = [&](int c) {
-            const E* p = static_cast<const E*>(a.d_out) + row0 * a.V + col;
+            // Rows behind the end and columns past V read the nearest one inside, and are dropped where used: no branches.
+            const E* p = static_cast<const E*>(a.d_out) + row0 * a.V + (col < a.V ? col : 0);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = c * kChunk + i0 + r;
-                dr[r] = i < s.len && col < a.V ? float(p[int64_t(i) * a.Hv * a.V]) : 0.f;
+                const int i = c * kChunk + i0 + r < s.len ? c * kChunk + i0 + r : s.len - 1;
+                dr[r] = p[int64_t(i) * a.Hv * a.V];
             }
             gamma = *reinterpret_cast<const f32x4*>(&reinterpret_cast<const Gates*>(hr + c * hstep + kGateOffset)->gamma[i0]);
         };
@@ -234,11 +242,11 @@ __global__ void __launch_bounds__(512) gdr_bwd_kernel(GdrArgs a, int strips) {
                 f32x4 x;
                 bf16x4 o[NPI], p[kParts];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = dr[r];
+                for (int r = 0; r < 4; ++r) x[r] = c * kChunk + i0 + r < s.len && col < a.V ? float(dr[r]) : 0.f;
                 split4(x, o);
                 put_parts(&of[w >> 1][0][0], 64, lane, w & 1, o);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = a.scale * gamma[r] * dr[r];
+                for (int r = 0; r < 4; ++r) x[r] *= a.scale * gamma[r];
                 split4(x, p);
                 put_parts(&gf[w >> 1][0][0], 64, lane, w & 1, p);
                 load_do(next);

@@ -78,13 +78,14 @@ struct GdrArgs {
     const int32_t* offsets;
     void* out;
     float* fin;
-    char *krec, *hrec;                 // workspace: [slots][Hk] and [slots][Hv] records
-    float *save_s, *save_u;            // saved: [slots][Hv][KP][VP] and [slots][Hv][64][VP] (or null)
+    // By head, then by chunk: a block of the passes over a sequence walks through memory, not across it.
+    char *krec, *hrec;                 // workspace: [Hk][slots] and [Hv][slots] records
+    float *save_s, *save_u;            // saved: [Hv][slots][KP][VP] and [Hv][slots][64][VP] (or null)
     const void* d_out;
     const float* d_fin;
     void *dq, *dk, *dv;
     float *dg, *db, *ds0;
-    float *x, *ds;                     // workspace: [slots][Hv][64][VP] and [slots][Hv][KP][VP]
+    float *x, *ds;                     // workspace: [Hv][slots][64][VP] and [Hv][slots][KP][VP]
     int64_t qs[3], ks[3], vs[3];
     int64_t T, slots, N, chunks;       // chunks: per sequence, without offsets
     int Hk, Hv, group, K, V, VP;
@@ -152,19 +153,30 @@ __device__ __forceinline__ int64_t slot_sequence(const GdrArgs& a, int64_t slot,
     return n;
 }
 
-// x as NP bfloat16 parts, each the rounding of what the ones before leave.
+// x as NP bfloat16 parts, each the rounding of what the ones before leave: one
+// leaves 2^-9 of x, two 2^-18, three nothing of its 24 bits.
 template <int NP, int W, class Vec>
 __device__ __forceinline__ void split(const float (&x)[W], Vec (&p)[NP]) {
+    static_assert(W % 2 == 0, "pairs");
+    typedef uint32_t Words __attribute__((ext_vector_type(W / 2)));
+    typedef __bf16 Pair __attribute__((ext_vector_type(2)));
+    Words out[NP];
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        float r = x[j];
+    for (int j = 0; j < W; j += 2) {
+        float a = x[j], b = x[j + 1];
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-            const __bf16 h = __bf16(r);
-            p[n][j] = h;
-            if (n + 1 < NP) r -= float(h);
+            const Pair h = {__bf16(a), __bf16(b)};
+            const uint32_t u = __builtin_bit_cast(uint32_t, h);      // both at once; taken apart by a shift and a mask
+            out[n][j / 2] = u;
+            if (n + 1 < NP) {
+                a -= __uint_as_float(u << 16);
+                b -= __uint_as_float(u & 0xffff0000u);
+            }
         }
     }
+#pragma unroll
+    for (int n = 0; n < NP; ++n) p[n] = __builtin_bit_cast(Vec, out[n]);
 }
 
 template <int NP>
@@ -185,6 +197,20 @@ __device__ __forceinline__ void mma(f32x4& acc, const bf16x8 (&a)[NA], const bf1
             if (j >= 0 && j < NB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc, 0, 0, 0);
         }
     }
+}
+
+// Zero that the compiler takes for a lane's own: an address with it is read by
+// a vector load.  A scalar load would be waited for with the LDS reads.
+__device__ __forceinline__ int lane_zero() {
+    int z = 0;
+    asm("" : "+v"(z));
+    return z;
+}
+
+// A lane's share of fragment f of a record (base and f the wave's: one address
+// register per lane serves all).
+__device__ __forceinline__ bf16x8 fragment(const char* base, int64_t f, int lane) {
+    return reinterpret_cast<const bf16x8*>(base + f * (kFrag * 2))[uint32_t(lane)];
 }
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }

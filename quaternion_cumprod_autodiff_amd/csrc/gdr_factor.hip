@@ -36,8 +36,8 @@ __global__ void __launch_bounds__(256) gdr_factor_kernel(GdrArgs a) {
     const bool lead = hv % a.group == 0;
     const int rem = s.len - chunk * kChunk;          // rows of this chunk, and of the ones behind it
     const int64_t t0 = s.t0 + int64_t(chunk) * kChunk;
-    char* kr = a.krec + (slot * a.Hk + hk) * krec_bytes(KB, NPI);
-    char* hr = a.hrec + (slot * a.Hv + hv) * kHrecBytes;
+    char* kr = a.krec + (hk * a.slots + slot) * krec_bytes(KB, NPI);
+    char* hr = a.hrec + (hv * a.slots + slot) * kHrecBytes;
     bf16x8* k_rows = reinterpret_cast<bf16x8*>(kr);
     bf16x8* q_set = k_rows + set_frags(KB, NPI) * 64;
     bf16x8* k_cols = q_set + set_frags(KB, NPI) * 64;

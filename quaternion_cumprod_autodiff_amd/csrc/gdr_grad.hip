@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
     if (slot_sequence(a, slot, s, chunk) < 0) return;
     const int rem = s.len - chunk * kChunk;
     const int64_t token0 = s.b * a.T + s.t0 + int64_t(chunk) * kChunk;      // dense index of the chunk's first token
-    const bf16x8* kr = reinterpret_cast<const bf16x8*>(a.krec + (slot * a.Hk + hk) * krec_bytes(KB, NPI));
+    const bf16x8* kr = reinterpret_cast<const bf16x8*>(a.krec + (hk * a.slots + slot) * krec_bytes(KB, NPI));
     const bf16x8* qt_set = kr + set_frags(KB, NPI) * 64;
     const bf16x8* kt_set = qt_set + set_frags(KB, NPI) * 64;
 
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
         for (int r = 0; r < 2; ++r) dq_all[x][r] = dk_all[x][r] = zero4();
 
     for (int hv = hk * a.group; hv < (hk + 1) * a.group; ++hv) {
-        const Gates* ga = reinterpret_cast<const Gates*>(a.hrec + (slot * a.Hv + hv) * kHrecBytes + kGateOffset);
+        const Gates* ga = reinterpret_cast<const Gates*>(a.hrec + (hv * a.slots + slot) * kHrecBytes + kGateOffset);
         __syncthreads();                                  // the head before is done with what is in LDS
         if (tid < 64) {
             gamma[tid] = ga->gamma[tid];
@@ -109,10 +109,10 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) aq[x][r] = ar[x][r] = aw[x][r] = zero4();
         float sds = 0.f, xdotv = 0.f;
-        const float* s0 = a.save_s + (slot * a.Hv + hv) * int64_t(32 * KB) * a.VP;
-        const float* s1 = a.ds + (slot * a.Hv + hv) * int64_t(32 * KB) * a.VP;
-        const float* us = a.save_u + (slot * a.Hv + hv) * int64_t(kChunk) * a.VP;
-        const float* xs = a.x + (slot * a.Hv + hv) * int64_t(kChunk) * a.VP;
+        const float* s0 = a.save_s + (hv * a.slots + slot) * int64_t(32 * KB) * a.VP;
+        const float* s1 = a.ds + (hv * a.slots + slot) * int64_t(32 * KB) * a.VP;
+        const float* us = a.save_u + (hv * a.slots + slot) * int64_t(kChunk) * a.VP;
+        const float* xs = a.x + (hv * a.slots + slot) * int64_t(kChunk) * a.VP;
         for (int v0 = 0; v0 < a.V; v0 += kPiece) {
             if (v0) __syncthreads();                      // the piece before is done
             // Thread (token, group of 16 columns): X, U, dO as fragments; X . v.
