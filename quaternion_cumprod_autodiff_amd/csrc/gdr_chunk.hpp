@@ -41,7 +41,10 @@
 // an axis stand for the indices 32 (r / 2) + 8 (m / 4) + 4 (r % 2) + m % 4 of
 // it, so that the accumulators of tiles 2b and 2b + 1 are, in place, the 8
 // consecutive indices of a B fragment's block b: results become operands
-// without a transpose.
+// without a transpose.  S0, U, X and dS1 go through memory as pieces of 16
+// columns of V, [Hv][slots][VP / 16][tiles][16 rows][16 columns] float32: what
+// one block writes of a chunk is whole lines, and 8 columns of a row are 32
+// bytes of one.
 #pragma once
 
 #include "gdr_internal.hpp"
@@ -80,12 +83,12 @@ struct GdrArgs {
     float* fin;
     // By head, then by chunk: a block of the passes over a sequence walks through memory, not across it.
     char *krec, *hrec;                 // workspace: [Hk][slots] and [Hv][slots] records
-    float *save_s, *save_u;            // saved: [Hv][slots][KP][VP] and [Hv][slots][64][VP] (or null)
+    float *save_s, *save_u;            // saved: S0 and U, pieces (below) of 2 KB and 4 tiles (or null)
     const void* d_out;
     const float* d_fin;
     void *dq, *dk, *dv;
     float *dg, *db, *ds0;
-    float *x, *ds;                     // workspace: [Hv][slots][64][VP] and [Hv][slots][KP][VP]
+    float *x, *ds;                     // workspace: X and dS1, as U and S0
     int64_t qs[3], ks[3], vs[3];
     int64_t T, slots, N, chunks;       // chunks: per sequence, without offsets
     int Hk, Hv, group, K, V, VP;

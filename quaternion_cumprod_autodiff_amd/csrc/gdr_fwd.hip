@@ -123,8 +123,12 @@ __global__ void __launch_bounds__(256, DT == 1 ? 2 : 1) gdr_fwd_kernel(GdrArgs a
     };
     const int64_t o_step = int64_t(a.Hv) * a.V;
     E* o_lane = static_cast<E*>(a.out) + (s.b * a.T + s.t0 + i0) * o_step + int64_t(hv) * a.V + col;
-    float* save_s = SAVE ? a.save_s + ((hv * a.slots + s.slot) * int64_t(32 * KB) + acc_index(w, g)) * a.VP + col : nullptr;
-    float* save_u = SAVE ? a.save_u + ((hv * a.slots + s.slot) * int64_t(kChunk) + i0) * a.VP + col : nullptr;
+    float *save_s = nullptr, *save_u = nullptr;
+    if constexpr (SAVE) {
+        const int64_t piece = ((hv * a.slots + s.slot) * strips + strip) * 256;
+        save_s = a.save_s + piece * (2 * KB) + w * 256 + (4 * g) * 16 + m;
+        save_u = a.save_u + piece * 4 + w * 256 + (4 * g) * 16 + m;
+    }
     if (chunks) {
         load_rows(0, 0, ka);
         load_v(0);
@@ -151,8 +155,8 @@ __global__ void __launch_bounds__(256, DT == 1 ? 2 : 1) gdr_fwd_kernel(GdrArgs a
             for (int y = 0; y < ST; ++y)
                 if (w + 4 * y < 2 * KB)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) save_s[(64 * y + r) * a.VP] = st[y][r];      // tile w + 4: 64 rows on
-            save_s += int64_t(32 * KB) * a.VP;
+                    for (int r = 0; r < 4; ++r) save_s[1024 * y + 16 * r] = st[y][r];
+            save_s += int64_t(strips) * (2 * KB) * 256;
         }
         f32x4 acc = zero4(), odd = zero4();       // two sums, so that products need not wait for each other
 #pragma unroll
@@ -209,8 +213,8 @@ __global__ void __launch_bounds__(256, DT == 1 ? 2 : 1) gdr_fwd_kernel(GdrArgs a
         load_t(next);
         if constexpr (SAVE) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) save_u[r * a.VP] = acc[r];
-            save_u += int64_t(kChunk) * a.VP;
+            for (int r = 0; r < 4; ++r) save_u[16 * r] = acc[r];
+            save_u += int64_t(strips) * 4 * 256;
         }
         __syncthreads();
         // Phase 3.

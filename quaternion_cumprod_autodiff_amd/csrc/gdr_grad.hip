@@ -109,10 +109,9 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) aq[x][r] = ar[x][r] = aw[x][r] = zero4();
         float sds = 0.f, xdotv = 0.f;
-        const float* s0 = a.save_s + (hv * a.slots + slot) * int64_t(32 * KB) * a.VP;
-        const float* s1 = a.ds + (hv * a.slots + slot) * int64_t(32 * KB) * a.VP;
-        const float* us = a.save_u + (hv * a.slots + slot) * int64_t(kChunk) * a.VP;
-        const float* xs = a.x + (hv * a.slots + slot) * int64_t(kChunk) * a.VP;
+        const int64_t piece = (hv * a.slots + slot) * int64_t(a.VP / 16) * 256;
+        const float *s0 = a.save_s + piece * (2 * KB), *s1 = a.ds + piece * (2 * KB);
+        const float *us = a.save_u + piece * 4, *xs = a.x + piece * 4;
         for (int v0 = 0; v0 < a.V; v0 += kPiece) {
             if (v0) __syncthreads();                      // the piece before is done
             // Thread (token, group of 16 columns): X, U, dO as fragments; X . v.
@@ -129,8 +128,9 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
                     float x8[8], u8[8];
                     const bool have = v < a.VP;
                     if (have) {
-                        load_floats<8>(xs + int64_t(t) * a.VP + v, x8);
-                        load_floats<8>(us + int64_t(t) * a.VP + v, u8);
+                        const int at = (v >> 4) * 1024 + tile * 256 + row * 16 + (v & 15);
+                        load_floats<8>(xs + at, x8);
+                        load_floats<8>(us + at, u8);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) x8[e] = u8[e] = 0.f;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
                     for (int y = 0; y < TW; ++y) {
                         float s8[8], d8[8];
                         if (v < a.VP) {
-                            const int64_t at = int64_t(tile_index(cg * TW + y, m)) * a.VP + v;
+                            const int at = (v >> 4) * (2 * KB * 256) + (cg * TW + y) * 256 + m * 16 + (v & 15);
                             load_floats<8>(s0 + at, s8);
                             load_floats<8>(s1 + at, d8);
                         } else {
