@@ -63,6 +63,7 @@ GdrArgs arguments(const gdr_dims& d, const Plan& p, const void* q, const void* k
     a.Hk = int(d.Hk); a.Hv = int(d.Hv); a.group = int(d.Hv / d.Hk); a.K = int(d.K); a.V = int(d.V); a.VP = int(p.vp);
     a.scale = d.scale;
     const size_t e = dtype_bytes(d.dtype);
+    a.vec_v = d.V % 8 == 0 && rows_on_16(v, d.v_stride, e);
     a.vec_qk = d.K % 8 == 0 && rows_on_16(q, d.q_stride, e) && rows_on_16(k, d.k_stride, e);
     return a;
 }
@@ -119,6 +120,7 @@ int gdr_fwd(const gdr_dims* dims, const void* query, const void* key, const void
     if (qc::outputs_overlap(sp, 4, 11)) return QC_ERR_ALIAS;
     if (!d.N) return QC_OK;
     qc::GdrArgs a = qc::arguments(d, p, query, key, value, log_decay, beta, offsets);
+    a.vec_o = d.V % 8 == 0 && qc::aligned_to(out, 16);
     a.s0 = initial_state; a.out = out; a.fin = final_state;
     a.krec = static_cast<char*>(workspace);
     a.hrec = a.krec + p.krec;
@@ -162,7 +164,7 @@ int gdr_bwd(const gdr_dims* dims, const void* query, const void* key, const void
     if (qc::outputs_overlap(sp, 7, 16)) return QC_ERR_ALIAS;
     if (!d.N) return QC_OK;
     qc::GdrArgs a = qc::arguments(d, p, query, key, value, log_decay, beta, offsets);
-    a.vec_v = d.V % 8 == 0 && qc::rows_on_16(value, d.v_stride, e) && qc::aligned_to(d_out, 16);
+    a.vec_o = d.V % 8 == 0 && qc::aligned_to(d_out, 16) && qc::aligned_to(d_value, 16);
     a.krec = static_cast<char*>(workspace);
     a.hrec = a.krec + p.krec;
     a.x = reinterpret_cast<float*>(a.hrec + p.hrec);

@@ -73,7 +73,7 @@ struct Gates {
     double cum[kChunk];
 };
 constexpr int64_t kGateOffset = 2 * kTriFrags * kFrag * 2;
-constexpr int64_t kHrecBytes = (kGateOffset + int64_t(sizeof(Gates)) + 255) / 256 * 256;
+constexpr int64_t kHrecBytes = (kGateOffset + int64_t(sizeof(Gates)) + 4095) / 4096 * 4096;
 
 struct GdrArgs {
     const void *q, *k, *v;
@@ -92,7 +92,7 @@ struct GdrArgs {
     int64_t qs[3], ks[3], vs[3];
     int64_t T, slots, N, chunks;       // chunks: per sequence, without offsets
     int Hk, Hv, group, K, V, VP;
-    int vec_qk, vec_v;                 // query and key rows, value and out rows: on 16 bytes, sizes multiples of 8
+    int vec_qk, vec_v, vec_o;          // query and key, value, and out (d_out, dv) rows: on 16 bytes, sizes multiples of 8 (16 for V in the passes)
     float scale;
 };
 
@@ -170,7 +170,8 @@ __device__ __forceinline__ void split(const float (&x)[W], Vec (&p)[NP]) {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
             const Pair h = {__bf16(a), __bf16(b)};
-            const uint32_t u = __builtin_bit_cast(uint32_t, h);      // both at once; taken apart by a shift and a mask
+            uint32_t u = __builtin_bit_cast(uint32_t, h);
+            asm("" : "+v"(u));      // one conversion for both, taken apart by a shift and a mask: left alone, the compiler converts twice
             out[n][j / 2] = u;
             if (n + 1 < NP) {
                 a -= __uint_as_float(u << 16);
@@ -272,5 +273,108 @@ __device__ __forceinline__ void put_parts(bf16x8* frag, int stride, int lane, in
 #pragma unroll
     for (int n = 0; n < NP; ++n) reinterpret_cast<bf16x4*>(frag + n * stride + lane)[half] = p[n];
 }
+
+// The memory wave of the passes over a sequence -----------------------------------
+//
+// A fifth wave moves a block's 16 columns between memory and LDS.  Stores wait
+// in the same queue as loads, so that a wave which stores would wait for its
+// stores at its next operand; and the columns' addresses, ends and conversions
+// stay out of the chain.  Between it and the others, columns lie in LDS by
+// column: [16][kColRow] floats of 64 tokens, where lane (g, m) finds 4 tokens
+// of column m in 16 bytes and the memory wave's lane t token t of each column.
+constexpr int kColRow = 68;
+// A 16 x 16 tile there: column m's rows 4 g .. in 16 bytes.
+constexpr int kTileRow = 20, kTile = 16 * kTileRow;
+
+// Token row p's 16 columns from `first` on, as they lie in memory (elements
+// are taken apart where they are used, so that nothing waits here).  VEC: whole
+// 16-byte pieces, all columns there; else columns past `size` read column 0.
+template <class E, bool VEC>
+struct Columns {
+    static constexpr int kWords = 16 * sizeof(E) / 4, kPer = 4 / sizeof(E);
+    typedef uint32_t Piece __attribute__((ext_vector_type(4)));
+    Piece x[kWords / 4];
+
+    __device__ __forceinline__ void load(const E* p, int first, int size) {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) x[i] = reinterpret_cast<const Piece*>(p + first)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                uint32_t u = 0;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int c = first + i * kPer + j;
+                    const E e = p[c < size ? c : 0];
+                    if constexpr (kPer == 1) u = __builtin_bit_cast(uint32_t, e);
+                    else u |= uint32_t(__builtin_bit_cast(uint16_t, e)) << (16 * j);
+                }
+                x[i / 4][i % 4] = u;
+            }
+        }
+    }
+
+    __device__ __forceinline__ float at(int j) const {
+        const uint32_t u = x[j / kPer / 4][j / kPer % 4];
+        if constexpr (kPer == 1) return __builtin_bit_cast(float, u);
+        else return float(__builtin_bit_cast(E, uint16_t(u >> (16 * (j % kPer)))));
+    }
+};
+
+template <class E, bool VEC>
+__device__ __forceinline__ void store_columns(E* p, int first, int size, const float (&x)[16]) {
+    if constexpr (VEC) {
+        store_floats<16>(p + first, x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (first + j < size) p[first + j] = E(x[j]);
+    }
+}
+
+// The other waves load their operands one phase ahead, from L2: the memory
+// wave has them there by then, touching the lines of the records two chunks on
+// (4 KiB at a time, the strips of a head in turn; with few strips the last of
+// them come from further away).
+template <int K_BYTES>
+struct Touch {
+    static constexpr int kTurns = 4, kUnits = K_BYTES / 4096 + int(kHrecBytes / 4096);
+    int x[kTurns] = {};
+
+    __device__ __forceinline__ void load(const char* krec, const char* hrec, int strip, int strips, int lane) {
+#pragma unroll
+        for (int j = 0; j < kTurns; ++j) {
+            int u = strip + j * strips;
+            u = u < kUnits ? u : kUnits - 1;
+            const char* p = u < K_BYTES / 4096 ? krec + u * 4096 : hrec + (u - K_BYTES / 4096) * 4096;
+            x[j] = reinterpret_cast<const int*>(p)[uint32_t(lane) * 16];
+        }
+    }
+    __device__ __forceinline__ void done() const {      // keeps the loads; waits for them
+#pragma unroll
+        for (int j = 0; j < kTurns; ++j) asm volatile("" ::"v"(x[j]));
+    }
+};
+
+// N tiles from LDS (each column by column) as a piece in memory has them (row by
+// row): read in one phase, stored in a later one.
+template <int N>
+struct Tiles {
+    f32x4 v[N];
+
+    __device__ __forceinline__ void read(const float* tiles, int lane) {
+        const int row = lane >> 2, c = (lane & 3) * 4;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] = tiles[i * kTile + (c + j) * kTileRow + row];
+    }
+
+    __device__ __forceinline__ void store(float* piece, int lane) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) *reinterpret_cast<f32x4*>(piece + i * 256 + lane * 4) = v[i];
+    }
+};
 
 }  // namespace qc

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
                     split<kParts, 8>(x8, xp8);
                     split<kParts, 8>(u8, up8);
                     const int left = in ? a.V - v : 0;
-                    load_parts<DT>(op_ + v, left, a.vec_v, o8);
+                    load_parts<DT>(op_ + v, left, a.vec_o, o8);
                     load_parts<DT>(vp + v, left, a.vec_v, v8);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
