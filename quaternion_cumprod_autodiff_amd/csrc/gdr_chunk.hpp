@@ -256,7 +256,7 @@ template <bool BWD> __device__ __forceinline__ int tri_index(int r, int b) { ret
 
 // The passes over a sequence: blocks of all the columns and heads that share a
 // key head run on one XCD (block % 8), where they share its fragments in L2.
-__device__ __forceinline__ bool unit_of(const GdrArgs& a, int strips, int64_t& n, int& hv, int& strip) {
+__device__ __forceinline__ bool unit_of(const GdrArgs& a, int strips, int64_t& n, int& hv, int& strip) {      // strip: of `strips` blocks
     const int per = strips * a.group;
     const int64_t u = blockIdx.x / (8 * int64_t(per)) * 8 + blockIdx.x % 8;
     const int s = int(blockIdx.x / 8 % per);
@@ -272,6 +272,15 @@ template <int NP>
 __device__ __forceinline__ void put_parts(bf16x8* frag, int stride, int lane, int half, const bf16x4 (&p)[NP]) {
 #pragma unroll
     for (int n = 0; n < NP; ++n) reinterpret_cast<bf16x4*>(frag + n * stride + lane)[half] = p[n];
+}
+
+// Strips of 16 columns to a block of the passes over a sequence.  One at a time
+// a CU holds one block (five waves, registers for two to a SIMD), and a block's
+// waves wait for each other three times a chunk.  So where strips are more than
+// CUs and pair up, a block takes two, ten waves in step, three to a SIMD; the
+// second strip finds the operands in L1.
+inline int strips_per_block(const GdrArgs& a, int strips, bool fits) {
+    return fits && strips % 2 == 0 && a.N * a.Hv * strips > 256 ? 2 : 1;
 }
 
 // The memory wave of the passes over a sequence -----------------------------------

@@ -18,20 +18,32 @@
 namespace qc {
 namespace {
 
-template <int DT, int KB, bool SAVE, bool VEC>
-__global__ void __launch_bounds__(320, 1) gdr_fwd_kernel(GdrArgs a, int strips) {
+template <int DT, int KB, bool SAVE, bool VEC, int NS>
+__global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrArgs a, int strips) {
     using E = typename Storage<DT>::type;
     constexpr int NPI = parts_of(DT);
     // Parts of S0, P and U that the output takes: two leave 2^-18 of them, far below the half step of bfloat16, 2^-9.
     constexpr int NPO = DT == 1 ? 2 : 3;
     constexpr int ST = (2 * KB + 3) / 4;             // tiles of S of a wave
-    __shared__ __align__(16) bf16x8 sf[KB][kParts][64], rf[2][kParts][64], ef[2][kParts][64], uf[2][NPO][64];
-    __shared__ __align__(16) float vb[16 * kColRow], ob[16 * kColRow], sb[SAVE ? 2 * KB * kTile : 4], ub[SAVE ? 4 * kTile : 4];
+    __shared__ __align__(16) bf16x8 sf_[NS][KB][kParts][64], rf_[NS][2][kParts][64], ef_[NS][2][kParts][64], uf_[NS][2][NPO][64];
+    __shared__ __align__(16) float vb_[NS][16 * kColRow], ob_[NS][16 * kColRow], sb_[NS][SAVE ? 2 * KB * kTile : 4], ub_[NS][SAVE ? 4 * kTile : 4];
+    __shared__ __align__(16) float gates_[NS][2][2][64];      // gamma and eta of this chunk and the next
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
+    const int sub = NS == 1 ? 0 : wave < 4 * NS ? wave >> 2 : wave - 4 * NS;      // which of the block's strips
+    auto& sf = sf_[sub];
+    auto& rf = rf_[sub];
+    auto& ef = ef_[sub];
+    auto& uf = uf_[sub];
+    auto& vb = vb_[sub];
+    auto& ob = ob_[sub];
+    auto& sb = sb_[sub];
+    auto& ub = ub_[sub];
+    auto& gates = gates_[sub];
     const int m = lane & 15, g = lane >> 4;
     int64_t n;
     int hv, strip;
-    if (!unit_of(a, strips, n, hv, strip)) return;
+    if (!unit_of(a, strips / NS, n, hv, strip)) return;
+    strip = strip * NS + sub;
     const Sequence s = sequence(a, n);
     const int chunks = (s.len + kChunk - 1) / kChunk;
 
@@ -40,7 +52,7 @@ __global__ void __launch_bounds__(320, 1) gdr_fwd_kernel(GdrArgs a, int strips) 
     const char* kr = a.krec + (hk * a.slots + s.slot) * krec;
     const char* hr = a.hrec + (hv * a.slots + s.slot) * kHrecBytes;
 
-    if (wave == 4) {
+    if (wave >= 4 * NS) {
         const E* v = static_cast<const E*>(a.v) + s.b * a.vs[0] + s.t0 * a.vs[1] + int64_t(hv) * a.vs[2];
         E* out = static_cast<E*>(a.out) + ((s.b * a.T + s.t0) * a.Hv + hv) * int64_t(a.V);
         const int64_t v_step = a.vs[1], o_step = int64_t(a.Hv) * a.V;
@@ -66,11 +78,24 @@ __global__ void __launch_bounds__(320, 1) gdr_fwd_kernel(GdrArgs a, int strips) 
             const int i = c * kChunk + lane;
             if (i < s.len) store_columns<E, VEC>(out + i * o_step, strip * 16, a.V, y);
         };
+        float gamma, eta;
+        auto load_gates = [&](int c) {
+            const Gates* p = reinterpret_cast<const Gates*>(hr + c * kHrecBytes + kGateOffset);
+            gamma = p->gamma[lane];
+            eta = p->eta[lane];
+        };
+        auto put_gates = [&](int c) {
+            gates[c & 1][0][lane] = gamma;
+            gates[c & 1][1][lane] = eta;
+        };
         Touch<int(krec)> ahead;
         if (chunks) {
             load_v(0);
+            load_gates(0);
             put_v(0);
+            put_gates(0);
             load_v(chunks > 1 ? 1 : 0);
+            load_gates(chunks > 1 ? 1 : 0);
             if (chunks > 1) ahead.load(kr + krec, hr + kHrecBytes, strip, strips, lane);
         }
         __syncthreads();
@@ -90,8 +115,10 @@ __global__ void __launch_bounds__(320, 1) gdr_fwd_kernel(GdrArgs a, int strips) 
             ahead.done();
             if (c + 1 < chunks) {
                 put_v(c + 1);
+                put_gates(c + 1);
                 const int then = c + 2 < chunks ? c + 2 : c + 1;
                 load_v(then);
+                load_gates(then);
                 ahead.load(kr + then * krec, hr + then * kHrecBytes, strip, strips, lane);
             }
             if (c) store_out(c - 1);
@@ -137,22 +164,12 @@ __global__ void __launch_bounds__(320, 1) gdr_fwd_kernel(GdrArgs a, int strips) 
     put_state();
 
     bf16x8 ka[KB][NPI], qa[KB][NPI], kt[ST][2][NPI], ta[2][kParts], pa[2][NPO];
-    // The gates of the next chunk are loaded a whole chunk ahead: the first of them is needed at the end of phase 1.
-    f32x4 gamma, eta, gamma_next, eta_next;
-    float last, last_next;
-    const int zero = lane_zero();
     auto load_rows = [&](int c, int set, bf16x8 (&x)[KB][NPI]) {
         const char* p = kr + c * krec;
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int i = 0; i < NPI; ++i) x[b][i] = fragment(p, set * set_frags(KB, NPI) + (w * KB + b) * NPI + i, lane);
-    };
-    auto load_gates = [&](int c) {
-        const Gates* p = reinterpret_cast<const Gates*>(hr + c * kHrecBytes + kGateOffset);
-        gamma_next = *reinterpret_cast<const f32x4*>(&p->gamma[i0]);
-        eta_next = *reinterpret_cast<const f32x4*>(&p->eta[i0]);
-        last_next = p->gamma[kChunk - 1 + zero];
     };
     auto load_kt = [&](int c) {
         const char* p = kr + c * krec;
@@ -167,7 +184,6 @@ __global__ void __launch_bounds__(320, 1) gdr_fwd_kernel(GdrArgs a, int strips) 
     if (chunks) {
         load_rows(0, 0, ka);
         load_rows(0, 1, qa);
-        load_gates(0);
     }
     __syncthreads();
     // Rows of the chunk's first half need one block of T and P, those of its second half two.
@@ -191,13 +207,11 @@ __global__ void __launch_bounds__(320, 1) gdr_fwd_kernel(GdrArgs a, int strips) 
         };
         for (int c = 0; c < chunks; ++c) {
             const int next = c + 1 < chunks ? c + 1 : c;
-            gamma = gamma_next;
-            eta = eta_next;
-            last = last_next;
             // Phase 1.  The two products share the reads of S0, and fill each other's waits.
             f32x4 acc = zero4(), odd = zero4(), o = zero4(), o_odd = zero4();
             load_t(c);
-            load_gates(next);
+            const float* gc = &gates[c & 1][0][0];
+            const f32x4 gamma = *reinterpret_cast<const f32x4*>(gc + i0);
             {
                 bf16x8 x[KB][kParts];
 #pragma unroll
@@ -236,7 +250,7 @@ __global__ void __launch_bounds__(320, 1) gdr_fwd_kernel(GdrArgs a, int strips) 
                     if ((b == 0 || HI)) mma(b ? odd : acc, ta[b], y[b]);
                 acc += odd;
                 bf16x4 p[kParts], q[NPO];
-                split4(eta * acc, p);
+                split4(*reinterpret_cast<const f32x4*>(gc + 64 + i0) * acc, p);
                 put_parts(&ef[w >> 1][0][0], 64, lane, w & 1, p);
                 split4(acc, q);
                 put_parts(&uf[w >> 1][0][0], 64, lane, w & 1, q);
@@ -247,7 +261,7 @@ __global__ void __launch_bounds__(320, 1) gdr_fwd_kernel(GdrArgs a, int strips) 
             load_rows(next, 0, ka);
             load_rows(next, 1, qa);
 #pragma unroll
-            for (int y = 0; y < ST; ++y) st[y] *= last;
+            for (int y = 0; y < ST; ++y) st[y] *= gc[kChunk - 1];
             {
                 bf16x8 y[2][kParts];
 #pragma unroll
@@ -293,15 +307,21 @@ hipError_t launch_gdr_fwd(int dt, int kb, bool save, const GdrArgs& a, hipStream
     return by_dtype_kb(dt, kb, [&](auto d, auto k) {
         constexpr int DT = decltype(d)::value, KB = decltype(k)::value;
         int strips = (a.V + 15) / 16;
-        const int64_t blocks = (a.N * a.Hk + 7) / 8 * 8 * strips * a.group;
+        const int ns = strips_per_block(a, strips, DT == 1);
+        const int64_t blocks = (a.N * a.Hk + 7) / 8 * 8 * (strips / ns) * a.group;
         const bool vec = a.vec_v && a.vec_o && a.V % 16 == 0;
-        const void* fn = save ? (vec ? reinterpret_cast<const void*>(&gdr_fwd_kernel<DT, KB, true, true>)
-                                     : reinterpret_cast<const void*>(&gdr_fwd_kernel<DT, KB, true, false>))
-                              : (vec ? reinterpret_cast<const void*>(&gdr_fwd_kernel<DT, KB, false, true>)
-                                     : reinterpret_cast<const void*>(&gdr_fwd_kernel<DT, KB, false, false>));
+        auto pick = [&](auto sv, auto vc) -> const void* {
+            constexpr bool SAVE = decltype(sv)::value, VEC = decltype(vc)::value;
+            if constexpr (DT == 1)
+                if (ns == 2) return reinterpret_cast<const void*>(&gdr_fwd_kernel<DT, KB, SAVE, VEC, 2>);
+            return reinterpret_cast<const void*>(&gdr_fwd_kernel<DT, KB, SAVE, VEC, 1>);
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        const void* fn = save ? (vec ? pick(yes, yes) : pick(yes, no)) : (vec ? pick(no, yes) : pick(no, no));
         GdrArgs args = a;
         void* params[] = {&args, &strips};
-        return hipLaunchKernel(fn, dim3(unsigned(blocks)), dim3(320), params, 0, st);
+        return hipLaunchKernel(fn, dim3(unsigned(blocks)), dim3(320u * ns), params, 0, st);
     });
 }
 
