@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
     };
     __shared__ __align__(16) Shared sh;
     __shared__ double cum[64];
-    __shared__ float gamma[64], eta[64], beta[64], xv[64], rowsum[2][64], red[3][4][64], dots[8];
+    __shared__ __align__(16) float gamma[64], eta[64], beta[64], xv[64], rowsum[2][64], red[3][4][64], dots[8];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, g = lane >> 4;
     const int cg = wave >> 1, rh = wave & 1;
@@ -59,41 +59,13 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
     const bf16x8* qt_set = kr + set_frags(KB, NPI) * 64;
     const bf16x8* kt_set = qt_set + set_frags(KB, NPI) * 64;
 
-    // K K^T, row tile rt against the column tiles 2 ch + 0, 1.
-    f32x4 kk[2] = {zero4(), zero4()};
-    if (tri_on) {
-#pragma unroll
-        for (int b = 0; b < KB; ++b) {
-            bf16x8 ka[NPI], kb[NPI];
-#pragma unroll
-            for (int p = 0; p < NPI; ++p) ka[p] = kr[((rt * KB + b) * NPI + p) * 64 + lane];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                for (int p = 0; p < NPI; ++p) kb[p] = kr[(((2 * ch + c) * KB + b) * NPI + p) * 64 + lane];
-                mma(kk[c], ka, kb);
-            }
-        }
-    }
-    // The wave's columns of K and Q, transposed: [tile][block of tokens].
-    bf16x8 kt[TW][2][NPI], qt[TW][2][NPI];
-    if (k_on) {
-#pragma unroll
-        for (int x = 0; x < TW; ++x)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int p = 0; p < NPI; ++p) {
-                    kt[x][b][p] = kt_set[(((cg * TW + x) * 2 + b) * NPI + p) * 64 + lane];
-                    qt[x][b][p] = qt_set[(((cg * TW + x) * 2 + b) * NPI + p) * 64 + lane];
-                }
-    }
     f32x4 dq_all[TW][2], dk_all[TW][2];
 #pragma unroll
     for (int x = 0; x < TW; ++x)
 #pragma unroll
         for (int r = 0; r < 2; ++r) dq_all[x][r] = dk_all[x][r] = zero4();
 
+#pragma unroll 1
     for (int hv = hk * a.group; hv < (hk + 1) * a.group; ++hv) {
         const Gates* ga = reinterpret_cast<const Gates*>(a.hrec + (hv * a.slots + slot) * kHrecBytes + kGateOffset);
         __syncthreads();                                  // the head before is done with what is in LDS
@@ -112,6 +84,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
         const int64_t piece = (hv * a.slots + slot) * int64_t(a.VP / 16) * 256;
         const float *s0 = a.save_s + piece * (2 * KB), *s1 = a.ds + piece * (2 * KB);
         const float *us = a.save_u + piece * 4, *xs = a.x + piece * 4;
+#pragma unroll 1
         for (int v0 = 0; v0 < a.V; v0 += kPiece) {
             if (v0) __syncthreads();                      // the piece before is done
             // Thread (token, group of 16 columns): X, U, dO as fragments; X . v.
@@ -160,45 +133,57 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
             }
             __syncthreads();
             const int blocks = a.V - v0 >= kPiece ? VB : (a.V - v0 + 31) / 32;
-            for (int b = 0; b < blocks; ++b) {
-                bf16x8 o[2][NPI], x[2][kParts], u[2][kParts];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-#pragma unroll
-                    for (int p = 0; p < NPI; ++p) o[r][p] = sh.rows.o[2 * rh + r][b][p][lane];
-#pragma unroll
-                    for (int p = 0; p < kParts; ++p) {
-                        x[r][p] = sh.rows.x[2 * rh + r][b][p][lane];
-                        u[r][p] = sh.rows.u[2 * rh + r][b][p][lane];
-                    }
-                }
-                const int v = v0 + 32 * b + 8 * g;
-                if (k_on) {
+            if (k_on) {
+                // The states' operands are loaded one block of V ahead.
+                float s8[TW][8], d8[TW][8];
+                auto load_states = [&](int b) {
+                    const int v = v0 + 32 * b + 8 * g;
+                    const bool have = v < a.VP;
 #pragma unroll
                     for (int y = 0; y < TW; ++y) {
-                        float s8[8], d8[8];
-                        if (v < a.VP) {
-                            const int at = (v >> 4) * (2 * KB * 256) + (cg * TW + y) * 256 + m * 16 + (v & 15);
-                            load_floats<8>(s0 + at, s8);
-                            load_floats<8>(s1 + at, d8);
-                        } else {
+                        const int at = have ? (v >> 4) * (2 * KB * 256) + (cg * TW + y) * 256 + m * 16 + (v & 15) : 0;
+                        load_floats<8>(s0 + at, s8[y]);
+                        load_floats<8>(s1 + at, d8[y]);
+                    }
+                };
+                load_states(0);
+#pragma unroll 1
+                for (int b = 0; b < blocks; ++b) {
+                    bf16x8 sp[TW][kParts], dp[TW][kParts];
+                    const bool have = v0 + 32 * b + 8 * g < a.VP;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) s8[e] = d8[e] = 0.f;
+                    for (int y = 0; y < TW; ++y) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            s8[y][e] = have ? s8[y][e] : 0.f;
+                            d8[y][e] = have ? d8[y][e] : 0.f;
+                            sds += s8[y][e] * d8[y][e];
                         }
-                        bf16x8 sp[kParts], dp[kParts];
-                        split<kParts, 8>(s8, sp);
-                        split<kParts, 8>(d8, dp);
+                        split<kParts, 8>(s8[y], sp[y]);
+                        split<kParts, 8>(d8[y], dp[y]);
+                    }
+                    load_states(b + 1 < blocks ? b + 1 : b);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) sds += s8[e] * d8[e];
+                    for (int r = 0; r < 2; ++r) {
+                        bf16x8 f[kParts], o[NPI];
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            mma(aq[y][r], o[r], sp);
-                            mma(ar[y][r], x[r], sp);
-                            mma(aw[y][r], u[r], dp);
-                        }
+                        for (int p = 0; p < kParts; ++p) f[p] = sh.rows.x[2 * rh + r][b][p][lane];
+#pragma unroll
+                        for (int p = 0; p < NPI; ++p) o[p] = sh.rows.o[2 * rh + r][b][p][lane];
+#pragma unroll
+                        for (int y = 0; y < TW; ++y) mma(ar[y][r], f, sp[y]);
+#pragma unroll
+                        for (int y = 0; y < TW; ++y) mma(aq[y][r], o, sp[y]);
+#pragma unroll
+                        for (int p = 0; p < kParts; ++p) f[p] = sh.rows.u[2 * rh + r][b][p][lane];
+#pragma unroll
+                        for (int y = 0; y < TW; ++y) mma(aw[y][r], f, dp[y]);
                     }
                 }
-                if (tri_on) {
+            }
+            if (tri_on) {
+#pragma unroll 1
+                for (int b = 0; b < blocks; ++b) {
                     bf16x8 xa[kParts], oa[NPI];
 #pragma unroll
                     for (int p = 0; p < kParts; ++p) xa[p] = sh.rows.x[rt][b][p][lane];
@@ -212,6 +197,22 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
                         mma(op[c], oa, ub);
                         mma(xp[c], xa, ub);
                     }
+                }
+            }
+        }
+        // K K^T, row tile rt against the column tiles 2 ch + 0, 1.
+        f32x4 kk[2] = {zero4(), zero4()};
+        if (tri_on) {
+#pragma unroll 1
+            for (int b = 0; b < KB; ++b) {
+                bf16x8 ka[NPI], kb[NPI];
+#pragma unroll
+                for (int p = 0; p < NPI; ++p) ka[p] = kr[((rt * KB + b) * NPI + p) * 64 + lane];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int p = 0; p < NPI; ++p) kb[p] = kr[(((2 * ch + c) * KB + b) * NPI + p) * 64 + lane];
+                    mma(kk[c], ka, kb);
                 }
             }
         }
@@ -260,87 +261,96 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
                 if (m == 0) rowsum[ch][i0 + r] = t;
             }
         }
-        // The products with the states: their shares of the gates' gradients, then their scales.
-        float kb0[2][4], kz[2][4], dg[2][4];
+        // The wave's columns of K and Q at its own tokens, as its accumulators have them.
+        float kd[TW][2][4], qd[TW][2][4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int x = 0; x < TW; ++x) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kd[x][e >> 2][e & 3] = qd[x][e >> 2][e & 3] = 0.f;
+            if (k_on)
+#pragma unroll
+                for (int p = NPI - 1; p >= 0; --p) {
+                    const int f = (((cg * TW + x) * 2 + rh) * NPI + p) * 64 + lane;
+                    const bf16x8 kv = kt_set[f], qv = qt_set[f];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        kd[x][e >> 2][e & 3] += float(kv[e]);
+                        qd[x][e >> 2][e & 3] += float(qv[e]);
+                    }
+                }
+        }
+        // The products with the states: their shares of the gates' gradients, then their scales.
+        auto reduce = [&](int which, int r, int i, float v) {
+            v = sum16(v);
+            if (m == 0) red[which][cg][acc_index(2 * rh + r, g) + i] = v;
+        };
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t0 = acc_index(2 * rh + r, g);
+            const f32x4 ga4 = *reinterpret_cast<const f32x4*>(&gamma[t0]), be4 = *reinterpret_cast<const f32x4*>(&beta[t0]),
+                        et4 = *reinterpret_cast<const f32x4*>(&eta[t0]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = acc_index(2 * rh + r, g) + i;
                 float b0 = 0.f, z = 0.f;
-                if (k_on) {
 #pragma unroll
-                    for (int x = 0; x < TW; ++x) {
-                        float k = 0.f;
-#pragma unroll
-                        for (int p = NPI - 1; p >= 0; --p) k += float(kt[x][rh][p][4 * r + i]);
-                        b0 += k * ar[x][r][i];
-                        z += k * aw[x][r][i];
-                        aq[x][r][i] *= a.scale * gamma[t];
-                        ar[x][r][i] *= -gamma[t] * beta[t];
-                        aw[x][r][i] *= eta[t];
-                    }
+                for (int x = 0; x < TW; ++x) {
+                    b0 += kd[x][r][i] * ar[x][r][i];
+                    z += kd[x][r][i] * aw[x][r][i];
                 }
-                kb0[r][i] = b0;
-                kz[r][i] = eta[t] * z;
+                reduce(1, r, i, b0);
+                reduce(2, r, i, et4[i] * z);
             }
+#pragma unroll
+            for (int x = 0; x < TW; ++x) {
+                aq[x][r] *= a.scale * ga4;
+                ar[x][r] *= -ga4 * be4;
+                aw[x][r] *= et4;
+            }
+        }
         __syncthreads();                                  // Phi and Psi are in LDS
         if (k_on) {
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                bf16x8 kt[TW][NPI], qt[TW][NPI];
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+                for (int x = 0; x < TW; ++x)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    bf16x8 f[kParts];
-                    if (b <= rh) {
-#pragma unroll
-                        for (int p = 0; p < kParts; ++p) f[p] = sh.tri.phi[2 * rh + r][b][p][lane];
-#pragma unroll
-                        for (int x = 0; x < TW; ++x) mma(aq[x][r], f, kt[x][b]);
-#pragma unroll
-                        for (int p = 0; p < kParts; ++p) f[p] = sh.tri.psi[2 * rh + r][b][p][lane];
-#pragma unroll
-                        for (int x = 0; x < TW; ++x) mma(ar[x][r], f, kt[x][b]);
+                    for (int p = 0; p < NPI; ++p) {
+                        kt[x][p] = kt_set[(((cg * TW + x) * 2 + b) * NPI + p) * 64 + lane];
+                        qt[x][p] = qt_set[(((cg * TW + x) * 2 + b) * NPI + p) * 64 + lane];
                     }
-                    if (b >= rh) {
+                auto times = [&](const bf16x8 (&f)[4][2][kParts][64], f32x4 (&acc)[TW][2], const bf16x8 (&k)[TW][NPI]) {
 #pragma unroll
-                        for (int p = 0; p < kParts; ++p) f[p] = sh.tri.phit[2 * rh + r][b][p][lane];
+                    for (int r = 0; r < 2; ++r) {
+                        bf16x8 v[kParts];
 #pragma unroll
-                        for (int x = 0; x < TW; ++x) mma(aw[x][r], f, qt[x][b]);
+                        for (int p = 0; p < kParts; ++p) v[p] = f[2 * rh + r][b][p][lane];
 #pragma unroll
-                        for (int p = 0; p < kParts; ++p) f[p] = sh.tri.psit[2 * rh + r][b][p][lane];
-#pragma unroll
-                        for (int x = 0; x < TW; ++x) mma(aw[x][r], f, kt[x][b]);
+                        for (int x = 0; x < TW; ++x) mma(acc[x][r], v, k[x]);
                     }
+                };
+                if (b <= rh) {
+                    times(sh.tri.phi, aq, kt);
+                    times(sh.tri.psi, ar, kt);
                 }
+                if (b >= rh) {
+                    times(sh.tri.phit, aw, qt);
+                    times(sh.tri.psit, aw, kt);
+                }
+            }
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float d = 0.f;
-                if (k_on) {
 #pragma unroll
-                    for (int x = 0; x < TW; ++x) {
-                        float k = 0.f, q = 0.f;
-#pragma unroll
-                        for (int p = NPI - 1; p >= 0; --p) {
-                            k += float(kt[x][rh][p][4 * r + i]);
-                            q += float(qt[x][rh][p][4 * r + i]);
-                        }
-                        d += q * aq[x][r][i] + k * (ar[x][r][i] - aw[x][r][i]);
-                        dq_all[x][r][i] += aq[x][r][i];
-                        dk_all[x][r][i] += ar[x][r][i] + aw[x][r][i];
-                    }
+                for (int x = 0; x < TW; ++x) {
+                    d += qd[x][r][i] * aq[x][r][i] + kd[x][r][i] * (ar[x][r][i] - aw[x][r][i]);
+                    dq_all[x][r][i] += aq[x][r][i];
+                    dk_all[x][r][i] += ar[x][r][i] + aw[x][r][i];
                 }
-                dg[r][i] = sum16(d);
-                kb0[r][i] = sum16(kb0[r][i]);
-                kz[r][i] = sum16(kz[r][i]);
-                if (m == 0) {
-                    const int t = acc_index(2 * rh + r, g) + i;
-                    red[0][cg][t] = dg[r][i];
-                    red[1][cg][t] = kb0[r][i];
-                    red[2][cg][t] = kz[r][i];
-                }
+                reduce(0, r, i, d);
             }
         __syncthreads();
         if (wave == 0) {
