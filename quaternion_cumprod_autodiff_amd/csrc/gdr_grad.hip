@@ -15,9 +15,16 @@ namespace {
 
 constexpr int kPiece = 128;     // columns of V at a time
 
+// Sum over the 16 lanes of a row, in every one of them.
+template <int CTRL>
+__device__ __forceinline__ float rotated(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
 __device__ __forceinline__ float sum16(float x) {
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) x += __shfl_xor(x, d, 64);
+    x += rotated<0x128>(x);      // by 8, 4, 2, 1 lanes within the row
+    x += rotated<0x124>(x);
+    x += rotated<0x122>(x);
+    x += rotated<0x121>(x);
     return x;
 }
 
@@ -41,7 +48,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
     };
     __shared__ __align__(16) Shared sh;
     __shared__ double cum[64];
-    __shared__ __align__(16) float gamma[64], eta[64], beta[64], xv[64], rowsum[2][64], red[3][4][64], dots[8];
+    __shared__ __align__(16) float gamma[64], eta[64], beta[64], xv[VB][64], rowsum[2][64], red[3][4][64], dots[8];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, g = lane >> 4;
     const int cg = wave >> 1, rh = wave & 1;
@@ -59,6 +66,22 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
     const bf16x8* qt_set = kr + set_frags(KB, NPI) * 64;
     const bf16x8* kt_set = qt_set + set_frags(KB, NPI) * 64;
 
+    // K K^T, row tile rt against the column tiles 2 ch + 0, 1.
+    f32x4 kk[2] = {zero4(), zero4()};
+    if (tri_on) {
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+            bf16x8 ka[NPI], kb[NPI];
+#pragma unroll
+            for (int p = 0; p < NPI; ++p) ka[p] = kr[((rt * KB + b) * NPI + p) * 64 + lane];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int p = 0; p < NPI; ++p) kb[p] = kr[(((2 * ch + c) * KB + b) * NPI + p) * 64 + lane];
+                mma(kk[c], ka, kb);
+            }
+        }
+    }
     f32x4 dq_all[TW][2], dk_all[TW][2];
 #pragma unroll
     for (int x = 0; x < TW; ++x)
@@ -80,104 +103,112 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
         for (int x = 0; x < TW; ++x)
 #pragma unroll
             for (int r = 0; r < 2; ++r) aq[x][r] = ar[x][r] = aw[x][r] = zero4();
-        float sds = 0.f, xdotv = 0.f;
+        float sds = 0.f;
         const int64_t piece = (hv * a.slots + slot) * int64_t(a.VP / 16) * 256;
         const float *s0 = a.save_s + piece * (2 * KB), *s1 = a.ds + piece * (2 * KB);
         const float *us = a.save_u + piece * 4, *xs = a.x + piece * 4;
 #pragma unroll 1
         for (int v0 = 0; v0 < a.V; v0 += kPiece) {
             if (v0) __syncthreads();                      // the piece before is done
-            // Thread (token, group of 16 columns): X, U, dO as fragments; X . v.
-            {
-                const int t = tid >> 3, c0 = (tid & 7) * 16;
-                const bool in = t < rem;
-                // Token t: tile 2 (t / 32) + (t / 4) % 2, row 4 ((t % 32) / 8) + t % 4.
-                const int tile = 2 * (t >> 5) + ((t >> 2) & 1), row = 4 * ((t & 31) >> 3) + (t & 3);
+            // A wave takes two (row tile, block of V) pairs: what a lane loads is what it holds of the fragment.  X . v on
+            // the way.
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int tile = wave >> 1, b = 2 * (wave & 1) + i, t = tile_index(tile, m), v = v0 + 32 * b + 8 * g;
+                const bool in = t < rem, have = v < a.VP;
                 const E* op_ = static_cast<const E*>(a.d_out) + ((token0 + (in ? t : 0)) * a.Hv + hv) * a.V;
                 const E* vp = static_cast<const E*>(a.v) + s.b * a.vs[0] + (s.t0 + int64_t(chunk) * kChunk + (in ? t : 0)) * a.vs[1] + int64_t(hv) * a.vs[2];
+                const int at = have ? (v >> 4) * 1024 + tile * 256 + m * 16 + (v & 15) : 0;
+                float x8[8], u8[8];
+                load_floats<8>(xs + at, x8);
+                load_floats<8>(us + at, u8);
+                const int left = in ? a.V - v : 0;
+                bf16x8 p3[kParts], o8[NPI], v8[NPI];
+                load_parts<DT>(op_ + v, left, a.vec_o, o8);
+                load_parts<DT>(vp + v, left, a.vec_v, v8);
+                float dot = 0.f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int c = c0 + 8 * i, v = v0 + c;
-                    float x8[8], u8[8];
-                    const bool have = v < a.VP;
-                    if (have) {
-                        const int at = (v >> 4) * 1024 + tile * 256 + row * 16 + (v & 15);
-                        load_floats<8>(xs + at, x8);
-                        load_floats<8>(us + at, u8);
-                    } else {
+                for (int e = 0; e < 8; ++e) {
+                    x8[e] = have ? x8[e] : 0.f;
+                    u8[e] = have ? u8[e] : 0.f;
+                    float ve = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x8[e] = u8[e] = 0.f;
-                    }
-                    bf16x8 xp8[kParts], up8[kParts], o8[NPI], v8[NPI];
-                    split<kParts, 8>(x8, xp8);
-                    split<kParts, 8>(u8, up8);
-                    const int left = in ? a.V - v : 0;
-                    load_parts<DT>(op_ + v, left, a.vec_o, o8);
-                    load_parts<DT>(vp + v, left, a.vec_v, v8);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float ve = 0.f;
-#pragma unroll
-                        for (int p = NPI - 1; p >= 0; --p) ve += float(v8[p][e]);
-                        xdotv += x8[e] * ve;
-                    }
-                    const int at = 16 * ((c & 31) >> 3) + row;
-#pragma unroll
-                    for (int p = 0; p < kParts; ++p) {
-                        sh.rows.x[tile][c >> 5][p][at] = xp8[p];
-                        sh.rows.u[tile][c >> 5][p][at] = up8[p];
-                    }
-#pragma unroll
-                    for (int p = 0; p < NPI; ++p) sh.rows.o[tile][c >> 5][p][at] = o8[p];
+                    for (int p = NPI - 1; p >= 0; --p) ve += float(v8[p][e]);
+                    dot += x8[e] * ve;
                 }
+                split<kParts, 8>(x8, p3);
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) sh.rows.x[tile][b][p][lane] = p3[p];
+                split<kParts, 8>(u8, p3);
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) sh.rows.u[tile][b][p][lane] = p3[p];
+#pragma unroll
+                for (int p = 0; p < NPI; ++p) sh.rows.o[tile][b][p][lane] = o8[p];
+                dot += __shfl_xor(dot, 16, 64);
+                dot += __shfl_xor(dot, 32, 64);
+                if (g == 0) xv[b][t] = (v0 ? xv[b][t] : 0.f) + dot;
             }
+            // The states' operands are loaded one block of V ahead.
+            float s8[TW][8], d8[TW][8];
+            auto load_states = [&](int b) {
+                const int v = v0 + 32 * b + 8 * g;
+                const bool have = v < a.VP && k_on;
+#pragma unroll
+                for (int y = 0; y < TW; ++y) {
+                    const int at = have ? (v >> 4) * (2 * KB * 256) + (cg * TW + y) * 256 + m * 16 + (v & 15) : 0;
+                    load_floats<8>(s0 + at, s8[y]);
+                    load_floats<8>(s1 + at, d8[y]);
+                }
+            };
+            load_states(0);
             __syncthreads();
             const int blocks = a.V - v0 >= kPiece ? VB : (a.V - v0 + 31) / 32;
             if (k_on) {
-                // The states' operands are loaded one block of V ahead.
-                float s8[TW][8], d8[TW][8];
-                auto load_states = [&](int b) {
-                    const int v = v0 + 32 * b + 8 * g;
-                    const bool have = v < a.VP;
-#pragma unroll
-                    for (int y = 0; y < TW; ++y) {
-                        const int at = have ? (v >> 4) * (2 * KB * 256) + (cg * TW + y) * 256 + m * 16 + (v & 15) : 0;
-                        load_floats<8>(s0 + at, s8[y]);
-                        load_floats<8>(s1 + at, d8[y]);
-                    }
-                };
-                load_states(0);
 #pragma unroll 1
                 for (int b = 0; b < blocks; ++b) {
-                    bf16x8 sp[TW][kParts], dp[TW][kParts];
                     const bool have = v0 + 32 * b + 8 * g < a.VP;
+                    // One state at a time: both states' parts together do not fit the registers.
+                    auto take = [&](float (&x)[TW][8], bf16x8 (&p)[TW][kParts]) {
 #pragma unroll
-                    for (int y = 0; y < TW; ++y) {
+                        for (int y = 0; y < TW; ++y) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            s8[y][e] = have ? s8[y][e] : 0.f;
-                            d8[y][e] = have ? d8[y][e] : 0.f;
-                            sds += s8[y][e] * d8[y][e];
+                            for (int e = 0; e < 8; ++e) x[y][e] = have ? x[y][e] : 0.f;
+                            split<kParts, 8>(x[y], p[y]);
                         }
-                        split<kParts, 8>(s8[y], sp[y]);
-                        split<kParts, 8>(d8[y], dp[y]);
+                    };
+                    {
+                        bf16x8 sp[TW][kParts];
+                        take(s8, sp);
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            bf16x8 f[kParts], o[NPI];
+#pragma unroll
+                            for (int p = 0; p < kParts; ++p) f[p] = sh.rows.x[2 * rh + r][b][p][lane];
+#pragma unroll
+                            for (int p = 0; p < NPI; ++p) o[p] = sh.rows.o[2 * rh + r][b][p][lane];
+#pragma unroll
+                            for (int y = 0; y < TW; ++y) mma(ar[y][r], f, sp[y]);
+#pragma unroll
+                            for (int y = 0; y < TW; ++y) mma(aq[y][r], o, sp[y]);
+                        }
                     }
-                    load_states(b + 1 < blocks ? b + 1 : b);
+                    __builtin_amdgcn_sched_barrier(0);
+                    {
+                        bf16x8 dp[TW][kParts];
+                        take(d8, dp);
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        bf16x8 f[kParts], o[NPI];
+                        for (int y = 0; y < TW; ++y)
 #pragma unroll
-                        for (int p = 0; p < kParts; ++p) f[p] = sh.rows.x[2 * rh + r][b][p][lane];
+                            for (int e = 0; e < 8; ++e) sds += s8[y][e] * d8[y][e];
+                        load_states(b + 1 < blocks ? b + 1 : b);
 #pragma unroll
-                        for (int p = 0; p < NPI; ++p) o[p] = sh.rows.o[2 * rh + r][b][p][lane];
+                        for (int r = 0; r < 2; ++r) {
+                            bf16x8 f[kParts];
 #pragma unroll
-                        for (int y = 0; y < TW; ++y) mma(ar[y][r], f, sp[y]);
+                            for (int p = 0; p < kParts; ++p) f[p] = sh.rows.u[2 * rh + r][b][p][lane];
 #pragma unroll
-                        for (int y = 0; y < TW; ++y) mma(aq[y][r], o, sp[y]);
-#pragma unroll
-                        for (int p = 0; p < kParts; ++p) f[p] = sh.rows.u[2 * rh + r][b][p][lane];
-#pragma unroll
-                        for (int y = 0; y < TW; ++y) mma(aw[y][r], f, dp[y]);
+                            for (int y = 0; y < TW; ++y) mma(aw[y][r], f, dp[y]);
+                        }
                     }
                 }
             }
@@ -200,26 +231,19 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
                 }
             }
         }
-        // K K^T, row tile rt against the column tiles 2 ch + 0, 1.
-        f32x4 kk[2] = {zero4(), zero4()};
-        if (tri_on) {
-#pragma unroll 1
-            for (int b = 0; b < KB; ++b) {
-                bf16x8 ka[NPI], kb[NPI];
+        // The wave's columns of K and Q, transposed: [tile][block of tokens].
+        bf16x8 kt[TW][2][NPI], qt[TW][2][NPI];
 #pragma unroll
-                for (int p = 0; p < NPI; ++p) ka[p] = kr[((rt * KB + b) * NPI + p) * 64 + lane];
+        for (int x = 0; x < TW; ++x)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int p = 0; p < NPI; ++p) kb[p] = kr[(((2 * ch + c) * KB + b) * NPI + p) * 64 + lane];
-                    mma(kk[c], ka, kb);
+                for (int p = 0; p < NPI; ++p) {
+                    const int f = (((k_on ? cg * TW + x : 0) * 2 + b) * NPI + p) * 64 + lane;
+                    kt[x][b][p] = kt_set[f];
+                    qt[x][b][p] = qt_set[f];
                 }
-            }
-        }
         __syncthreads();                                  // X, U, dO are done; Phi and Psi take their place
-#pragma unroll
-        for (int d = 1; d < 8; d *= 2) xdotv += __shfl_xor(xdotv, d, 64);
-        if ((tid & 7) == 0) xv[tid >> 3] = xdotv;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) sds += __shfl_xor(sds, d, 64);
         if (lane == 0) dots[wave] = rh == 0 ? sds : 0.f;
@@ -261,97 +285,81 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
                 if (m == 0) rowsum[ch][i0 + r] = t;
             }
         }
-        // The wave's columns of K and Q at its own tokens, as its accumulators have them.
-        float kd[TW][2][4], qd[TW][2][4];
+        // The products with the states: their shares of the gates' gradients, then their scales.
+        float kd[TW][2][4], qd[TW][2][4];                 // the wave's columns of K and Q at its own tokens
 #pragma unroll
-        for (int x = 0; x < TW; ++x) {
+        for (int x = 0; x < TW; ++x)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) kd[x][e >> 2][e & 3] = qd[x][e >> 2][e & 3] = 0.f;
-            if (k_on)
+            for (int e = 0; e < 8; ++e) {
+                float k = 0.f, q = 0.f;
 #pragma unroll
                 for (int p = NPI - 1; p >= 0; --p) {
-                    const int f = (((cg * TW + x) * 2 + rh) * NPI + p) * 64 + lane;
-                    const bf16x8 kv = kt_set[f], qv = qt_set[f];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        kd[x][e >> 2][e & 3] += float(kv[e]);
-                        qd[x][e >> 2][e & 3] += float(qv[e]);
-                    }
+                    k += float(rh ? kt[x][1][p][e] : kt[x][0][p][e]);
+                    q += float(rh ? qt[x][1][p][e] : qt[x][0][p][e]);
                 }
-        }
-        // The products with the states: their shares of the gates' gradients, then their scales.
-        auto reduce = [&](int which, int r, int i, float v) {
-            v = sum16(v);
-            if (m == 0) red[which][cg][acc_index(2 * rh + r, g) + i] = v;
+                kd[x][e >> 2][e & 3] = k;
+                qd[x][e >> 2][e & 3] = q;
+            }
+        // Sums over the wave's columns of K, per token.
+        auto reduce = [&](int which, int r, f32x4 v) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = sum16(v[i]);
+            if (m == 0) *reinterpret_cast<f32x4*>(&red[which][cg][acc_index(2 * rh + r, g)]) = v;
         };
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int t0 = acc_index(2 * rh + r, g);
             const f32x4 ga4 = *reinterpret_cast<const f32x4*>(&gamma[t0]), be4 = *reinterpret_cast<const f32x4*>(&beta[t0]),
                         et4 = *reinterpret_cast<const f32x4*>(&eta[t0]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float b0 = 0.f, z = 0.f;
-#pragma unroll
-                for (int x = 0; x < TW; ++x) {
-                    b0 += kd[x][r][i] * ar[x][r][i];
-                    z += kd[x][r][i] * aw[x][r][i];
-                }
-                reduce(1, r, i, b0);
-                reduce(2, r, i, et4[i] * z);
-            }
+            f32x4 b0 = zero4(), z = zero4();
 #pragma unroll
             for (int x = 0; x < TW; ++x) {
+                const f32x4 k = {kd[x][r][0], kd[x][r][1], kd[x][r][2], kd[x][r][3]};
+                b0 += k * ar[x][r];
+                z += k * aw[x][r];
                 aq[x][r] *= a.scale * ga4;
                 ar[x][r] *= -ga4 * be4;
                 aw[x][r] *= et4;
             }
+            reduce(1, r, b0);
+            reduce(2, r, et4 * z);
         }
         __syncthreads();                                  // Phi and Psi are in LDS
         if (k_on) {
-#pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-                bf16x8 kt[TW][NPI], qt[TW][NPI];
+            auto times = [&](const bf16x8 (&f)[4][2][kParts][64], int b, f32x4 (&acc)[TW][2], const bf16x8 (&k)[TW][2][NPI]) {
 #pragma unroll
-                for (int x = 0; x < TW; ++x)
+                for (int r = 0; r < 2; ++r) {
+                    bf16x8 v[kParts];
 #pragma unroll
-                    for (int p = 0; p < NPI; ++p) {
-                        kt[x][p] = kt_set[(((cg * TW + x) * 2 + b) * NPI + p) * 64 + lane];
-                        qt[x][p] = qt_set[(((cg * TW + x) * 2 + b) * NPI + p) * 64 + lane];
-                    }
-                auto times = [&](const bf16x8 (&f)[4][2][kParts][64], f32x4 (&acc)[TW][2], const bf16x8 (&k)[TW][NPI]) {
+                    for (int p = 0; p < kParts; ++p) v[p] = f[2 * rh + r][b][p][lane];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        bf16x8 v[kParts];
-#pragma unroll
-                        for (int p = 0; p < kParts; ++p) v[p] = f[2 * rh + r][b][p][lane];
-#pragma unroll
-                        for (int x = 0; x < TW; ++x) mma(acc[x][r], v, k[x]);
-                    }
-                };
-                if (b <= rh) {
-                    times(sh.tri.phi, aq, kt);
-                    times(sh.tri.psi, ar, kt);
+                    for (int x = 0; x < TW; ++x) mma(acc[x][r], v, k[x][b]);
                 }
-                if (b >= rh) {
-                    times(sh.tri.phit, aw, qt);
-                    times(sh.tri.psit, aw, kt);
-                }
+            };
+            times(sh.tri.phi, 0, aq, kt);                 // blocks of tokens at or before the wave's
+            times(sh.tri.psi, 0, ar, kt);
+            times(sh.tri.phit, 1, aw, qt);                // at or behind them
+            times(sh.tri.psit, 1, aw, kt);
+            if (rh) {
+                times(sh.tri.phi, 1, aq, kt);
+                times(sh.tri.psi, 1, ar, kt);
+            } else {
+                times(sh.tri.phit, 0, aw, qt);
+                times(sh.tri.psit, 0, aw, kt);
             }
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < 2; ++r) {
+            f32x4 d = zero4();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float d = 0.f;
-#pragma unroll
-                for (int x = 0; x < TW; ++x) {
-                    d += qd[x][r][i] * aq[x][r][i] + kd[x][r][i] * (ar[x][r][i] - aw[x][r][i]);
-                    dq_all[x][r][i] += aq[x][r][i];
-                    dk_all[x][r][i] += ar[x][r][i] + aw[x][r][i];
-                }
-                reduce(0, r, i, d);
+            for (int x = 0; x < TW; ++x) {
+                const f32x4 k = {kd[x][r][0], kd[x][r][1], kd[x][r][2], kd[x][r][3]}, q = {qd[x][r][0], qd[x][r][1], qd[x][r][2], qd[x][r][3]};
+                d += q * aq[x][r] + k * (ar[x][r] - aw[x][r]);
+                dq_all[x][r] += aq[x][r];
+                dk_all[x][r] += ar[x][r] + aw[x][r];
             }
+            reduce(0, r, d);
+        }
         __syncthreads();
         if (wave == 0) {
             float d = 0.f, b0 = 0.f, z = 0.f;
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
                 // dg is a multiple of exp(g): nothing where that is 0, whatever rounding leaves of the sum.
                 const float decay = expf(float(cum[lane] - (lane ? cum[lane - 1] : 0.0)));
                 if (a.dg) a.dg[at] = decay > 0.f || decay != decay ? float(sum) : 0.f;
-                if (a.db) a.db[at] = xv[lane] - gamma[lane] * b0 - (rowsum[0][lane] + rowsum[1][lane]);
+                if (a.db) a.db[at] = (xv[0][lane] + xv[1][lane] + xv[2][lane] + xv[3][lane]) - gamma[lane] * b0 - (rowsum[0][lane] + rowsum[1][lane]);
             }
         }
     }
