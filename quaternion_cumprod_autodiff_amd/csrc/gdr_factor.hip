@@ -21,11 +21,29 @@ template <int DT, int KB, bool BWD>
 __global__ void __launch_bounds__(256) gdr_factor_kernel(GdrArgs a) {
     using E = typename Storage<DT>::type;
     constexpr int NPI = parts_of(DT);
-    __shared__ __align__(16) bf16x8 kf[4][KB][NPI][64];
-    __shared__ __align__(16) bf16x8 qf[BWD ? 4 : 1][BWD ? KB : 1][BWD ? NPI : 1][64];
-    __shared__ __align__(16) float ma[64 * kRow], mp[64 * kRow], mx[64 * kRow];
+    // The inverse takes K's place once K K^T and the transposed fragments are made.
+    struct Rows {
+        bf16x8 k[4][KB][NPI][64];
+    };
+    union Shared {
+        __device__ Shared() {}
+        Rows rows;
+        float inverse[64 * kRow];
+    };
+    __shared__ __align__(16) Shared sh;
+    // Q's rows, for its transposed fragments (backward), then A and P.
+    union Matrices {
+        __device__ Matrices() {}
+        bf16x8 q[BWD ? 4 : 1][BWD ? KB : 1][BWD ? NPI : 1][64];
+        float ap[2][64 * kRow];
+    };
+    __shared__ __align__(16) Matrices mat;
+    auto& qf = mat.q;
+    float *ma = mat.ap[0], *mp = mat.ap[1];
+    auto& kf = sh.rows.k;
+    float* mx = sh.inverse;
     __shared__ double cum[64];
-    __shared__ float beta[64];
+    __shared__ __align__(16) float beta[64];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 15, g = lane >> 4;
     const int hv = int(blockIdx.x % a.Hv);
     const int64_t slot = blockIdx.x / a.Hv;
@@ -42,8 +60,14 @@ __global__ void __launch_bounds__(256) gdr_factor_kernel(GdrArgs a) {
     bf16x8* q_set = k_rows + set_frags(KB, NPI) * 64;
     bf16x8* k_cols = q_set + set_frags(KB, NPI) * 64;
 
-    // Row tile w of K and Q.
-    bf16x8 qa[KB][NPI];
+    // Everything that comes from far away first: the gates (wave 0), row tile w of K and Q.
+    const int64_t gate_at = (s.b * a.T + t0 + (lane < rem ? lane : 0)) * a.Hv + hv;
+    float g_raw = 0.f, b_raw = 0.f;
+    if (w == 0) {
+        g_raw = a.g[gate_at];
+        b_raw = a.b[gate_at];
+    }
+    bf16x8 qa[KB][NPI], ka[KB][NPI];
     {
         const int t = tile_index(w, m);
         const bool in = t < rem;
@@ -52,27 +76,15 @@ __global__ void __launch_bounds__(256) gdr_factor_kernel(GdrArgs a) {
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
             const int c = 32 * b + 8 * g, left = in ? a.K - c : 0;
-            bf16x8 kx[NPI];
-            load_parts<DT>(kp + c, left, a.vec_qk, kx);
+            load_parts<DT>(kp + c, left, a.vec_qk, ka[b]);
             load_parts<DT>(qp + c, left, a.vec_qk, qa[b]);
-#pragma unroll
-            for (int p = 0; p < NPI; ++p) {
-                kf[w][b][p][lane] = kx[p];
-                if constexpr (BWD) qf[w][b][p][lane] = qa[b][p];
-                if (lead) {
-                    k_rows[((w * KB + b) * NPI + p) * 64 + lane] = kx[p];
-                    if constexpr (!BWD) q_set[((w * KB + b) * NPI + p) * 64 + lane] = qa[b][p];
-                }
-            }
         }
     }
     // Gates: decays cumulated in 64 bits.  -2000 stands for every decay below it: exp() of it is 0, and sums with it
     // leave the differences behind it exact to 1e-11.
     if (w == 0) {
         const bool in = lane < rem;
-        const int64_t at = (s.b * a.T + t0 + (in ? lane : 0)) * a.Hv + hv;
-        const float gt = in ? a.g[at] : 0.f;
-        const float bt = in ? a.b[at] : 0.f;
+        const float gt = in ? g_raw : 0.f, bt = in ? b_raw : 0.f;
         double c = gt < -2000.f ? -2000.0 : double(gt);
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
@@ -88,32 +100,72 @@ __global__ void __launch_bounds__(256) gdr_factor_kernel(GdrArgs a) {
         ga->beta[lane] = bt;
         ga->cum[lane] = c;
     }
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+        for (int p = 0; p < NPI; ++p) {
+            kf[w][b][p][lane] = ka[b][p];
+            if constexpr (BWD) qf[w][b][p][lane] = qa[b][p];
+        }
     __syncthreads();
-    // K K^T and Q K^T, the rows of tile w, against the tokens of no later block of 32.
-    {
-        bf16x8 ka[KB][NPI];
+    // K (backward: Q too) transposed: tiles of K, blocks of tokens.
+    if (lead) {
+        const __bf16* ks = reinterpret_cast<const __bf16*>(&kf);
+        const __bf16* qs = reinterpret_cast<const __bf16*>(&qf);
+        for (int f = w; f < 4 * KB; f += 4) {
+            const int tile = f >> 1, b = f & 1;
+            const int c = tile_index(tile, m);
+#pragma unroll
+            for (int p = 0; p < NPI; ++p) {
+                bf16x8 kx, qx;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    // Token 32 b + 8 g + e: row tile 2 b + e / 4, row 4 g + e % 4; element c: block c / 32, lane group (c % 32) / 8.
+                    const int at = (((2 * b + (e >> 2)) * KB + (c >> 5)) * NPI + p) * 512 + (16 * ((c & 31) >> 3) + 4 * g + (e & 3)) * 8 + (c & 7);
+                    kx[e] = ks[at];
+                    if constexpr (BWD) qx[e] = qs[at];
+                }
+                k_cols[(f * NPI + p) * 64 + lane] = kx;
+                if constexpr (BWD) q_set[(f * NPI + p) * 64 + lane] = qx;
+            }
+        }
+    }
+    if constexpr (BWD) __syncthreads();      // A and P take Q's place
+    if (lead) {
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
-            for (int p = 0; p < NPI; ++p) ka[b][p] = kf[w][b][p][lane];
-        const int i0 = acc_index(w, g);
-        for (int c = 0; c < 2 * (w >> 1) + 2; ++c) {
-            f32x4 kk = zero4(), qk = zero4();
-#pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                bf16x8 kb[NPI];
-#pragma unroll
-                for (int p = 0; p < NPI; ++p) kb[p] = kf[c][b][p][lane];
-                mma(kk, ka[b], kb);
-                mma(qk, qa[b], kb);
+            for (int p = 0; p < NPI; ++p) {
+                k_rows[((w * KB + b) * NPI + p) * 64 + lane] = ka[b][p];
+                if constexpr (!BWD) q_set[((w * KB + b) * NPI + p) * 64 + lane] = qa[b][p];
             }
-            const int j = tile_index(c, m);
+    }
+    // K K^T and Q K^T, the rows of tile w, against the tokens of no later block of 32, two tiles at a time.
+    {
+        const int i0 = acc_index(w, g);
+        for (int c = 0; c < 2 * (w >> 1) + 2; c += 2) {
+            f32x4 kk[2] = {zero4(), zero4()}, qk[2] = {zero4(), zero4()};
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = i0 + r;
-                const float d = i >= j ? expf(float(cum[i] - cum[j])) : 0.f;
-                ma[i * kRow + j] = i > j ? beta[i] * d * kk[r] : 0.f;
-                mp[i * kRow + j] = i >= j ? d * qk[r] : 0.f;
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    bf16x8 kb[NPI];
+#pragma unroll
+                    for (int p = 0; p < NPI; ++p) kb[p] = kf[c + y][b][p][lane];
+                    mma(kk[y], ka[b], kb);
+                    mma(qk[y], qa[b], kb);
+                }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int j = tile_index(c + y, m);
+                const double cj = cum[j];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = i0 + r;
+                    const float d = expf(float(cum[i] - cj));
+                    ma[i * kRow + j] = i > j ? beta[i] * d * kk[y][r] : 0.f;
+                    mp[i * kRow + j] = i >= j ? d * qk[y][r] : 0.f;
+                }
             }
         }
     }
@@ -169,12 +221,26 @@ __global__ void __launch_bounds__(256) gdr_factor_kernel(GdrArgs a) {
         for (int b = 0; b < 2; ++b) {
             if (!tri_has<BWD>(w, b)) continue;
             float t[8], p[8];
+            const int c0 = 32 * b + 8 * g;
+            if constexpr (BWD) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = 32 * b + 8 * g + e;
-                const int i = BWD ? c : row, j = BWD ? row : c;
-                t[e] = i >= j ? mx[i * kRow + j] * (BWD ? 1.f : beta[j]) : 0.f;
-                p[e] = i >= j ? mp[i * kRow + j] : 0.f;
+                for (int e = 0; e < 8; ++e) {
+                    t[e] = mx[(c0 + e) * kRow + row];
+                    p[e] = mp[(c0 + e) * kRow + row];
+                }
+            } else {
+                float bt[8];
+                load_floats<8>(&mx[row * kRow + c0], t);
+                load_floats<8>(&mp[row * kRow + c0], p);
+                load_floats<8>(&beta[c0], bt);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] *= bt[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {      // what lies across the diagonal was never written
+                const bool in = BWD ? c0 + e >= row : row >= c0 + e;
+                t[e] = in ? t[e] : 0.f;
+                p[e] = in ? p[e] : 0.f;
             }
             bf16x8 ts[kParts], ps[kParts];
             split<kParts, 8>(t, ts);
@@ -184,28 +250,6 @@ __global__ void __launch_bounds__(256) gdr_factor_kernel(GdrArgs a) {
             for (int n = 0; n < kParts; ++n) {
                 tf[(f + n) * 64 + lane] = ts[n];
                 pf[(f + n) * 64 + lane] = ps[n];
-            }
-        }
-    }
-    // K (backward: Q too) transposed: tiles of K, blocks of tokens.
-    if (lead) {
-        const __bf16* ks = reinterpret_cast<const __bf16*>(kf);
-        const __bf16* qs = reinterpret_cast<const __bf16*>(qf);
-        for (int f = w; f < 4 * KB; f += 4) {
-            const int tile = f >> 1, b = f & 1;
-            const int c = tile_index(tile, m);
-#pragma unroll
-            for (int p = 0; p < NPI; ++p) {
-                bf16x8 kx, qx;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // Token 32 b + 8 g + e: row tile 2 b + e / 4, row 4 g + e % 4; element c: block c / 32, lane group (c % 32) / 8.
-                    const int at = (((2 * b + (e >> 2)) * KB + (c >> 5)) * NPI + p) * 512 + (16 * ((c & 31) >> 3) + 4 * g + (e & 3)) * 8 + (c & 7);
-                    kx[e] = ks[at];
-                    if constexpr (BWD) qx[e] = qs[at];
-                }
-                k_cols[(f * NPI + p) * 64 + lane] = kx;
-                if constexpr (BWD) q_set[(f * NPI + p) * 64 + lane] = qx;
             }
         }
     }
