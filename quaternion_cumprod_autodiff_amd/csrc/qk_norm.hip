@@ -35,9 +35,9 @@ struct QknArgs {
     const void *gq, *gk;           // VJP: cotangents
     float *pq, *pk;                // VJP: partial sums [blocks][D] (null: no gradient of that weight)
     int64_t qs[3], ks[3];
-    int64_t T, rows_q, rows_k, D, R, P;
+    int64_t T, tokens, D, R, P;
     int hq, hk, blocks_q, blocks_k;
-    int pos64, interleaved;
+    int pos64, interleaved, small;
     float eps, inv_size;
 };
 
@@ -66,8 +66,13 @@ __device__ __forceinline__ Slot<W> slot_of(int p, int D, int R, bool interleaved
     return s;
 }
 
-template <int W, class E>
+template <int W, bool FULL, class E>
 __device__ __forceinline__ void load_pair(const E* row, const Slot<W>& s, float (&a)[W], float (&b)[W]) {
+    if constexpr (FULL) {
+        load_floats<W>(row + s.a, a);
+        load_floats<W>(row + s.b, b);
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < W; ++i) a[i] = b[i] = 0.f;
     if (s.has_a) load_floats<W>(row + s.a, a);
@@ -104,30 +109,26 @@ __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
-__device__ __forceinline__ int64_t table_row(const QknArgs& a, int64_t token) {
-    if (!a.pos) return token % a.T;
-    const int64_t p = a.pos64 ? static_cast<const int64_t*>(a.pos)[token] : int64_t(static_cast<const int32_t*>(a.pos)[token]);
-    return p;
+__device__ __forceinline__ int64_t table_row(const QknArgs& a, int64_t token, int64_t t) {
+    if (!a.pos) return t;
+    return a.pos64 ? static_cast<const int64_t*>(a.pos)[token] : int64_t(static_cast<const int32_t*>(a.pos)[token]);
 }
 
-struct Row {
-    int64_t offset, token;
-};
-
-__device__ __forceinline__ Row row_of(int64_t i, int heads, const int64_t (&st)[3], int64_t T) {
-    const int64_t token = i / heads;
-    const int64_t h = i - token * heads, b = token / T, t = token - b * T;
-    return {b * st[0] + t * st[1] + h * st[2], token};
+// n / d: in 32 bits where everything fits, as it nearly always does (a 64-bit
+// division is some hundred instructions).
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d, bool small) {
+    return small ? int64_t(uint32_t(n) / uint32_t(d)) : n / d;
 }
 
-// One head per group of G lanes; S slots of W pairs per lane.  DT: storage
-// type; BWD: the VJP.
-template <int DT, int W, int G, int S, bool BWD>
+// One head per group of G lanes; S slots of W pairs per lane.  A group takes HC
+// heads of one token in a row: they share the token's angles and its place.
+// DT: storage type; BWD: the VJP; FULL: every lane has its elements (D = 2 W G S)
+// and every group its HC heads, so that nothing is checked.
+template <int DT, int W, int G, int S, int HC, bool BWD, bool FULL>
 __global__ void __launch_bounds__(kThreads) qkn_kernel(QknArgs a) {
     using E = typename Storage<DT>::type;
     const int lane = threadIdx.x % G, group = threadIdx.x / G;
     const bool is_q = int(blockIdx.x) < a.blocks_q;
-    const int64_t rows = is_q ? a.rows_q : a.rows_k;
     const int heads = is_q ? a.hq : a.hk;
     const int block = is_q ? blockIdx.x : blockIdx.x - a.blocks_q, blocks = is_q ? a.blocks_q : a.blocks_k;
     const E* x = static_cast<const E*>(is_q ? a.q : a.k);
@@ -135,90 +136,124 @@ __global__ void __launch_bounds__(kThreads) qkn_kernel(QknArgs a) {
     E* y = static_cast<E*>(is_q ? a.yq : a.yk);
     const E* g = static_cast<const E*>(is_q ? a.gq : a.gk);
     float* part = is_q ? a.pq : a.pk;
+    const int64_t sb = is_q ? a.qs[0] : a.ks[0], st = is_q ? a.qs[1] : a.ks[1], sh = is_q ? a.qs[2] : a.ks[2];
     const int D = int(a.D), R = int(a.R);
-    const bool inter = a.interleaved != 0;
+    const bool inter = a.interleaved != 0, small = a.small != 0;
     Slot<W> slot[S];
-    float wa[S][W], wb[S][W], sa[S][W], sb[S][W];
+    float wa[S][W], wb[S][W], sa[S][W], sb_[S][W];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         slot[s] = slot_of<W>(lane + G * s, D, R, inter);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             wa[s][i] = wb[s][i] = 1.f;
-            sa[s][i] = sb[s][i] = 0.f;
+            sa[s][i] = sb_[s][i] = 0.f;
         }
-        if (wt) load_pair<W>(wt, slot[s], wa[s], wb[s]);
+        if (wt) load_pair<W, FULL>(wt, slot[s], wa[s], wb[s]);
     }
     constexpr int kGroups = kThreads / G;
-    for (int64_t i = int64_t(block) * kGroups + group; i < rows; i += int64_t(blocks) * kGroups) {
-        const Row at = is_q ? row_of(i, heads, a.qs, a.T) : row_of(i, heads, a.ks, a.T);
-        float xa[S][W], xb[S][W], ga[S][W], gb[S][W];
-        float sum = 0.f;
+    const int per = (heads + HC - 1) / HC;
+    const int64_t units = a.tokens * per;
+    for (int64_t u = int64_t(block) * kGroups + group; u < units; u += int64_t(blocks) * kGroups) {
+        const int64_t token = per == 1 ? u : quotient(u, per, small);
+        const int h0 = int(u - token * per) * HC;
+        const int64_t b = quotient(token, a.T, small), t = token - b * a.T;
+        const E* px = x + b * sb + t * st + h0 * sh;
+        const int64_t dense = (token * heads + h0) * D;
+        // The position first: its wait then covers nothing else, and the angles are on their way with the heads.
+        int64_t row = R ? table_row(a, token, t) : 0;
+        constexpr int kHeld = BWD ? 1 : HC;      // heads in registers; two in the VJP cost half its waves, 134 us for 108
+        float xa[kHeld][S][W], xb[kHeld][S][W], ga[BWD ? kHeld : 1][S][W], gb[BWD ? kHeld : 1][S][W], c[S][W], sn[S][W];
+        auto load_head = [&](int k) {
+            if (FULL || HC == 1 || h0 + k < heads)
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            load_pair<W>(x + at.offset, slot[s], xa[s], xb[s]);
-            if constexpr (BWD) load_pair<W>(g + i * D, slot[s], ga[s], gb[s]);
+                for (int s = 0; s < S; ++s) {
+                    load_pair<W, FULL>(px + k * sh, slot[s], xa[BWD ? 0 : k][s], xb[BWD ? 0 : k][s]);
+                    if constexpr (BWD) load_pair<W, FULL>(g + dense + k * D, slot[s], ga[0][s], gb[0][s]);
+                }
+        };
+        if constexpr (!BWD) {
+#pragma unroll
+            for (int k = 0; k < HC; ++k) load_head(k);
         }
-        int64_t row = 0;
         float poison = 0.f;
         if (R) {
-            row = table_row(a, at.token);
             if (row < 0 || row >= a.P) {
                 row = 0;
                 poison = __builtin_nanf("");
             }
-        }
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int j = 0; j < W; ++j) sum += xa[s][j] * xa[s][j] + xb[s][j] * xb[s][j];
-        sum = group_sum<G>(sum);
-        const float r = 1.f / sqrtf(sum * a.inv_size + a.eps) + poison;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            float c[W], sn[W];
-            if (slot[s].turns) {
-                const int64_t t = row * (R / 2) + int64_t(lane + G * s) * W;
-                load_floats<W>(a.cos + t, c);
-                load_floats<W>(a.sin + t, sn);
-            }
-            if constexpr (!BWD) {
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    xa[s][j] = xa[s][j] * r * wa[s][j];
-                    xb[s][j] = xb[s][j] * r * wb[s][j];
-                }
-                if (slot[s].turns) turn<W>(xa[s], xb[s], c, sn, inter, 1.f);
-                if (slot[s].has_a) store_floats<W>(y + i * D + slot[s].a, xa[s]);
-                if (slot[s].has_b) store_floats<W>(y + i * D + slot[s].b, xb[s]);
-            } else if (slot[s].turns) {
-                turn<W>(ga[s], gb[s], c, sn, inter, -1.f);
-            }
-        }
-        if constexpr (BWD) {
-            float dot = 0.f;
 #pragma unroll
             for (int s = 0; s < S; ++s)
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    sa[s][j] += ga[s][j] * (xa[s][j] * r);
-                    sb[s][j] += gb[s][j] * (xb[s][j] * r);
-                    ga[s][j] *= wa[s][j];
-                    gb[s][j] *= wb[s][j];
-                    dot += ga[s][j] * xa[s][j] + gb[s][j] * xb[s][j];
+                if (slot[s].turns) {
+                    const int64_t at = row * (R / 2) + int64_t(lane + G * s) * W;
+                    load_floats<W>(a.cos + at, c[s]);
+                    load_floats<W>(a.sin + at, sn[s]);
                 }
-            dot = group_sum<G>(dot);
-            const float f = r * r * r * dot * a.inv_size;
-            if (y) {
+        }
+        if constexpr (!BWD) {
+#pragma unroll
+            for (int k = 0; k < HC; ++k) {
+                if (!FULL && HC > 1 && h0 + k >= heads) break;
+                float sum = 0.f;
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+#pragma unroll
+                    for (int j = 0; j < W; ++j) sum += xa[k][s][j] * xa[k][s][j] + xb[k][s][j] * xb[k][s][j];
+                sum = group_sum<G>(sum);
+                const float r = 1.f / sqrtf(sum * a.inv_size + a.eps) + poison;
 #pragma unroll
                 for (int s = 0; s < S; ++s) {
 #pragma unroll
                     for (int j = 0; j < W; ++j) {
-                        xa[s][j] = r * ga[s][j] - xa[s][j] * f;
-                        xb[s][j] = r * gb[s][j] - xb[s][j] * f;
+                        xa[k][s][j] = xa[k][s][j] * r * wa[s][j];
+                        xb[k][s][j] = xb[k][s][j] * r * wb[s][j];
                     }
-                    if (slot[s].has_a) store_floats<W>(y + i * D + slot[s].a, xa[s]);
-                    if (slot[s].has_b) store_floats<W>(y + i * D + slot[s].b, xb[s]);
+                    if (slot[s].turns) turn<W>(xa[k][s], xb[k][s], c[s], sn[s], inter, 1.f);
+                    E* py = y + dense + k * D;
+                    if (FULL || slot[s].has_a) store_floats<W>(py + slot[s].a, xa[k][s]);
+                    if (FULL || slot[s].has_b) store_floats<W>(py + slot[s].b, xb[k][s]);
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < HC; ++k) {
+                if (!FULL && HC > 1 && h0 + k >= heads) break;
+                load_head(k);
+                float (&pa)[S][W] = xa[0], (&pb)[S][W] = xb[0], (&pg)[S][W] = ga[0], (&ph)[S][W] = gb[0];
+                float sum = 0.f;
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+#pragma unroll
+                    for (int j = 0; j < W; ++j) sum += pa[s][j] * pa[s][j] + pb[s][j] * pb[s][j];
+                sum = group_sum<G>(sum);
+                const float r = 1.f / sqrtf(sum * a.inv_size + a.eps) + poison;
+                float dot = 0.f;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    if (slot[s].turns) turn<W>(pg[s], ph[s], c[s], sn[s], inter, -1.f);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        sa[s][j] += pg[s][j] * (pa[s][j] * r);
+                        sb_[s][j] += ph[s][j] * (pb[s][j] * r);
+                        pg[s][j] *= wa[s][j];
+                        ph[s][j] *= wb[s][j];
+                        dot += pg[s][j] * pa[s][j] + ph[s][j] * pb[s][j];
+                    }
+                }
+                dot = group_sum<G>(dot);
+                const float f = r * r * r * dot * a.inv_size;
+                if (y) {
+                    E* py = y + dense + k * D;
+#pragma unroll
+                    for (int s = 0; s < S; ++s) {
+#pragma unroll
+                        for (int j = 0; j < W; ++j) {
+                            pa[s][j] = r * pg[s][j] - pa[s][j] * f;
+                            pb[s][j] = r * ph[s][j] - pb[s][j] * f;
+                        }
+                        if (FULL || slot[s].has_a) store_floats<W>(py + slot[s].a, pa[s]);
+                        if (FULL || slot[s].has_b) store_floats<W>(py + slot[s].b, pb[s]);
+                    }
                 }
             }
         }
@@ -234,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) qkn_kernel(QknArgs a) {
 #pragma unroll
                 for (int m = G; m < 64; m *= 2) {
                     sa[s][j] += __shfl_xor(sa[s][j], m, 64);
-                    sb[s][j] += __shfl_xor(sb[s][j], m, 64);
+                    sb_[s][j] += __shfl_xor(sb_[s][j], m, 64);
                 }
             }
         const int wave = threadIdx.x / 64;
@@ -244,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) qkn_kernel(QknArgs a) {
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
                     red[wave][(s * W + j) * 2 * G + lane] = sa[s][j];
-                    red[wave][((s * W + j) * 2 + 1) * G + lane] = sb[s][j];
+                    red[wave][((s * W + j) * 2 + 1) * G + lane] = sb_[s][j];
                 }
         }
         __syncthreads();
@@ -265,25 +300,29 @@ __global__ void __launch_bounds__(kThreads) qkn_kernel(QknArgs a) {
     }
 }
 
-// dw[d] = sum of the blocks' partial sums, 16 columns and 16 runs of blocks to
+// dw[d] = sum of the blocks' partial sums, 16 columns and 64 runs of blocks to
 // a block of threads, the runs joined in order.
+constexpr int kRuns = 64;
+
 template <int DT>
-__global__ void __launch_bounds__(kThreads) qkn_weight_kernel(const float* pq, const float* pk, int nq, int nk, void* dq, void* dk, int D) {
+__global__ void __launch_bounds__(16 * kRuns) qkn_weight_kernel(const float* pq, const float* pk, int nq, int nk, void* dq, void* dk, int D) {
     using E = typename Storage<DT>::type;
     const float* part = blockIdx.y ? pk : pq;
     const int n = blockIdx.y ? nk : nq;
     E* out = static_cast<E*>(blockIdx.y ? dk : dq);
     if (!out) return;
     const int col = blockIdx.x * 16 + threadIdx.x % 16, run = threadIdx.x / 16;
-    __shared__ float red[16][17];
+    __shared__ float red[kRuns][17];
     float s = 0.f;
     if (col < D)
-        for (int i = run; i < n; i += 16) s += part[int64_t(i) * D + col];
+#pragma unroll 4
+        for (int i = run; i < n; i += kRuns) s += part[int64_t(i) * D + col];
     red[run][threadIdx.x % 16] = s;
     __syncthreads();
     if (threadIdx.x < 16 && col < D) {
         float t = 0.f;
-        for (int i = 0; i < 16; ++i) t += red[i][threadIdx.x];
+#pragma unroll 8
+        for (int i = 0; i < kRuns; ++i) t += red[i][threadIdx.x];
         out[col] = E(t);
     }
 }
@@ -296,9 +335,12 @@ int pow2_at_least(int64_t n) {
 
 struct Shape {
     bool wide;          // W = 8
-    int g, s;           // lanes per head, slots per lane
+    int g, s, hc;       // lanes per head, slots per lane, heads in a row
 };
 
+// Four heads of a token in a row where that still leaves 8 waves for each of
+// 1024 SIMDs, one otherwise: measured on 16384 tokens of 40 heads of 128,
+// KEEP_NORM_FOUR us against KEEP_NORM_ONE; on 64 tokens of 18 heads the launch is all there is.
 Shape shape_of(const qkn_dims& d, bool wide) {
     Shape sh;
     sh.wide = wide;
@@ -306,12 +348,13 @@ Shape shape_of(const qkn_dims& d, bool wide) {
     sh.g = wide ? pow2_at_least(slots) : 64;
     if (wide && sh.g < 4) sh.g = 4;
     sh.s = wide ? 1 : pow2_at_least((slots + 63) / 64);
+    sh.hc = d.B * d.T * (d.Hq + d.Hk) * sh.g >= 4 * 64 * 8 * 1024 ? 4 : 1;
     return sh;
 }
 
-// Blocks for so many heads; past 2^20 blocks the blocks loop.
-int64_t blocks_for(int64_t rows, int g) {
-    const int64_t n = (rows * g + kThreads - 1) / kThreads;
+// Blocks for so many tokens' heads; past 2^20 blocks the blocks loop.
+int64_t blocks_for(int64_t tokens, int64_t heads, const Shape& sh) {
+    const int64_t n = (tokens * ((heads + sh.hc - 1) / sh.hc) * sh.g + kThreads - 1) / kThreads;
     return n < (int64_t(1) << 20) ? n : int64_t(1) << 20;
 }
 
@@ -322,22 +365,30 @@ hipError_t by_dtype(int dt, F&& f) {
     return f(std::integral_constant<int, 2>{});
 }
 
+template <int DT, int HC, bool BWD, bool FULL>
+const void* wide_kernel(int g) {
+    return g == 4    ? reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 4, 1, HC, BWD, FULL>)
+           : g == 8  ? reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 8, 1, HC, BWD, FULL>)
+           : g == 16 ? reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 16, 1, HC, BWD, FULL>)
+           : g == 32 ? reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 32, 1, HC, BWD, FULL>)
+                     : reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 64, 1, HC, BWD, FULL>);
+}
+
+template <int DT, int HC, bool BWD>
+const void* kernel_of(const Shape& sh, bool full) {
+    if (sh.wide) return full ? wide_kernel<DT, HC, BWD, true>(sh.g) : wide_kernel<DT, HC, BWD, false>(sh.g);
+    return sh.s == 1   ? reinterpret_cast<const void*>(&qkn_kernel<DT, 1, 64, 1, HC, BWD, false>)
+           : sh.s == 2 ? reinterpret_cast<const void*>(&qkn_kernel<DT, 1, 64, 2, HC, BWD, false>)
+           : sh.s == 4 ? reinterpret_cast<const void*>(&qkn_kernel<DT, 1, 64, 4, HC, BWD, false>)
+                       : reinterpret_cast<const void*>(&qkn_kernel<DT, 1, 64, 8, HC, BWD, false>);
+}
+
 template <bool BWD>
-hipError_t launch(int dt, Shape sh, const QknArgs& a, hipStream_t st) {
+hipError_t launch(int dt, const Shape& sh, const QknArgs& a, hipStream_t st) {
     return by_dtype(dt, [&](auto t) {
         constexpr int DT = decltype(t)::value;
-        const void* fn;
-        if (sh.wide)
-            fn = sh.g == 4    ? reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 4, 1, BWD>)
-                 : sh.g == 8  ? reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 8, 1, BWD>)
-                 : sh.g == 16 ? reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 16, 1, BWD>)
-                 : sh.g == 32 ? reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 32, 1, BWD>)
-                              : reinterpret_cast<const void*>(&qkn_kernel<DT, 8, 64, 1, BWD>);
-        else
-            fn = sh.s == 1   ? reinterpret_cast<const void*>(&qkn_kernel<DT, 1, 64, 1, BWD>)
-                 : sh.s == 2 ? reinterpret_cast<const void*>(&qkn_kernel<DT, 1, 64, 2, BWD>)
-                 : sh.s == 4 ? reinterpret_cast<const void*>(&qkn_kernel<DT, 1, 64, 4, BWD>)
-                             : reinterpret_cast<const void*>(&qkn_kernel<DT, 1, 64, 8, BWD>);
+        const bool full = sh.wide && a.D == 16 * sh.g && a.hq % sh.hc == 0 && a.hk % sh.hc == 0;
+        const void* fn = sh.hc == 4 ? kernel_of<DT, 4, BWD>(sh, full) : kernel_of<DT, 1, BWD>(sh, full);
         QknArgs args = a;
         void* params[] = {&args};
         return hipLaunchKernel(fn, dim3(unsigned(a.blocks_q + a.blocks_k)), dim3(kThreads), params, 0, st);
@@ -402,9 +453,10 @@ Common common(const qkn_dims* d, const void* q, const void* k, const void* wq, c
         a.qs[i] = d->q_stride[i];
         a.ks[i] = d->k_stride[i];
     }
-    a.T = d->T; a.rows_q = tokens * d->Hq; a.rows_k = tokens * d->Hk; a.D = d->D; a.R = d->R; a.P = d->P;
+    a.T = d->T; a.tokens = tokens; a.D = d->D; a.R = d->R; a.P = d->P;
     a.hq = int(d->Hq); a.hk = int(d->Hk);
     a.pos64 = d->positions64; a.interleaved = d->interleaved;
+    a.small = tokens * (d->Hq + d->Hk) < (int64_t(1) << 31);
     a.eps = d->eps;
     a.inv_size = d->kind == QKN_RMS ? 1.f / float(d->D) : 1.f;
     return c;
@@ -433,8 +485,8 @@ int qkn_fwd(const qkn_dims* dims, const void* query, const void* key, const void
     if (qc::outputs_overlap(sp, 2, 9)) return QC_ERR_ALIAS;
     c.a.yq = query_out;
     c.a.yk = key_out;
-    c.a.blocks_q = int(qc::blocks_for(c.a.rows_q, c.sh.g));
-    c.a.blocks_k = int(qc::blocks_for(c.a.rows_k, c.sh.g));
+    c.a.blocks_q = int(qc::blocks_for(c.a.tokens, c.a.hq, c.sh));
+    c.a.blocks_k = int(qc::blocks_for(c.a.tokens, c.a.hk, c.sh));
     if (c.a.blocks_q + c.a.blocks_k == 0) return QC_OK;
     const hipError_t err = qc::launch<false>(dims->dtype, c.sh, c.a, static_cast<hipStream_t>(stream));
     return err == hipSuccess ? QC_OK : qc::record_hip_error(err);
@@ -476,13 +528,13 @@ int qkn_bwd(const qkn_dims* dims, const void* query, const void* key, const void
                                {d_query_out, size_t(c.q_out)}, {d_key_out, size_t(c.k_out)}};
     if (qc::outputs_overlap(sp, 5, 14)) return QC_ERR_ALIAS;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    auto blocks = [&](bool any, const void* dw, int64_t rows) -> int {
+    auto blocks = [&](bool any, const void* dw, int64_t heads) -> int {
         if (!any) return 0;
-        const int64_t n = qc::blocks_for(rows, c.sh.g), most = qc::partials(rows);
+        const int64_t n = qc::blocks_for(c.a.tokens, heads, c.sh), most = qc::partials(c.a.tokens * heads);
         return int(dw && n > most ? most : n);
     };
-    c.a.blocks_q = blocks(any_q, d_query_weight, c.a.rows_q);
-    c.a.blocks_k = blocks(any_k, d_key_weight, c.a.rows_k);
+    c.a.blocks_q = blocks(any_q, d_query_weight, c.a.hq);
+    c.a.blocks_k = blocks(any_k, d_key_weight, c.a.hk);
     c.a.yq = d_query; c.a.yk = d_key; c.a.gq = d_query_out; c.a.gk = d_key_out;
     c.a.pq = d_query_weight ? static_cast<float*>(workspace) : nullptr;
     c.a.pk = d_key_weight ? static_cast<float*>(workspace) + (d_query_weight ? int64_t(c.a.blocks_q) * dims->D : 0) : nullptr;
@@ -495,7 +547,7 @@ int qkn_bwd(const qkn_dims* dims, const void* query, const void* key, const void
             void *dq = d_query_weight, *dk = d_key_weight;
             void* params[] = {&pq, &pk, &nq, &nk, &dq, &dk, &D};
             return hipLaunchKernel(reinterpret_cast<const void*>(&qc::qkn_weight_kernel<decltype(t)::value>),
-                                   dim3(unsigned((D + 15) / 16), 2), dim3(qc::kThreads), params, 0, st);
+                                   dim3(unsigned((D + 15) / 16), 2), dim3(16 * qc::kRuns), params, 0, st);
         });
     }
     return err == hipSuccess ? QC_OK : qc::record_hip_error(err);
