@@ -31,6 +31,32 @@ struct StepArgs {
     float scale;
 };
 
+// N consecutive elements as they lie in memory: taken apart where they are used,
+// so that the next token's are on their way during this one's work.  VEC: pieces
+// of up to 16 bytes, each inside or outside `left` as a whole.
+template <class E, int N, bool VEC>
+struct Held {
+    static constexpr int kPer = N * sizeof(E) >= 16 ? 16 / sizeof(E) : N;
+    typedef E Vec __attribute__((ext_vector_type(kPer)));
+    Vec x[N / kPer];
+
+    __device__ __forceinline__ void load(const E* p, int left) {
+#pragma unroll
+        for (int i = 0; i < N / kPer; ++i) {
+            if constexpr (VEC) {
+                x[i] = i * kPer < left ? reinterpret_cast<const Vec*>(p)[i] : Vec(E(0.f));
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) x[i][j] = i * kPer + j < left ? p[i * kPer + j] : E(0.f);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&y)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = float(x[i / kPer][i % kPer]);
+    }
+};
+
 // Sum over the eight row groups: lanes l, l ^ 8, l ^ 16, l ^ 32.
 __device__ __forceinline__ float rows_sum(float x) {
     x += __shfl_xor(x, 8, 64);
@@ -39,28 +65,48 @@ __device__ __forceinline__ float rows_sum(float x) {
     return x;
 }
 
-// NR: rows per lane.  VEC: K = 8 NR, V a multiple of 4 and every row on 16
-// bytes; otherwise elements are read one by one and checked against K and V.
-template <int DT, int NR, bool VEC>
+// NR: rows per lane.  VEC: K a multiple of 8, V of 4 and every row on 16 bytes;
+// otherwise elements are read one by one.  MANY: more than one token, the next
+// one's q, k, v loaded ahead.  STREAM: the states pass by the caches.
+template <int DT, int NR, bool VEC, bool MANY, bool STREAM>
 __global__ void __launch_bounds__(64) gdr_step_kernel(StepArgs a) {
     using E = typename Storage<DT>::type;
     const int lane = threadIdx.x, c0 = lane % 8 * 4, r0 = lane / 8 * NR;
-    const int tile = int(blockIdx.x % a.tiles);
-    const int64_t rest = blockIdx.x / a.tiles;
+    // The tiles of a state on one XCD (block % 8), next to each other in time.
+    const int tile = int(blockIdx.x / 8 % a.tiles);
+    const int64_t rest = blockIdx.x / (8 * a.tiles) * 8 + blockIdx.x % 8;
+    if (rest >= a.N * a.Hv) return;
     const int h = int(rest % a.Hv);
     const int64_t n = rest / a.Hv;
     const int col = tile * kCols + c0;
-    int64_t slot = n;
-    bool run = true;
-    if (a.slots) {
-        slot = a.slots[n];
+    const int64_t slot = a.slots ? a.slots[n] : n;
+    bool run = slot >= 0 && slot < a.n_slots;
+    E* out = static_cast<E*>(a.out) + (n * a.T * a.Hv + h) * int64_t(a.V) + col;
+    const int64_t out_step = int64_t(a.Hv) * a.V;
+    // The state is on its way while the earlier rows' slots are looked through.
+    float* st = a.state + (run ? slot : 0) * a.slot_stride + int64_t(h) * a.K * a.V;
+    float s[NR][4];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        if constexpr (VEC) {
+            f32x4 x = {0.f, 0.f, 0.f, 0.f};
+            if (run && col < a.V && r0 + i < a.K) {
+                const f32x4* p = reinterpret_cast<const f32x4*>(st + int64_t(r0 + i) * a.V + col);
+                if constexpr (STREAM) x = __builtin_nontemporal_load(p);
+                else x = *p;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = x[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = run && r0 + i < a.K && col + j < a.V ? st[int64_t(r0 + i) * a.V + col + j] : 0.f;
+        }
+    }
+    if (a.slots && run) {
         bool twin = false;
         for (int64_t m = lane; m < n; m += 64) twin |= a.slots[m] == slot;
         run = __ballot(twin) == 0;
     }
-    run = run && slot >= 0 && slot < a.n_slots;
-    E* out = static_cast<E*>(a.out) + (n * a.T * a.Hv + h) * int64_t(a.V) + col;
-    const int64_t out_step = int64_t(a.Hv) * a.V;
     if (!run) {
         if (lane < 8)
             for (int64_t t = 0; t < a.T; ++t)
@@ -68,39 +114,34 @@ __global__ void __launch_bounds__(64) gdr_step_kernel(StepArgs a) {
                     if (col + j < a.V) out[t * out_step + j] = E(0.f);
         return;
     }
-    float* st = a.state + slot * a.slot_stride + int64_t(h) * a.K * a.V;
-    float s[NR][4];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        if constexpr (VEC) {
-            const f32x4 x = col < a.V ? *reinterpret_cast<const f32x4*>(st + int64_t(r0 + i) * a.V + col) : f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = x[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = r0 + i < a.K && col + j < a.V ? st[int64_t(r0 + i) * a.V + col + j] : 0.f;
-        }
-    }
     const E* q = static_cast<const E*>(a.q) + n * a.qs[0] + (h / a.group) * a.qs[2] + r0;
     const E* k = static_cast<const E*>(a.k) + n * a.ks[0] + (h / a.group) * a.ks[2] + r0;
     const E* v = static_cast<const E*>(a.v) + n * a.vs[0] + h * a.vs[2] + col;
     const float* g = a.g + n * a.T * a.Hv + h;
     const float* b = a.b + n * a.T * a.Hv + h;
+    Held<E, NR, VEC> k_next, q_next;
+    Held<E, 4, false> v_next;
+    float g_next, b_next;
+    auto load = [&] {
+        k_next.load(k, a.K - r0);
+        q_next.load(q, a.K - r0);
+        v_next.load(v, a.V - col);
+        g_next = *g;
+        b_next = *b;
+        q += a.qs[1];
+        k += a.ks[1];
+        v += a.vs[1];
+        g += a.Hv;
+        b += a.Hv;
+    };
+    load();
     for (int64_t t = 0; t < a.T; ++t) {
         float kr[NR], qr[NR], vr[4];
-        if constexpr (VEC) {
-            load_floats<NR>(k, kr);
-            load_floats<NR>(q, qr);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                kr[i] = r0 + i < a.K ? float(k[i]) : 0.f;
-                qr[i] = r0 + i < a.K ? float(q[i]) : 0.f;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) vr[j] = col + j < a.V ? float(v[j]) : 0.f;
-        const float decay = expf(*g), beta = *b;
+        k_next.get(kr);
+        q_next.get(qr);
+        v_next.get(vr);
+        const float decay = expf(g_next), beta = b_next;
+        if (MANY && t + 1 < a.T) load();
         float p[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f}, kq = 0.f;
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
@@ -128,16 +169,16 @@ __global__ void __launch_bounds__(64) gdr_step_kernel(StepArgs a) {
                 if (col + j < a.V) out[j] = E(o[j]);
         }
         out += out_step;
-        q += a.qs[1];
-        k += a.ks[1];
-        v += a.vs[1];
-        g += a.Hv;
-        b += a.Hv;
     }
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         if constexpr (VEC) {
-            if (col < a.V) *reinterpret_cast<f32x4*>(st + int64_t(r0 + i) * a.V + col) = f32x4{s[i][0], s[i][1], s[i][2], s[i][3]};
+            if (col < a.V && r0 + i < a.K) {
+                f32x4* p = reinterpret_cast<f32x4*>(st + int64_t(r0 + i) * a.V + col);
+                const f32x4 x = {s[i][0], s[i][1], s[i][2], s[i][3]};
+                if constexpr (STREAM) __builtin_nontemporal_store(x, p);
+                else *p = x;
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -146,12 +187,26 @@ __global__ void __launch_bounds__(64) gdr_step_kernel(StepArgs a) {
     }
 }
 
-template <int DT>
-const void* step_kernel(int nr, bool vec) {
-    if (nr == 4) return vec ? reinterpret_cast<const void*>(&gdr_step_kernel<DT, 4, true>) : reinterpret_cast<const void*>(&gdr_step_kernel<DT, 4, false>);
-    if (nr == 8) return vec ? reinterpret_cast<const void*>(&gdr_step_kernel<DT, 8, true>) : reinterpret_cast<const void*>(&gdr_step_kernel<DT, 8, false>);
-    return vec ? reinterpret_cast<const void*>(&gdr_step_kernel<DT, 16, true>) : reinterpret_cast<const void*>(&gdr_step_kernel<DT, 16, false>);
+template <int DT, bool VEC, bool MANY, bool STREAM>
+const void* step_kernel(int nr) {
+    return nr == 4   ? reinterpret_cast<const void*>(&gdr_step_kernel<DT, 4, VEC, MANY, STREAM>)
+           : nr == 8 ? reinterpret_cast<const void*>(&gdr_step_kernel<DT, 8, VEC, MANY, STREAM>)
+                     : reinterpret_cast<const void*>(&gdr_step_kernel<DT, 16, VEC, MANY, STREAM>);
 }
+
+template <int DT>
+const void* step_kernel(int nr, bool vec, bool many, bool stream) {
+    if (!vec) return many ? step_kernel<DT, false, true, false>(nr) : step_kernel<DT, false, false, false>(nr);
+    if (stream) return many ? step_kernel<DT, true, true, true>(nr) : step_kernel<DT, true, false, true>(nr);
+    return many ? step_kernel<DT, true, true, false>(nr) : step_kernel<DT, true, false, false>(nr);
+}
+
+// From how many bytes of states on a call streams them.  A model calls for one
+// layer after another, so that a layer's states are gone from the 256 MB cache
+// when its turn comes again; three pools in turn: 48 MB 20.3 us (19.4 streamed),
+// 134 MB 60.7 (53.6), 268 MB 112 (104), 805 MB 168 (156).  One pool alone stays
+// there up to its size: 100 MB 37 us (42), 268 MB 92 (103).
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
 }  // namespace
 }  // namespace qc
@@ -169,7 +224,7 @@ extern "C" int gdr_step(const gdr_dims* dims, const void* query, const void* key
     const int64_t extent = n_slots ? qc::count(n_slots - 1, slot_stride) : 0;
     if (extent < 0 || (!slots && n_slots < d.N)) return QC_ERR_SHAPE;
     const int tiles = int((d.V + qc::kCols - 1) / qc::kCols);
-    const int64_t blocks = qc::count(d.N, d.Hv * tiles);
+    const int64_t heads = qc::count(d.N, d.Hv), blocks = heads < 0 ? -1 : qc::count((heads + 7) / 8 * 8, tiles);
     if (blocks < 0 || blocks > (int64_t(1) << 25)) return QC_ERR_SHAPE;   // 64 threads each, below 2^32 in all
     const size_t e = qc::dtype_bytes(d.dtype);
     for (const void* p : {query, key, value, static_cast<const void*>(out)})
@@ -196,9 +251,10 @@ extern "C" int gdr_step(const gdr_dims* dims, const void* query, const void* key
     a.Hv = int(d.Hv); a.group = int(d.Hv / d.Hk); a.K = int(d.K); a.V = int(d.V); a.tiles = tiles;
     a.scale = d.scale;
     const int nr = d.K <= 32 ? 4 : d.K <= 64 ? 8 : 16;
-    const bool vec = d.K == 8 * nr && d.V % 4 == 0 && qc::aligned_to(state, 16) && slot_stride % 4 == 0 &&
+    const bool vec = d.K % 8 == 0 && d.V % 4 == 0 && qc::aligned_to(state, 16) && slot_stride % 4 == 0 &&
                      qc::rows_on_16(query, d.q_stride, e) && qc::rows_on_16(key, d.k_stride, e);
-    const void* fn = d.dtype == GDR_F32 ? qc::step_kernel<0>(nr, vec) : d.dtype == GDR_BF16 ? qc::step_kernel<1>(nr, vec) : qc::step_kernel<2>(nr, vec);
+    const bool far = heads * d.K * d.V * 4 >= qc::kStreamBytes;
+    const void* fn = d.dtype == GDR_F32 ? qc::step_kernel<0>(nr, vec, d.T > 1, far) : d.dtype == GDR_BF16 ? qc::step_kernel<1>(nr, vec, d.T > 1, far) : qc::step_kernel<2>(nr, vec, d.T > 1, far);
     void* params[] = {&a};
     const hipError_t err = hipLaunchKernel(fn, dim3(unsigned(blocks)), dim3(64), params, 0, static_cast<hipStream_t>(stream));
     return err == hipSuccess ? QC_OK : qc::record_hip_error(err);

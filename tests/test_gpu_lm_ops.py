@@ -117,6 +117,18 @@ def test_step_with_nothing_to_do():
     assert torch.equal(state, kept)
 
 
+def test_step_on_many_large_states():
+    # 136 MB of states, which pass by the caches, against the same rows in two calls of half as many
+    args = step_inputs(70, 2, 4, 32, 128, 120, 70, BF16, seed=6)
+    q, k, v, g, b, state, slots = args
+    twin = state.clone()
+    out = gated_delta_step(q, k, v, g, b, state, slots=slots)
+    for rows in (slice(0, 35), slice(35, 70)):
+        part = gated_delta_step(q[rows], k[rows], v[rows], g[rows], b[rows], twin, slots=slots[rows])
+        assert torch.equal(part, out[rows])
+    assert torch.equal(state, twin)
+
+
 def test_step_on_another_stream_and_in_a_graph():
     size = (5, 1, 2, 4, 128, 128, 8)
     q, k, v, g, b, state, slots = step_inputs(*size, BF16, seed=4)
@@ -218,6 +230,32 @@ def test_norm(size, interleaved, dtype):
     print(f"[norm {size} {interleaved} {dtype}]", flush=True)
     check_norm(*norm_inputs(*size, dtype, True, seed=sum(size)), interleaved=interleaved)
     check_norm(*norm_inputs(*size, dtype, False, seed=sum(size)), kind="l2", eps=1e-3, interleaved=interleaved)
+
+
+@pytest.mark.parametrize("size", [(1, 8300, 3, 2, 6, 4, 50), (2, 16500, 8, 4, 128, 128, 300), (1, 33000, 7, 2, 128, 64, 300)], ids=str)
+def test_norm_of_many_heads_equals_its_parts(size):
+    """Calls so large that a group takes four heads in a row, against slices of their tokens small enough for one each."""
+    print(f"[norm {size}]", flush=True)
+    q, k, wq, wk, cos, sin, pos = norm_inputs(*size, BF16, True, seed=3)
+    whole = [t.detach().requires_grad_() for t in (q, k, wq, wk)]
+    out = qk_norm_rotate(*whole, cos, sin, pos)
+    cot = [torch.randn_like(t) for t in out]
+    grads = torch.autograd.grad(out, whole, cot)
+    half = 2.0 ** -8
+    sums = [torch.zeros(size[4], dtype=torch.float64, device=DEV) for _ in range(2)]
+    step = 700
+    for t0 in range(0, size[1], step):
+        cut = slice(t0, t0 + step)
+        leaves = [t[:, cut].detach().float().requires_grad_() for t in (q, k)] + [t.detach().float().requires_grad_() for t in (wq, wk)]
+        part = qk_norm_rotate(*leaves, cos, sin, pos[:, cut].contiguous())
+        pg = torch.autograd.grad(part, leaves, [c[:, cut].float() for c in cot])
+        for a, b in zip((*out, *grads[:2]), (*part, *pg[:2])):         # the part in float32: the whole rounds once more
+            a, b = a[:, cut].double(), b.double()
+            assert ((a - b).abs() <= half * b.abs() + 1e-5 * b.abs().max()).all()
+        for s, g in zip(sums, pg[2:]):
+            s += g.double()
+    for a, b in zip(grads[2:], sums):
+        assert ((a.double() - b).abs() <= half * b.abs() + 1e-5 * b.abs().max()).all()
 
 
 def test_norm_of_strided_views_positions_of_64_bits_and_none():
