@@ -338,18 +338,20 @@ struct Shape {
     int g, s, hc;       // lanes per head, slots per lane, heads in a row
 };
 
-// Forward: four heads of a token in a row where that still leaves 8 waves for
-// each of 1024 SIMDs (16384 tokens of 40 heads of 128: 67 us, 77 one by one),
-// one otherwise.  VJP: always one (with its forward on 4 x 4096 tokens of
-// 32 heads: 140 us, 172 for four, whose registers leave fewer waves).
-Shape shape_of(const qkn_dims& d, bool wide, bool vjp) {
+// Four heads of a token in a row where that still leaves 8 waves for each of
+// 1024 SIMDs, one otherwise: they share the angles, the position and the
+// divisions.  Forward, 16384 tokens of 40 heads of 128: 60 us, 79 one by one;
+// 4 x 4096 tokens of 32 heads of 128: 48 us (61), and their VJP 82 us (88).
+// Below the bound the blocks no longer fill the card: 512 tokens of 40 heads
+// are 320 blocks one by one and would be 80.
+Shape shape_of(const qkn_dims& d, bool wide) {
     Shape sh;
     sh.wide = wide;
     const int64_t slots = (d.D + (wide ? 15 : 1)) / (wide ? 16 : 2);
     sh.g = wide ? pow2_at_least(slots) : 64;
     if (wide && sh.g < 4) sh.g = 4;
     sh.s = wide ? 1 : pow2_at_least((slots + 63) / 64);
-    sh.hc = !vjp && d.B * d.T * (d.Hq + d.Hk) * sh.g >= 4 * 64 * 8 * 1024 ? 4 : 1;
+    sh.hc = d.B * d.T * (d.Hq + d.Hk) * sh.g >= 4 * 64 * 8 * 1024 ? 4 : 1;
     return sh;
 }
 
@@ -389,10 +391,7 @@ hipError_t launch(int dt, const Shape& sh, const QknArgs& a, hipStream_t st) {
     return by_dtype(dt, [&](auto t) {
         constexpr int DT = decltype(t)::value;
         const bool full = sh.wide && a.D == 16 * sh.g && a.hq % sh.hc == 0 && a.hk % sh.hc == 0;
-        const void* fn = nullptr;
-        if constexpr (!BWD)
-            if (sh.hc == 4) fn = kernel_of<DT, 4, BWD>(sh, full);
-        if (!fn) fn = kernel_of<DT, 1, BWD>(sh, full);
+        const void* fn = sh.hc == 4 ? kernel_of<DT, 4, BWD>(sh, full) : kernel_of<DT, 1, BWD>(sh, full);
         QknArgs args = a;
         void* params[] = {&args};
         return hipLaunchKernel(fn, dim3(unsigned(a.blocks_q + a.blocks_k)), dim3(kThreads), params, 0, st);
@@ -418,7 +417,7 @@ struct Common {
     int64_t q_bytes, k_bytes, q_out, k_out;
 };
 
-Common common(const qkn_dims* d, bool vjp, const void* q, const void* k, const void* wq, const void* wk, const float* cos, const float* sin,
+Common common(const qkn_dims* d, const void* q, const void* k, const void* wq, const void* wk, const float* cos, const float* sin,
               const void* pos) {
     Common c{};
     c.rc = check_dims(d);
@@ -450,7 +449,7 @@ Common common(const qkn_dims* d, bool vjp, const void* q, const void* k, const v
     const bool wide = d->D % 8 == 0 && d->R % 16 == 0 && rows_on_16(q, d->q_stride, e) && rows_on_16(k, d->k_stride, e) &&
                       (!wq || aligned_to(wq, 16)) && (!wk || aligned_to(wk, 16)) &&
                       (!d->R || (aligned_to(cos, 16) && aligned_to(sin, 16)));
-    c.sh = shape_of(*d, wide, vjp);
+    c.sh = shape_of(*d, wide);
     QknArgs& a = c.a;
     a.q = q; a.k = k; a.wq = wq; a.wk = wk; a.cos = cos; a.sin = sin; a.pos = pos;
     for (int i = 0; i < 3; ++i) {
@@ -475,13 +474,13 @@ extern "C" {
 
 int qkn_fwd(const qkn_dims* dims, const void* query, const void* key, const void* query_weight, const void* key_weight,
             const float* cos, const float* sin, const void* positions, void* query_out, void* key_out, void* stream) {
-    qc::Common c = qc::common(dims, false, query, key, query_weight, key_weight, cos, sin, positions);
+    qc::Common c = qc::common(dims, query, key, query_weight, key_weight, cos, sin, positions);
     if (c.rc != QC_OK) return c.rc;
     if ((c.q_out && !query_out) || (c.k_out && !key_out)) return QC_ERR_NULL;
     const size_t e = qc::dtype_bytes(dims->dtype), w = size_t(dims->D) * e, table = size_t(dims->P * (dims->R / 2)) * 4;
     if ((query_out && !qc::aligned_to(query_out, c.sh.wide ? 16 : e)) || (key_out && !qc::aligned_to(key_out, c.sh.wide ? 16 : e))) {
         if ((query_out && !qc::aligned_to(query_out, e)) || (key_out && !qc::aligned_to(key_out, e))) return QC_ERR_ALIGN;
-        c.sh = qc::shape_of(*dims, false, false);
+        c.sh = qc::shape_of(*dims, false);
     }
     const qc::ByteSpan sp[] = {{query_out, size_t(c.q_out)}, {key_out, size_t(c.k_out)}, {query, size_t(c.q_bytes)},
                                {key, size_t(c.k_bytes)}, {query_weight, w}, {key_weight, w}, {cos, table}, {sin, table},
@@ -506,7 +505,7 @@ int qkn_bwd(const qkn_dims* dims, const void* query, const void* key, const void
             const float* cos, const float* sin, const void* positions, const void* d_query_out, const void* d_key_out,
             void* d_query, void* d_key, void* d_query_weight, void* d_key_weight, void* workspace,
             size_t workspace_bytes, void* stream) {
-    qc::Common c = qc::common(dims, true, query, key, query_weight, key_weight, cos, sin, positions);
+    qc::Common c = qc::common(dims, query, key, query_weight, key_weight, cos, sin, positions);
     if (c.rc != QC_OK) return c.rc;
     if (!d_query && !d_key && !d_query_weight && !d_key_weight) return QC_OK;
     const bool any_q = d_query || d_query_weight, any_k = d_key || d_key_weight;
@@ -524,7 +523,7 @@ int qkn_bwd(const qkn_dims* dims, const void* query, const void* key, const void
     }
     for (const void* p : {d_query_weight, d_key_weight})
         if (p && !qc::aligned_to(p, e)) return QC_ERR_ALIGN;
-    c.sh = qc::shape_of(*dims, wide, true);
+    c.sh = qc::shape_of(*dims, wide);
     const qc::ByteSpan sp[] = {{d_query, size_t(c.q_out)}, {d_key, size_t(c.k_out)}, {d_query_weight, w}, {d_key_weight, w},
                                {weights ? workspace : nullptr, need}, {query, size_t(c.q_bytes)}, {key, size_t(c.k_bytes)},
                                {query_weight, w}, {key_weight, w}, {cos, table}, {sin, table},
