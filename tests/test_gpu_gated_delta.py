@@ -129,6 +129,33 @@ def check_packed(args, cot, lengths, tail):
     return out, state, grads
 
 
+PAIRED = [(2, 70, 4, 40, 64, 64, None), (1, 130, 3, 66, 32, 60, None), (3, 65, 2, 24, 128, 128, None), (1, 40, 1, 130, 100, 32, None),
+          (1, 203, 2, 10, 40, 96, [64, 0, 1, 65, 70])]
+
+
+@pytest.mark.parametrize("size", PAIRED, ids=str)
+def test_many_heads_of_two_strips_to_a_block(size):
+    """More strips of columns than compute units, an even number to a head: the passes take two at once.  Whole
+    rows on 16 bytes and rows that are not, each count of key blocks, and a batch packed into one row."""
+    print(f"[paired {size}]", flush=True)
+    B, T, Hk, Hv, K, V, lengths = size
+    check(*inputs(B, T, Hk, Hv, K, V, BF16, N=None if lengths is None else len(lengths), seed=Hv), lengths)
+
+
+def test_two_strips_to_a_block_equal_one_bit_for_bit():
+    """The strips of a block share operands and nothing else: 33 sequences of 2 heads in one call, and one by one."""
+    args, cot = inputs(33, 70, 1, 2, 64, 64, BF16, seed=5)
+    leaves = [t.clone().requires_grad_() for t in args]
+    whole = gated_delta_rule(*leaves)
+    grads = torch.autograd.grad(whole, leaves, cot)
+    for n in (0, 17, 32):
+        one = [t[n:n + 1].clone().requires_grad_() for t in args]
+        part = gated_delta_rule(*one)
+        pg = torch.autograd.grad(part, one, [c[n:n + 1] for c in cot])
+        for a, b in zip((*whole, *grads), (*part, *pg)):
+            assert torch.equal(a[n:n + 1], b)
+
+
 def test_packed_equals_a_batch_bit_for_bit():
     args, cot = inputs(3, 100, 1, 2, 64, 32, BF16, seed=11)
     leaves = [t.clone().requires_grad_() for t in args]
