@@ -34,7 +34,7 @@
  * Arithmetic: products run on bfloat16 MFMA with every operand split into
  * bfloat16 parts that hold its whole significand (three for float32), and are
  * summed in float32: float32 accuracy for every dtype.  Decays are cumulated
- * in float64.  log_decay of -inf clears the state, as exp(-inf) = 0 says.
+ * in float64.  log_decay of -inf clears a finite state, as exp(-inf) = 0 says.
  * States and gate gradients are float32; out and the gradients of query, key
  * and value are rounded once to the dtype.  Results do not depend on what else
  * runs, bit for bit.

@@ -266,17 +266,18 @@ def gated_delta_rule(query, key, value, log_decay, beta, initial_state=None, *, 
         S = exp(log_decay_t) S;  u = beta_t (value_t - S^T key_t);  S = S + key_t u^T;  out_t = scale S^T query_t
 
     query, key [B, T, Hk, K] and value [B, T, Hv, V]: float32, bfloat16 or
-    float16, any strides; log_decay (at most zero; -inf clears the state) and
+    float16, any strides; log_decay (at most zero; -inf clears a finite state) and
     beta [B, T, Hv], initial_state [N, Hv, K, V] (None: zeros) and the final
     states float32; K <= 128, V <= 1024.  scale defaults to K ** -0.5.
 
     Without ``offsets`` N = B.  With them (int32 [N + 1] on the GPU, ascending,
     within 0 .. T), B is 1 and sequence n is rows offsets[n] .. offsets[n + 1]
     - 1, of any length down to zero; rows of no sequence have zero out and zero
-    gradients.  A non-finite input spreads at most through its own sequence
-    from its chunk of 64 tokens on."""
+    gradients.  A non-finite input spreads at most through its own sequence, in
+    the outputs from its chunk of 64 tokens on."""
     query, key, value = _last_dense(query), _last_dense(key), _last_dense(value)
     log_decay, beta = log_decay.contiguous(), beta.contiguous()
+    scale = None if scale is None else float(scale)
     if initial_state is not None:
         initial_state = initial_state.contiguous()
     if _grads_wanted(query, key, value, log_decay, beta, initial_state):
@@ -329,7 +330,7 @@ def qk_norm_rotate(query, key, query_weight=None, key_weight=None, cos=None, sin
     cos and sin are refused."""
     if _grads_wanted(cos, sin):
         raise ValueError("qk_norm_rotate has no gradient of cos and sin: detach them")
-    query, key = _last_dense(query), _last_dense(key)
+    query, key, eps = _last_dense(query), _last_dense(key), float(eps)
     if _grads_wanted(query, key, query_weight, key_weight):
         return QkNormRotateFunction.apply(query, key, query_weight, key_weight, cos, sin, positions, kind, eps, interleaved)
     return capi.qkn_fwd(query, key, query_weight, key_weight, cos, sin, positions, kind=kind, eps=eps, interleaved=interleaved)

@@ -802,6 +802,7 @@ def _gdr_dims(query, key, value, n, scale):
 
 
 def _gdr_plan(query, key, value, n, scale):
+    scale = None if scale is None else float(scale)      # a tensor would be kept by its identity, whatever it holds later
     return _lm_plan((0, query.shape, key.shape, value.shape, query.stride(), key.stride(), value.stride(), query.dtype,
                      key.dtype, value.dtype, query.device, key.device, value.device, n, scale),
                     lambda: _gdr_dims(query, key, value, n, scale))
@@ -950,7 +951,7 @@ def _qkn_dims(query, key, cos, positions, kind, eps, interleaved):
 
 
 def _qkn_plan(query, key, query_weight, key_weight, cos, sin, positions, kind, eps, interleaved):
-    device = query.device
+    device, eps = query.device, float(eps)
     d = _lm_plan((1, query.shape, key.shape, query.stride(), key.stride(), query.dtype, key.dtype, device, key.device,
                   None if cos is None else cos.shape, None if positions is None else positions.dtype, kind, eps,
                   bool(interleaved)),

@@ -359,6 +359,26 @@ def test_streams_graphs_and_bits():
         assert all(torch.equal(a, b) for a, b in zip(call(), want))
 
 
+def test_a_scale_or_eps_in_a_tensor_is_read_at_each_call():
+    args, cot = inputs(1, 20, 1, 2, 16, 16, F32, seed=9)
+    scale, eps = torch.tensor(0.5), torch.tensor(0.25)
+    leaves = [t.clone().requires_grad_() for t in args]
+    out = gated_delta_rule(*leaves, scale=scale)
+    first = gated_delta_step(*args[:5], args[5].clone(), scale=scale)
+    normed = qk_norm_rotate(*leaves[:2], eps=eps)
+    scale.fill_(2.0)
+    eps.fill_(4.0)
+    want = gated_delta_rule(*leaves, scale=0.5)
+    for a, b in zip(torch.autograd.grad(out, leaves, cot), torch.autograd.grad(want, leaves, cot)):
+        assert torch.equal(a, b)                     # the backward pass keeps the forward's
+    want = torch.autograd.grad(qk_norm_rotate(*leaves[:2], eps=0.25), leaves[:2], args[:2])
+    assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(normed, leaves[:2], args[:2]), want))
+    assert torch.equal(gated_delta_rule(*args, scale=scale)[0], gated_delta_rule(*args, scale=2.0)[0])
+    second = gated_delta_step(*args[:5], args[5].clone(), scale=scale)
+    assert torch.equal(second, gated_delta_step(*args[:5], args[5].clone(), scale=2.0)) and not torch.equal(first, second)
+    assert torch.equal(qk_norm_rotate(*args[:2], eps=eps)[0], qk_norm_rotate(*args[:2], eps=4.0)[0])
+
+
 def test_refusals():
     args, cot = inputs(2, 5, 2, 4, 16, 8, BF16, seed=22)
     q, k, v, g, b, s = args
