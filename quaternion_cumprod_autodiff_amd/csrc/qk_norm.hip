@@ -338,12 +338,12 @@ struct Shape {
     int g, s, hc;       // lanes per head, slots per lane, heads in a row
 };
 
-// Four heads of a token in a row where that still leaves 8 waves for each of
+// Four heads of a token in a row where that still leaves two waves for each of
 // 1024 SIMDs, one otherwise: they share the angles, the position and the
-// divisions.  Forward, 16384 tokens of 40 heads of 128: 60 us, 79 one by one;
-// 4 x 4096 tokens of 32 heads of 128: 48 us (61), and their VJP 82 us (88).
-// Below the bound the blocks no longer fill the card: 512 tokens of 40 heads
-// are 320 blocks one by one and would be 80.
+// divisions.  By four and one by one, heads of 128 in bfloat16, forward and
+// VJP: 256 tokens of 40 heads 4.5 us (3.5) and 9.7 (8.0), 1024 tokens 6.2
+// (5.6) and 12.0 (14.0), 2048 tokens 9.3 (9.5) and 17.4 (19.6), 16384 tokens
+// 60 (79) forward; 16384 tokens of 32 heads 48 (61) and 82 (88).
 Shape shape_of(const qkn_dims& d, bool wide) {
     Shape sh;
     sh.wide = wide;
@@ -351,7 +351,7 @@ Shape shape_of(const qkn_dims& d, bool wide) {
     sh.g = wide ? pow2_at_least(slots) : 64;
     if (wide && sh.g < 4) sh.g = 4;
     sh.s = wide ? 1 : pow2_at_least((slots + 63) / 64);
-    sh.hc = d.B * d.T * (d.Hq + d.Hk) * sh.g >= 4 * 64 * 8 * 1024 ? 4 : 1;
+    sh.hc = d.B * d.T * (d.Hq + d.Hk) * sh.g >= 4 * 64 * 2 * 1024 ? 4 : 1;
     return sh;
 }
 
