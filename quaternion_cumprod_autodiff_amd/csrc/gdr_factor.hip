@@ -10,6 +10,12 @@
 // on the float32 MFMA, the X_kj staying in accumulators.  Forward
 // substitution by blocks, so no power of A is formed: alike keys do not cost
 // accuracy.
+//
+// Bound by the latency of its steps in a row (loads, product, substitution of
+// 16 rows, three block rows), which three blocks to a CU hide in part: 8192
+// tokens of 32 heads of 128, bfloat16, 79 us; 4 x 4096, 148 us before the
+// forward pass and 154 before the backward one; 8 x 2048 tokens of 16 heads of
+// 64, float32, 128 and 137.
 #include "gdr_chunk.hpp"
 
 namespace qc {

@@ -10,9 +10,17 @@
 // with a barrier after each; S0, the bracket and U pass between waves as
 // fragments in LDS, where one read of S0 serves both of its products.  What a
 // wave multiplies from the left it alone needs, and loads straight into
-// registers, ahead of its phase; V, out and what is saved go through the memory
-// wave.  A sequence's time is the chain of these
-// phases; blocks that share a CU fill each other's gaps.
+// registers, ahead of its phase, out of an L2 that the memory wave's touches
+// fill two chunks before; V, out and what is saved go through the memory wave.
+//
+// Bound by the chain of a sequence's chunks, not by bytes: a chunk is three
+// barriers with reads of LDS, MFMAs and splits of their results between them,
+// about 2 us for heads of 128 in bfloat16.  8192 tokens of 32 heads, 128 chunks
+// in line, 250 us; 12001 tokens of 16 heads in 29 packed sequences 216;
+// 4 x 4096 of 32 heads, saving states, 515, two rounds of blocks.  Set aside: eight waves of
+// half the columns' rows (more reads of LDS for the same products, slower);
+// no touches (431 us became 480 with the factors); 128 registers, for two
+// blocks to a CU (spills: 515 became 780).
 #include "gdr_chunk.hpp"
 
 namespace qc {

@@ -9,7 +9,9 @@
 // small.  A wave owns 32 columns of one state, in registers: lane l holds
 // rows (l / 8) NR .. of columns 4 (l % 8) .. + 3 (NR = K / 8 rounded up to 4,
 // 8 or 16), so a row's piece is one 128-byte line, all of a state's loads are
-// in flight at once, and the reduction stays inside the wave.
+// in flight at once, and the reduction stays inside the wave.  810 MB of states
+// (read and written): 156 us, 5.2 TB/s, a copy's rate; one row of 32 heads of
+// 128 x 128: 4 us, less than a launch.
 #include "gdr_internal.hpp"
 
 #include <type_traits>
