@@ -9,7 +9,7 @@
 // with a barrier after each.  The memory wave brings dO, as the operands dO and
 // scale gamma dO, and takes dS1, X and dV = b X away.  Bound by the chain of
 // chunks as the forward pass is: 4 x 4096 tokens of 32 heads of 128, bfloat16,
-// 510 us; 8 x 2048 tokens of 16 heads of 64 by 128, float32, 355.
+// 510 us; 8 x 2048 tokens of 16 heads of 64 by 128, float32, 315.
 #include "gdr_chunk.hpp"
 
 namespace qc {
@@ -291,12 +291,12 @@ hipError_t launch_gdr_bwd_state(int dt, int kb, const GdrArgs& a, hipStream_t st
     return by_dtype_kb(dt, kb, [&](auto d, auto k) {
         constexpr int DT = decltype(d)::value, KB = decltype(k)::value;
         int strips = (a.V + 15) / 16;
-        const int ns = strips_per_block(a, strips, DT == 1);
+        const int ns = strips_per_block(a, strips, DT != 0 || KB <= 2);
         const int64_t blocks = (a.N * a.Hk + 7) / 8 * 8 * (strips / ns) * a.group;
         const bool vec = a.vec_o && a.V % 16 == 0;
         auto pick = [&](auto vc) -> const void* {
             constexpr bool VEC = decltype(vc)::value;
-            if constexpr (DT == 1)
+            if constexpr (DT != 0 || KB <= 2)
                 if (ns == 2) return reinterpret_cast<const void*>(&gdr_bwd_kernel<DT, KB, VEC, 2>);
             return reinterpret_cast<const void*>(&gdr_bwd_kernel<DT, KB, VEC, 1>);
         };

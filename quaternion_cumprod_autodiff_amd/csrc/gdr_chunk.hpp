@@ -281,9 +281,12 @@ __device__ __forceinline__ void put_parts(bf16x8* frag, int stride, int lane, in
 // second strip finds the operands in L1.  One and two, bfloat16, heads of 128:
 // 4 x 4096 tokens of 32 heads with gradients (1024 strips) forward 595 us and
 // 515, backward 685 and 510; 12001 tokens of 16 heads in 29 packed sequences
-// 237 and 216.  Up to 256 strips each has a CU to itself, and two to a block
-// would leave CUs idle.  fits: the operands leave three waves to a SIMD their registers, which
-// those of one part (bfloat16) do and those of two and three do not.
+// 237 and 216.  8 x 2048 tokens of 16 heads with the factors, float32, K = 32:
+// 400 and 326, backward 420 and 345; K = 64: 475 and 447, 479 and 432; float16
+// K = 64: 358 and 339, 395 and 344; K = 128 backward 575 and 516.  Up to 256
+// strips each has a CU to itself, and two to a block would leave CUs idle.
+// fits: three waves to a SIMD have the registers they need, 168; more parts of
+// longer keys take up to 256.
 inline int strips_per_block(const GdrArgs& a, int strips, bool fits) {
     return fits && strips % 2 == 0 && a.N * a.Hv * strips > 256 ? 2 : 1;
 }

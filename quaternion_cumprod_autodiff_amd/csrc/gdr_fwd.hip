@@ -315,12 +315,12 @@ hipError_t launch_gdr_fwd(int dt, int kb, bool save, const GdrArgs& a, hipStream
     return by_dtype_kb(dt, kb, [&](auto d, auto k) {
         constexpr int DT = decltype(d)::value, KB = decltype(k)::value;
         int strips = (a.V + 15) / 16;
-        const int ns = strips_per_block(a, strips, DT == 1);
+        const int ns = strips_per_block(a, strips, DT == 1 || KB <= 2);
         const int64_t blocks = (a.N * a.Hk + 7) / 8 * 8 * (strips / ns) * a.group;
         const bool vec = a.vec_v && a.vec_o && a.V % 16 == 0;
         auto pick = [&](auto sv, auto vc) -> const void* {
             constexpr bool SAVE = decltype(sv)::value, VEC = decltype(vc)::value;
-            if constexpr (DT == 1)
+            if constexpr (DT == 1 || KB <= 2)
                 if (ns == 2) return reinterpret_cast<const void*>(&gdr_fwd_kernel<DT, KB, SAVE, VEC, 2>);
             return reinterpret_cast<const void*>(&gdr_fwd_kernel<DT, KB, SAVE, VEC, 1>);
         };

@@ -142,6 +142,13 @@ def test_many_heads_of_two_strips_to_a_block(size):
     check(*inputs(B, T, Hk, Hv, K, V, BF16, N=None if lengths is None else len(lengths), seed=Hv), lengths)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16], ids=str)
+@pytest.mark.parametrize("size", [(3, 67, 4, 24, 64, 64), (1, 129, 2, 68, 27, 60), (2, 66, 2, 34, 128, 64), (5, 40, 7, 7, 48, 128)], ids=str)
+def test_many_heads_of_two_strips_to_a_block_of_other_types(size, dtype):
+    print(f"[paired {size} {dtype}]", flush=True)
+    check(*inputs(*size, dtype, seed=size[3]))
+
+
 def test_two_strips_to_a_block_equal_one_bit_for_bit():
     """The strips of a block share operands and nothing else: 33 sequences of 2 heads in one call, and one by one."""
     args, cot = inputs(33, 70, 1, 2, 64, 64, BF16, seed=5)
