@@ -40,7 +40,8 @@
  * runs, bit for bit.
  *
  * Limits: 1 <= K <= 128, 1 <= V <= 1024, Hv a multiple of Hk, B, T, N >= 0,
- * element counts below 2^40.
+ * element counts below 2^40; chunks of 64 tokens in all sequences times Hv,
+ * and N Hv (V + 15) / 16, below 2^23 (gdr_step: N Hv (V + 31) / 32 up to 2^25).
  *
  * Conventions: as in gdn2.h.  Device pointers are the caller's; the library
  * never allocates, frees or keeps one.  Validation is on the host, before any

@@ -274,7 +274,11 @@ def gated_delta_rule(query, key, value, log_decay, beta, initial_state=None, *, 
     within 0 .. T), B is 1 and sequence n is rows offsets[n] .. offsets[n + 1]
     - 1, of any length down to zero; rows of no sequence have zero out and zero
     gradients.  A non-finite input spreads at most through its own sequence, in
-    the outputs from its chunk of 64 tokens on."""
+    the outputs from its chunk of 64 tokens on.
+
+    Forward and backward can be captured into a graph.  As for every autograd
+    function, no eager graph of the same leaves may be alive at the capture of
+    a backward pass: drop the warm-up's outputs first."""
     query, key, value = _last_dense(query), _last_dense(key), _last_dense(value)
     log_decay, beta = log_decay.contiguous(), beta.contiguous()
     scale = None if scale is None else float(scale)
@@ -327,7 +331,8 @@ def qk_norm_rotate(query, key, query_weight=None, key_weight=None, cos=None, sin
     pairs (i, i + R / 2), or (2i, 2i + 1) with ``interleaved``.  Token (b, t)
     takes table row positions[b, t] (int32 or int64), or row t without
     positions; a position outside the table makes its heads NaN.  Gradients of
-    cos and sin are refused."""
+    cos and sin are refused.  Capturing a backward pass: as for
+    :func:`gated_delta_rule`."""
     if _grads_wanted(cos, sin):
         raise ValueError("qk_norm_rotate has no gradient of cos and sin: detach them")
     query, key, eps = _last_dense(query), _last_dense(key), float(eps)
