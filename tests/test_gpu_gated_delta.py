@@ -366,6 +366,33 @@ def test_streams_graphs_and_bits():
         assert all(torch.equal(a, b) for a, b in zip(call(), want))
 
 
+def test_a_training_step_of_a_layer_captured_and_replayed():
+    args, cot = inputs(2, 90, 2, 4, 64, 32, BF16, seed=31)
+    leaves = [t.clone().requires_grad_() for t in args]
+
+    def step():
+        q, k = qk_norm_rotate(*leaves[:2], kind="l2")
+        out, state = gated_delta_rule(q, k, *leaves[2:])
+        return [t.detach() for t in (out, state, *torch.autograd.grad([out, state], leaves, cot))]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        for t in got:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(torch.equal(a, b) for a, b in zip(step(), want))
+
+
 def test_a_scale_or_eps_in_a_tensor_is_read_at_each_call():
     args, cot = inputs(1, 20, 1, 2, 16, 16, F32, seed=9)
     scale, eps = torch.tensor(0.5), torch.tensor(0.25)
