@@ -30,10 +30,8 @@ template <int DT, int KB, bool SAVE, bool VEC, int NS>
 __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrArgs a, int strips) {
     using E = typename Storage<DT>::type;
     constexpr int NPI = parts_of(DT);
-    // Parts of S0, P and U that the output takes: two leave 2^-18 of them, far below the half step of bfloat16, 2^-9.
-    constexpr int NPO = DT == 1 ? 2 : 3;
     constexpr int ST = (2 * KB + 3) / 4;             // tiles of S of a wave
-    __shared__ __align__(16) bf16x8 sf_[NS][KB][kParts][64], rf_[NS][2][kParts][64], ef_[NS][2][kParts][64], uf_[NS][2][NPO][64];
+    __shared__ __align__(16) bf16x8 sf_[NS][KB][kParts][64], rf_[NS][2][kParts][64], ef_[NS][2][kParts][64], uf_[NS][2][kParts][64];
     __shared__ __align__(16) float vb_[NS][16 * kColRow], ob_[NS][16 * kColRow], sb_[NS][SAVE ? 2 * KB * kTile : 4], ub_[NS][SAVE ? 4 * kTile : 4];
     __shared__ __align__(16) float gates_[NS][2][2][64];      // gamma and eta of this chunk and the next
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
@@ -171,7 +169,7 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
         }
     put_state();
 
-    bf16x8 ka[KB][NPI], qa[KB][NPI], kt[ST][2][NPI], ta[2][kParts], pa[2][NPO];
+    bf16x8 ka[KB][NPI], qa[KB][NPI], kt[ST][2][NPI], ta[2][kParts], pa[2][kParts];
     auto load_rows = [&](int c, int set, bf16x8 (&x)[KB][NPI]) {
         const char* p = kr + c * krec;
 #pragma unroll
@@ -211,7 +209,7 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
             for (int b = 0; b < 2; ++b)
                 if ((b == 0 || HI))
 #pragma unroll
-                    for (int i = 0; i < NPO; ++i) pa[b][i] = fragment(p, kTriFrags + tri_index<false>(w, b) * kParts + i, lane);
+                    for (int i = 0; i < kParts; ++i) pa[b][i] = fragment(p, kTriFrags + tri_index<false>(w, b) * kParts + i, lane);
         };
         for (int c = 0; c < chunks; ++c) {
             const int next = c + 1 < chunks ? c + 1 : c;
@@ -230,10 +228,7 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
 #pragma unroll
                 for (int b = 0; b < KB; ++b) {
                     mma(b & 1 ? odd : acc, ka[b], x[b]);
-                    bf16x8 z[NPO];
-#pragma unroll
-                    for (int i = 0; i < NPO; ++i) z[i] = x[b][i];
-                    mma(b & 1 ? o_odd : o, qa[b], z);
+                    mma(b & 1 ? o_odd : o, qa[b], x[b]);
                 }
                 acc += odd;
                 bf16x4 p[kParts];
@@ -257,7 +252,7 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
                 for (int b = 0; b < 2; ++b)
                     if ((b == 0 || HI)) mma(b ? odd : acc, ta[b], y[b]);
                 acc += odd;
-                bf16x4 p[kParts], q[NPO];
+                bf16x4 p[kParts], q[kParts];
                 split4(*reinterpret_cast<const f32x4*>(gc + 64 + i0) * acc, p);
                 put_parts(&ef[w >> 1][0][0], 64, lane, w & 1, p);
                 split4(acc, q);
@@ -286,9 +281,9 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
 #pragma unroll
             for (int b = 0; b < 2; ++b)
                 if ((b == 0 || HI)) {
-                    bf16x8 y[NPO];
+                    bf16x8 y[kParts];
 #pragma unroll
-                    for (int i = 0; i < NPO; ++i) y[i] = uf[b][i][lane];
+                    for (int i = 0; i < kParts; ++i) y[i] = uf[b][i][lane];
                     mma(o, pa[b], y);
                 }
             *reinterpret_cast<f32x4*>(&ob[m * kColRow + i0]) = o;

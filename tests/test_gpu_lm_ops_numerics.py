@@ -1,0 +1,80 @@
+"""Where the gated delta rule, its decoding step and the query/key norm lose bits, range or bookkeeping, if they do:
+each against the float64 oracle's value or formula (needs an MI355X)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import lm_ops as ref
+from quaternion_cumprod_autodiff_amd import capi, gated_delta_rule, gated_delta_step, qk_norm_rotate
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def close(label, got, want, top=None):
+    """Half a step of the type for its one rounding, and 1e-5 of the largest value for the float32 arithmetic, as derived
+    beside the operators' other tests."""
+    rel = torch.finfo(got.dtype).eps / 2
+    got, want = f64(got), np.asarray(want)
+    top = float(np.abs(want).max()) if top is None else top
+    off = float((np.abs(got - want) - rel * np.abs(want)).max())
+    assert np.isfinite(got).all() and off <= 1e-5 * top, f"{label}: {off:.3e} over the rounding, largest {top:.3e}"
+
+
+def randn(gen, shape, dtype=F32):
+    return torch.randn(shape, generator=gen, device=DEV, dtype=F32).to(dtype)
+
+
+def unit(gen, shape, dtype):
+    return torch.nn.functional.normalize(randn(gen, shape), dim=-1).to(dtype)
+
+
+# ------------------------------------------------------------------ whole significands
+
+def nearly_equal(gen, shape):
+    """Float32 numbers in [1, 2) with random last bits, and the same moved by 2^-17: the difference is exact, and two
+    bfloat16 parts, whose last step there is 2^-16, cannot tell how large it is."""
+    a = (1 + 0.9 * torch.rand(shape, generator=gen, device=DEV)).double()
+    a = (a * 2 ** 22).round() / 2 ** 22
+    return a.float(), (a + 2.0 ** -17).float()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=str)
+@pytest.mark.parametrize("K", [32, 64, 128])
+def test_differences_of_state_rows_keep_the_last_bits(K, dtype):
+    """out = S_0 - S_1, rows of the initial state that are alike to 2^-17 of their size.  Six products of parts and their
+    float32 sums are off by at most 6 * 2^-24 * (1 + 1 + 2 * 2) * 2 / 2 < 2^-20; a part left out costs 2^-17 or more."""
+    gen = torch.Generator(device=DEV).manual_seed(K)
+    T, V = 70, 48
+    q, k, v = torch.zeros(1, T, 1, K, device=DEV, dtype=dtype), torch.zeros(1, T, 1, K, device=DEV, dtype=dtype), torch.zeros(1, T, 1, V, device=DEV, dtype=dtype)
+    q[..., 1], q[..., K - 1] = 1, -1
+    g = b = torch.zeros(1, T, 1, device=DEV)
+    s = torch.zeros(1, 1, K, V, device=DEV)
+    s[0, 0, K - 1], s[0, 0, 1] = nearly_equal(gen, (V,))
+    out, state = gated_delta_rule(q, k, v, g, b, s, scale=1.0)
+    want = (s[0, 0, 1].double() - s[0, 0, K - 1].double()).expand(1, T, 1, V)
+    assert torch.equal(state, s)
+    assert ((out.double() - want).abs() <= 2.0 ** -20).all(), float((out.double() - want).abs().max())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=str)
+def test_differences_of_updates_keep_the_last_bits(dtype):
+    """The same for two updates within a chunk: u_0 = b_0, u_1 = b_1 (values of 1, keys that are unit vectors), and later
+    queries read u_0 - u_1."""
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    T, K, V, H = 40, 64, 16, 24
+    q, k = (torch.zeros(1, T, 1, K, device=DEV, dtype=dtype) for _ in range(2))
+    v = torch.ones(1, T, H, V, device=DEV, dtype=dtype)
+    k[0, 0, 0, 0] = k[0, 1, 0, 1] = 1
+    q[0, 2:, 0, 0], q[0, 2:, 0, 1] = -1, 1
+    g, b = torch.zeros(1, T, H, device=DEV), torch.zeros(1, T, H, device=DEV)
+    b[0, 0], b[0, 1] = nearly_equal(gen, (H,))
+    out, _ = gated_delta_rule(q, k, v, g, b, scale=1.0)
+    want = (b[0, 1].double() - b[0, 0].double())[None, None, :, None].expand(1, T, H, V).clone()
+    want[:, :2] = 0
+    assert ((out.double() - want).abs() <= 2.0 ** -20).all(), float((out.double() - want).abs().max())
