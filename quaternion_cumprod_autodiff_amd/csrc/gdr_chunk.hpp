@@ -18,9 +18,13 @@
 //     dKr = -gamma b (X S0^T) + Psi K         (k as the reader of the state)
 //     dKw = eta (U dS1^T) + Phi^T Q + Psi^T K   (k as its writer),   dK = dKr + dKw
 //     db_i = X_i.v_i - gamma_i k_i.(X S0^T)_i - sum_j (X_i.U_j) L_ij
-//     dG_i = q_i.dQ_i + k_i.dKr_i - k_i.dKw_i,   dG_last += gamma_last <S0, dS1> + sum_i eta_i k_i.(U dS1^T)_i
-//     dg_t = sum of dG_i over i >= t
-// All exponents are of differences that decays keep at or below zero.
+//     dg_t = gamma_last <S0, dS1> + sum_{i >= t} gamma_i (scale q_i.(dO S0^T)_i - b_i k_i.(X S0^T)_i)
+//            + sum_{j < t} eta_j k_j.(U dS1^T)_j + sum_{i >= t > j} M_ij,
+//     M_ij = scale (dO_i.U_j) P_ij - b_i (X_i.U_j) L_ij
+// All exponents are of differences that decays keep at or below zero.  Every
+// term of dg_t carries exp(g_t): with q_i.dQ_i + k_i.dKr_i - k_i.dKw_i summed
+// over i >= t, terms of order 1 would have to cancel, and a strong decay's
+// gradient would be their rounding.
 //
 // Kernels: gdr_factor (T, P and the operands' layouts, every chunk at once),
 // gdr_fwd and gdr_bwd_state (the states pass from chunk to chunk: one block per
@@ -201,14 +205,6 @@ __device__ __forceinline__ void mma(f32x4& acc, const bf16x8 (&a)[NA], const bf1
             if (j >= 0 && j < NB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc, 0, 0, 0);
         }
     }
-}
-
-// Zero that the compiler takes for a lane's own: an address with it is read by
-// a vector load.  A scalar load would be waited for with the LDS reads.
-__device__ __forceinline__ int lane_zero() {
-    int z = 0;
-    asm("" : "+v"(z));
-    return z;
 }
 
 // A lane's share of fragment f of a record (base and f the wave's: one address

@@ -22,6 +22,7 @@ namespace qc {
 namespace {
 
 constexpr int kPiece = 128;     // columns of V at a time
+constexpr int kPairRow = 68;    // LDS row of a 64 x 64 float matrix
 
 // Sum over the 16 lanes of a row, in every one of them.
 template <int CTRL>
@@ -33,6 +34,16 @@ __device__ __forceinline__ float sum16(float x) {
     x += rotated<0x124>(x);
     x += rotated<0x122>(x);
     x += rotated<0x121>(x);
+    return x;
+}
+
+// x, as a value of its own: places in LDS that depend on the lane alone are
+// formed where they are used, for each head.  Kept through the loops over V
+// they take registers that these loops spill for: at K = 128 in bfloat16 33
+// registers without this, 2 with it, and a training step of 4 x 4096 tokens of
+// 32 heads 2364 us and 2167 (float32 K = 128: 108 registers and 76).
+__device__ __forceinline__ int formed_here(int x) {
+    asm volatile("" : "+v"(x));
     return x;
 }
 
@@ -48,6 +59,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
     };
     struct Tri {
         bf16x8 phi[4][2][kParts][64], phit[4][2][kParts][64], psi[4][2][kParts][64], psit[4][2][kParts][64];
+        float pairs[64 * kPairRow];      // M
     };
     union Shared {
         __device__ Shared() {}
@@ -56,7 +68,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
     };
     __shared__ __align__(16) Shared sh;
     __shared__ double cum[64];
-    __shared__ __align__(16) float gamma[64], eta[64], beta[64], xv[VB][64], rowsum[2][64], red[3][4][64], dots[8];
+    __shared__ __align__(16) float gamma[64], eta[64], beta[64], xv[VB][64], rowsum[2][64], red[3][4][64], across[8][64], dots[8];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, g = lane >> 4;
     const int cg = wave >> 1, rh = wave & 1;
@@ -98,7 +110,12 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
 
 #pragma unroll 1
     for (int hv = hk * a.group; hv < (hk + 1) * a.group; ++hv) {
-        const Gates* ga = reinterpret_cast<const Gates*>(a.hrec + (hv * a.slots + slot) * kHrecBytes + kGateOffset);
+        const char* hr = a.hrec + (hv * a.slots + slot) * kHrecBytes;
+        const Gates* ga = reinterpret_cast<const Gates*>(hr + kGateOffset);
+        const bf16x8* pf = reinterpret_cast<const bf16x8*>(hr) + kTriFrags * 64;      // P transposed
+        // P's lines on their way to L2, beside the gates: they are needed where nothing hides how far away they are.
+        int line = 0;
+        if (tid < int(kTriFrags * kFrag * 2 / 128)) line = reinterpret_cast<const int*>(pf)[tid * 32];
         __syncthreads();                                  // the head before is done with what is in LDS
         if (tid < 64) {
             gamma[tid] = ga->gamma[tid];
@@ -106,6 +123,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
             beta[tid] = ga->beta[tid];
             cum[tid] = ga->cum[tid];
         }
+        asm volatile("" ::"v"(line));
         f32x4 aq[TW][2], ar[TW][2], aw[TW][2], op[2] = {zero4(), zero4()}, xp[2] = {zero4(), zero4()};
 #pragma unroll
         for (int x = 0; x < TW; ++x)
@@ -120,8 +138,10 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
             if (v0) __syncthreads();                      // the piece before is done
             // A wave takes two (row tile, block of V) pairs: what a lane loads is what it holds of the fragment.  X . v on
             // the way.
+            const int here = formed_here(lane);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                const int lane = here, m = lane & 15, g = lane >> 4;
                 const int tile = wave >> 1, b = 2 * (wave & 1) + i, t = tile_index(tile, m), v = v0 + 32 * b + 8 * g;
                 const bool in = t < rem, have = v < a.VP;
                 const E* op_ = static_cast<const E*>(a.d_out) + ((token0 + (in ? t : 0)) * a.Hv + hv) * a.V;
@@ -251,12 +271,21 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
                     kt[x][b][p] = kt_set[f];
                     qt[x][b][p] = qt_set[f];
                 }
+        // P of the wave's products, which the factors hold transposed: a lane's accumulators are half of its fragment.
+        bf16x4 pt[2][kParts];
+        if (tri_on) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int p = 0; p < kParts; ++p)
+                    pt[c][p] = reinterpret_cast<const bf16x4*>(pf + (tri_index<true>(2 * ch + c, rt >> 1) * kParts + p) * 64 + lane)[rt & 1];
+        }
         __syncthreads();                                  // X, U, dO are done; Phi and Psi take their place
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) sds += __shfl_xor(sds, d, 64);
         if (lane == 0) dots[wave] = rh == 0 ? sds : 0.f;
         {
-            const int i0 = acc_index(rt, g);
+            const int here = formed_here(lane), m = here & 15, g = here >> 4, i0 = acc_index(rt, g);
             float part[4] = {0.f, 0.f, 0.f, 0.f};
             if (tri_on) {
 #pragma unroll
@@ -269,7 +298,10 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
                         const float d = i >= j ? expf(float(cum[i] - cum[j])) : 0.f;
                         phi[r] = i >= j ? a.scale * d * op[c][r] : 0.f;
                         psi[r] = i > j ? -beta[i] * d * xp[c][r] : 0.f;
-                        if (i > j) part[r] += xp[c][r] * (d * kk[c][r]);
+                        const float xl = i > j ? xp[c][r] * (d * kk[c][r]) : 0.f;
+                        part[r] += xl;
+                        const float p = float(pt[c][2][r]) + float(pt[c][1][r]) + float(pt[c][0][r]);
+                        sh.tri.pairs[i * kPairRow + j] = i > j ? a.scale * op[c][r] * p - beta[i] * xl : 0.f;
                     }
                     bf16x4 pp[kParts], ps[kParts];
                     split4(phi, pp);
@@ -309,30 +341,65 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
                 qd[x][e >> 2][e & 3] = q;
             }
         // Sums over the wave's columns of K, per token.
+        const int here = formed_here(lane);
         auto reduce = [&](int which, int r, f32x4 v) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = sum16(v[i]);
-            if (m == 0) *reinterpret_cast<f32x4*>(&red[which][cg][acc_index(2 * rh + r, g)]) = v;
+            if ((here & 15) == 0) *reinterpret_cast<f32x4*>(&red[which][cg][acc_index(2 * rh + r, here >> 4)]) = v;
         };
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int t0 = acc_index(2 * rh + r, g);
+            const int t0 = acc_index(2 * rh + r, here >> 4);
             const f32x4 ga4 = *reinterpret_cast<const f32x4*>(&gamma[t0]), be4 = *reinterpret_cast<const f32x4*>(&beta[t0]),
                         et4 = *reinterpret_cast<const f32x4*>(&eta[t0]);
-            f32x4 b0 = zero4(), z = zero4();
+            f32x4 d0 = zero4(), b0 = zero4(), z = zero4();
 #pragma unroll
             for (int x = 0; x < TW; ++x) {
-                const f32x4 k = {kd[x][r][0], kd[x][r][1], kd[x][r][2], kd[x][r][3]};
+                const f32x4 k = {kd[x][r][0], kd[x][r][1], kd[x][r][2], kd[x][r][3]}, q = {qd[x][r][0], qd[x][r][1], qd[x][r][2], qd[x][r][3]};
+                d0 += q * aq[x][r];
                 b0 += k * ar[x][r];
                 z += k * aw[x][r];
                 aq[x][r] *= a.scale * ga4;
                 ar[x][r] *= -ga4 * be4;
                 aw[x][r] *= et4;
             }
+            reduce(0, r, a.scale * d0 - be4 * b0);
             reduce(1, r, b0);
             reduce(2, r, et4 * z);
         }
-        __syncthreads();                                  // Phi and Psi are in LDS
+        __syncthreads();                                  // Phi, Psi and M are in LDS
+        // The sums of M over i >= t > j: a thread has eight columns of a row, whose sums over j < t a row's eight threads join;
+        // then a wave's eight rows meet, each thread left with one t.  Adding alone, so that no larger term is ever taken away
+        // again.
+        {
+            const int own = formed_here(lane), i = 8 * wave + (own >> 3), t0 = 8 * (own & 7);
+            float x[8], sum = 0.f;
+            load_floats<8>(&sh.tri.pairs[i * kPairRow + t0], x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float y = t0 + e < i ? x[e] : 0.f;      // what lies across the diagonal was not written
+                x[e] = sum;
+                sum += y;
+            }
+#pragma unroll
+            for (int n = 1; n < 8; n *= 2) {
+                const float y = __shfl_up(sum, n, 8);
+                sum += (own & 7) >= n ? y : 0.f;
+            }
+            const float y = __shfl_up(sum, 1, 8), before = own & 7 ? y : 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = t0 + e <= i ? before + x[e] : 0.f;
+#pragma unroll
+            for (int n = 4; n >= 1; n /= 2) {
+                const bool upper = own & (8 * n);
+#pragma unroll
+                for (int e = 0; e < n; ++e) {
+                    const float other = __shfl_xor(upper ? x[e] : x[e + n], 8 * n, 64);
+                    x[e] = (upper ? x[e + n] : x[e]) + other;
+                }
+            }
+            across[wave][t0 + (own >> 3 & 1) + 2 * (own >> 4 & 1) + 4 * (own >> 5)] = x[0];
+        }
         if (k_on) {
             auto times = [&](const bf16x8 (&f)[4][2][kParts][64], int b, f32x4 (&acc)[TW][2], const bf16x8 (&k)[TW][2][NPI]) {
 #pragma unroll
@@ -357,17 +424,12 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
             }
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            f32x4 d = zero4();
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int x = 0; x < TW; ++x) {
-                const f32x4 k = {kd[x][r][0], kd[x][r][1], kd[x][r][2], kd[x][r][3]}, q = {qd[x][r][0], qd[x][r][1], qd[x][r][2], qd[x][r][3]};
-                d += q * aq[x][r] + k * (ar[x][r] - aw[x][r]);
                 dq_all[x][r] += aq[x][r];
                 dk_all[x][r] += ar[x][r] + aw[x][r];
             }
-            reduce(0, r, d);
-        }
         __syncthreads();
         if (wave == 0) {
             float d = 0.f, b0 = 0.f, z = 0.f;
@@ -377,23 +439,24 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(GdrArgs a) {
                 b0 += red[1][c][lane];
                 z += red[2][c][lane];
             }
-#pragma unroll
-            for (int i = 1; i < 64; i *= 2) z += __shfl_xor(z, i, 64);
-            float dot = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dot += dots[i];
-            double sum = d;
-            if (lane == 63) sum += double(gamma[63]) * dot + z;
+            // A lane's token t: what it and later tokens read of S0, what earlier ones leave in S1, and the pairs across it.
+            d *= gamma[lane];
 #pragma unroll
             for (int i = 1; i < 64; i *= 2) {
-                const double y = __shfl_down(sum, i, 64);
-                if (lane + i < 64) sum += y;
+                const float x = __shfl_down(d, i, 64), y = __shfl_up(z, i, 64);
+                d += lane + i < 64 ? x : 0.f;
+                z += lane >= i ? y : 0.f;
+            }
+            z = __shfl_up(z, 1, 64);
+            float dot = 0.f, pairs = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dot += dots[i];
+                pairs += across[i][lane];
             }
             if (lane < rem) {
                 const int64_t at = (token0 + lane) * a.Hv + hv;
-                // dg is a multiple of exp(g): nothing where that is 0, whatever rounding leaves of the sum.
-                const float decay = expf(float(cum[lane] - (lane ? cum[lane - 1] : 0.0)));
-                if (a.dg) a.dg[at] = decay > 0.f || decay != decay ? float(sum) : 0.f;
+                if (a.dg) a.dg[at] = gamma[63] * dot + d + (lane ? z : 0.f) + pairs;
                 if (a.db) a.db[at] = (xv[0][lane] + xv[1][lane] + xv[2][lane] + xv[3][lane]) - gamma[lane] * b0 - (rowsum[0][lane] + rowsum[1][lane]);
             }
         }

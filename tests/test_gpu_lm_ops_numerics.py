@@ -78,3 +78,45 @@ def test_differences_of_updates_keep_the_last_bits(dtype):
     want = (b[0, 1].double() - b[0, 0].double())[None, None, :, None].expand(1, T, H, V).clone()
     want[:, :2] = 0
     assert ((out.double() - want).abs() <= 2.0 ** -20).all(), float((out.double() - want).abs().max())
+
+
+# ------------------------------------------------------------------ gradients of strong decays
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=str)
+@pytest.mark.parametrize("g0", [-3.0, -8.0, -20.0, -40.0])
+def test_gradients_of_uniform_strong_decays(g0, dtype):
+    """The gradient of log_decay scales with exp(log_decay): nothing that does not carry the decay may be left in it."""
+    gen = torch.Generator(device=DEV).manual_seed(int(-g0))
+    B, T, Hk, Hv, K, V = 1, 150, 1, 2, 64, 48
+    args = [unit(gen, (B, T, Hk, K), dtype), unit(gen, (B, T, Hk, K), dtype), randn(gen, (B, T, Hv, V), dtype),
+            torch.full((B, T, Hv), g0, device=DEV), torch.rand(B, T, Hv, generator=gen, device=DEV), randn(gen, (B, Hv, K, V))]
+    cot = [randn(gen, (B, T, Hv, V), dtype), randn(gen, (B, Hv, K, V))]
+    leaves = [t.requires_grad_() for t in args]
+    grads = torch.autograd.grad(gated_delta_rule(*leaves), leaves, cot)
+    want = ref.gdr_bwd(*[f64(t) for t in args], K ** -0.5, *[f64(c) for c in cot])
+    for name, got, w in zip(("query", "key", "value", "log_decay", "beta", "initial_state"), grads, want):
+        close("gradient of " + name, got, w)
+
+
+@pytest.mark.parametrize("K", [24, 128])
+def test_gradients_of_strong_decays_among_weak_ones(K):
+    """At the tokens whose decay is strong the gradient is far below the others': it is held to its own size.  A decay of
+    exactly nothing has a gradient of exactly nothing."""
+    gen = torch.Generator(device=DEV).manual_seed(K)
+    B, T, H, V = 2, 200, 2, 32
+    args = [unit(gen, (B, T, H, K), F32), unit(gen, (B, T, H, K), F32), randn(gen, (B, T, H, V)), -0.1 * torch.rand(B, T, H, generator=gen, device=DEV),
+            torch.rand(B, T, H, generator=gen, device=DEV), randn(gen, (B, H, K, V))]
+    cot = [randn(gen, (B, T, H, V)), randn(gen, (B, H, K, V))]
+    strong = [0, 5, 63, 64, 90, 127, 128, 191, 192, 199]
+    args[3][:, strong] = -25.0
+    args[3][:, [30, 150]] = -float("inf")
+    leaves = [t.requires_grad_() for t in args]
+    got = torch.autograd.grad(gated_delta_rule(*leaves), leaves, cot)[3]
+    want = ref.gdr_bwd(*[f64(t) for t in args], K ** -0.5, *[f64(c) for c in cot])[3]
+    close("all", got, want)
+    # The bound is 1e-5 of the token's own largest gradient.  (exp(-25) times the largest of all tokens is no bound on it: at
+    # the last token <dS, S> is 20 times that of a weak token, and 1e-5 of the smaller figure would be 5e-7 of the value,
+    # below the sqrt(6 (128 + 32 + 64)) 2^-23 = 4e-6 that float32 sums of so many terms are off by.)
+    for t in strong:
+        close(f"token {t}", got[:, t], want[:, t])
+    assert not got[:, [30, 150]].any()
