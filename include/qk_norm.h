@@ -21,6 +21,8 @@
  * (elements; the last axis is dense); outputs, cotangents and gradients are
  * dense [B, T, H, D].  One dtype (QKN_F32, QKN_BF16, QKN_F16) for query, key,
  * weights, outputs and gradients; arithmetic is float32, rounded once.
+ * The sum of squares is float32 too: a head whose sum passes its range (elements
+ * of 1e19) becomes zeros.
  * Outputs may not overlap inputs.
  *
  * The VJP takes the outputs' cotangents and returns those of query, key and

@@ -3,8 +3,10 @@
 //
 // Forward, per head x [D] with r = 1 / sqrt(sum x^2 / size + eps) (size D or
 // 1): n = x r w, y = turn(n).  VJP, with the cotangent g of y:
-//     dn = turn^-1(g),   dh = dn w,   c = sum dh x
-//     dx = r dh - x r^3 c / size,     dw = sum over tokens and heads of dn x r
+//     dn = turn^-1(g),   dh = dn w,   h = x r,   c = sum dh h
+//     dx = r (dh - h c / size),       dw = sum over tokens and heads of dn h
+// (r^3, in the same gradient's r dh - x r^3 sum(dh x) / size, leaves the range
+// of float32 long before dx does.)
 // The statistics, the products and the weights' sums are float32.
 //
 // Bound by memory: every element is read once (twice as x and g in the VJP)
@@ -233,23 +235,25 @@ __global__ void __launch_bounds__(kThreads) qkn_kernel(QknArgs a) {
                     if (slot[s].turns) turn<W>(pg[s], ph[s], c[s], sn[s], inter, -1.f);
 #pragma unroll
                     for (int j = 0; j < W; ++j) {
-                        sa[s][j] += pg[s][j] * (pa[s][j] * r);
-                        sb_[s][j] += ph[s][j] * (pb[s][j] * r);
+                        pa[s][j] *= r;
+                        pb[s][j] *= r;
+                        sa[s][j] += pg[s][j] * pa[s][j];
+                        sb_[s][j] += ph[s][j] * pb[s][j];
                         pg[s][j] *= wa[s][j];
                         ph[s][j] *= wb[s][j];
                         dot += pg[s][j] * pa[s][j] + ph[s][j] * pb[s][j];
                     }
                 }
                 dot = group_sum<G>(dot);
-                const float f = r * r * r * dot * a.inv_size;
+                const float f = dot * a.inv_size;
                 if (y) {
                     E* py = y + dense + k * D;
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
 #pragma unroll
                         for (int j = 0; j < W; ++j) {
-                            pa[s][j] = r * pg[s][j] - pa[s][j] * f;
-                            pb[s][j] = r * ph[s][j] - pb[s][j] * f;
+                            pa[s][j] = r * (pg[s][j] - pa[s][j] * f);
+                            pb[s][j] = r * (ph[s][j] - pb[s][j] * f);
                         }
                         if (FULL || slot[s].has_a) store_floats<W>(py + slot[s].a, pa[s]);
                         if (FULL || slot[s].has_b) store_floats<W>(py + slot[s].b, pb[s]);

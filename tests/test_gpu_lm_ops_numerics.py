@@ -120,3 +120,28 @@ def test_gradients_of_strong_decays_among_weak_ones(K):
     for t in strong:
         close(f"token {t}", got[:, t], want[:, t])
     assert not got[:, [30, 150]].any()
+
+
+# ------------------------------------------------------------------ heads far from one
+
+@pytest.mark.parametrize("kind", ["rms", "l2"])
+@pytest.mark.parametrize("D", [64, 90])
+@pytest.mark.parametrize("size,eps", [(1e15, 1e-6), (1e13, 1e-6), (1e-14, 0.0), (1e-16, 1e-36)])
+def test_norm_gradients_of_large_and_small_heads(size, eps, D, kind):
+    """The gradient is of the order 1 / |x|, whatever |x|: no factor on the way may leave the range of float32.  Its two
+    terms cancel in part, so the bound is of the largest term (see the norm's other tests)."""
+    gen = torch.Generator(device=DEV).manual_seed(D)
+    q, k = randn(gen, (2, 9, 3, D)) * size, randn(gen, (2, 9, 2, D)) * size
+    w = 1 + 0.1 * randn(gen, (D,))
+    leaves = [t.requires_grad_() for t in (q, k, w)]
+    out = qk_norm_rotate(leaves[0], leaves[1], leaves[2], kind=kind, eps=eps)
+    cot = [randn(gen, t.shape) for t in out]
+    gq, gk, gw = torch.autograd.grad(out, leaves, cot)
+    how = (None, None, None, kind, float(np.float32(eps)), False)
+    close("out", out[0], ref.qkn_fwd(f64(q), f64(w), *how))
+    want, want_w = ref.qkn_bwd(f64(q), f64(w), *how, f64(cot[0]))
+    top = np.abs(want).max()
+    assert np.isfinite(f64(gq)).all() and np.abs(f64(gq) - want).max() <= 1e-5 * 4 * top
+    close("weight", gw, want_w)
+    want, _ = ref.qkn_bwd(f64(k), None, *how, f64(cot[1]))
+    assert np.isfinite(f64(gk)).all() and np.abs(f64(gk) - want).max() <= 1e-5 * 4 * np.abs(want).max()
