@@ -296,7 +296,8 @@ def gated_delta_step(query, key, value, log_decay, beta, state, *, slots=None, s
     [slots, Hv, K, V] float32, is updated in place; row n uses state slots[n]
     (int32; without ``slots`` state n).  Returns out [B, T, Hv, V].  A row
     whose slot is outside the pool (-1 for padding) or named by an earlier row
-    is not run: its out is zero.  Not differentiable."""
+    is not run: its out is zero.  Not differentiable; a graph that saved the
+    pool before raises in its backward pass, as after any operation in place."""
     if _grads_wanted(query, key, value, log_decay, beta, state):
         raise ValueError("gated_delta_step updates its states in place and has no gradient: use gated_delta_rule")
     return capi.gdr_step(query, key, value, log_decay, beta, state, slots, scale=scale)

@@ -776,6 +776,14 @@ def _lm_dense(name, t, shape, dtype, device):
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _lm_written(*tensors):
+    """Tells autograd that a call wrote these tensors of the caller's (None: none given), which it cannot
+    see: a graph that saved one refuses its backward pass, as after any operation in place."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _gdr_dims(query, key, value, n, scale):
     _lm_heads("query", query)
     _lm_heads("key", key, query)
@@ -838,7 +846,7 @@ def gdr_fwd(query, key, value, log_decay, beta, initial_state=None, *, scale=Non
     ws_bytes = lib.gdr_workspace_bytes(d, 0)
     if ws_bytes == 0:
         raise QuatCumprodError(-2, "gdr_fwd")
-    shape = (d.B, d.T, d.Hv, d.V)
+    shape, given = (d.B, d.T, d.Hv, d.V), out
     if out is None:
         out = (torch.empty if offsets is None else torch.zeros)(shape, dtype=query.dtype, device=device)
     else:
@@ -850,6 +858,7 @@ def gdr_fwd(query, key, value, log_decay, beta, initial_state=None, *, scale=Non
                      _data_ptr(offsets), _data_ptr(initial_state), out.data_ptr(), fin.data_ptr(), _data_ptr(saved),
                      ws.data_ptr(), ws_bytes, torch.cuda.current_stream(device).cuda_stream)
     _check(rc, "gdr_fwd")
+    _lm_written(given)
     return out, fin, saved
 
 
@@ -905,7 +914,7 @@ def gdr_step(query, key, value, log_decay, beta, state, slots=None, *, scale=Non
         _lm_dense("slots", slots, (d.B,), torch.int32, device)
     elif state.shape[0] < d.B:
         raise ValueError(f"state must have a slot for each of {d.B} rows, got {state.shape[0]}")
-    shape = (d.B, d.T, d.Hv, d.V)
+    shape, given = (d.B, d.T, d.Hv, d.V), out
     if out is None:
         out = torch.empty(shape, dtype=query.dtype, device=device)
     else:
@@ -915,6 +924,7 @@ def gdr_step(query, key, value, log_decay, beta, state, slots=None, *, scale=Non
                          None if slots is None else slots.data_ptr(), out.data_ptr(),
                          torch.cuda.current_stream(device).cuda_stream)
     _check(rc, "gdr_step")
+    _lm_written(state, given)
     return out
 
 
@@ -984,6 +994,7 @@ def qkn_fwd(query, key, query_weight=None, key_weight=None, cos=None, sin=None, 
         return _lm_there(device, stream, qkn_fwd, query, key, query_weight, key_weight, cos, sin, positions, kind=kind,
                          eps=eps, interleaved=interleaved, query_out=query_out, key_out=key_out)
     d = _qkn_plan(query, key, query_weight, key_weight, cos, sin, positions, kind, eps, interleaved)
+    given = query_out, key_out
     if query_out is None:
         query_out = torch.empty(query.shape, dtype=query.dtype, device=device)
     else:
@@ -996,6 +1007,7 @@ def qkn_fwd(query, key, query_weight=None, key_weight=None, cos=None, sin=None, 
                         _data_ptr(sin), _data_ptr(positions), query_out.data_ptr(), key_out.data_ptr(),
                         torch.cuda.current_stream(device).cuda_stream)
     _check(rc, "qkn_fwd")
+    _lm_written(*given)
     return query_out, key_out
 
 

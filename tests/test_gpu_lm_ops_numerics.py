@@ -145,3 +145,35 @@ def test_norm_gradients_of_large_and_small_heads(size, eps, D, kind):
     close("weight", gw, want_w)
     want, _ = ref.qkn_bwd(f64(k), None, *how, f64(cot[1]))
     assert np.isfinite(f64(gk)).all() and np.abs(f64(gk) - want).max() <= 1e-5 * 4 * np.abs(want).max()
+
+
+# ------------------------------------------------------------------ in place
+
+def test_a_step_on_states_that_a_graph_saved_is_noticed():
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    q, k, v = unit(gen, (2, 1, 1, 16), F32), unit(gen, (2, 1, 1, 16), F32), randn(gen, (2, 1, 2, 8))
+    g, b = -torch.rand(2, 1, 2, generator=gen, device=DEV), torch.rand(2, 1, 2, generator=gen, device=DEV)
+    pool = randn(gen, (3, 2, 2, 16, 8))
+    w = torch.ones_like(pool).requires_grad_()
+    loss = (w * pool).sum()
+    version = pool._version
+    gated_delta_step(q, k, v, g, b, pool[:, 1])                    # a view of the pool
+    assert pool._version > version
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        gated_delta_step(q, k, v, g, b, torch.zeros(2, 2, 16, 8, device=DEV))    # has no version
+
+
+def test_given_outputs_count_as_modified():
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    q, k, v = unit(gen, (2, 3, 1, 16), F32), unit(gen, (2, 3, 1, 16), F32), randn(gen, (2, 3, 2, 8))
+    g, b = -torch.rand(2, 3, 2, generator=gen, device=DEV), torch.rand(2, 3, 2, generator=gen, device=DEV)
+    out, qo, ko = torch.zeros_like(v), torch.zeros_like(q), torch.zeros_like(k)
+    at = [t._version for t in (out, qo, ko)]
+    capi.gdr_fwd(q, k, v, g, b, out=out)
+    capi.qkn_fwd(q, k, query_out=qo, key_out=ko)
+    assert all(t._version > n for t, n in zip((out, qo, ko), at))
+    n = out._version
+    capi.gdr_step(q, k, v, g, b, torch.zeros(2, 2, 16, 8, device=DEV), out=out)
+    assert out._version > n
