@@ -22,6 +22,7 @@ All arithmetic runs in the HIP library through :mod:`.capi`.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import capi
 
@@ -231,6 +232,13 @@ def _grads_wanted(*tensors) -> bool:
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
+def _refuse_forward_mode(name, *tensors):
+    """A dual tensor of forward-mode differentiation does not require a gradient: without this its tangent would be
+    dropped in silence."""
+    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"{name} has no forward-mode derivative")
+
+
 def _last_dense(t):
     return t if t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
 
@@ -279,6 +287,7 @@ def gated_delta_rule(query, key, value, log_decay, beta, initial_state=None, *, 
     Forward and backward can be captured into a graph.  As for every autograd
     function, no eager graph of the same leaves may be alive at the capture of
     a backward pass: drop the warm-up's outputs first."""
+    _refuse_forward_mode("gated_delta_rule", query, key, value, log_decay, beta, initial_state)
     query, key, value = _last_dense(query), _last_dense(key), _last_dense(value)
     log_decay, beta = log_decay.contiguous(), beta.contiguous()
     scale = None if scale is None else float(scale)
@@ -298,6 +307,7 @@ def gated_delta_step(query, key, value, log_decay, beta, state, *, slots=None, s
     whose slot is outside the pool (-1 for padding) or named by an earlier row
     is not run: its out is zero.  Not differentiable; a graph that saved the
     pool before raises in its backward pass, as after any operation in place."""
+    _refuse_forward_mode("gated_delta_step", query, key, value, log_decay, beta, state)
     if _grads_wanted(query, key, value, log_decay, beta, state):
         raise ValueError("gated_delta_step updates its states in place and has no gradient: use gated_delta_rule")
     return capi.gdr_step(query, key, value, log_decay, beta, state, slots, scale=scale)
@@ -334,6 +344,7 @@ def qk_norm_rotate(query, key, query_weight=None, key_weight=None, cos=None, sin
     positions; a position outside the table makes its heads NaN.  Gradients of
     cos and sin are refused.  Capturing a backward pass: as for
     :func:`gated_delta_rule`."""
+    _refuse_forward_mode("qk_norm_rotate", query, key, query_weight, key_weight, cos, sin)
     if _grads_wanted(cos, sin):
         raise ValueError("qk_norm_rotate has no gradient of cos and sin: detach them")
     query, key, eps = _last_dense(query), _last_dense(key), float(eps)
