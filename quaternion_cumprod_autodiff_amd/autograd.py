@@ -31,6 +31,13 @@ _STATUS_MODES = ("deferred", "sync")
 _SAVED_MODES = ("boundary", "final", "none")
 
 
+def _refuse_forward_mode(name, *tensors):
+    """A dual tensor of forward-mode differentiation does not require a gradient: without this its tangent would be
+    dropped in silence."""
+    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"{name} has no forward-mode derivative")
+
+
 class QuatCumprodFunction(torch.autograd.Function):
     """cum = quat_cumprod(q, init); backward = the recompute-based VJP.
 
@@ -85,6 +92,7 @@ def quat_cumprod(q: torch.Tensor, init: torch.Tensor, *, saved: str = "boundary"
         raise ValueError(f"status_check must be one of {_STATUS_MODES}")
     if saved not in _SAVED_MODES:
         raise ValueError(f"saved must be one of {_SAVED_MODES}")
+    _refuse_forward_mode("quat_cumprod", q, init)
     if torch.is_grad_enabled() and (q.requires_grad or init.requires_grad):
         return QuatCumprodFunction.apply(q, init, saved, status_check)
     capi.default_workspace.poll()
@@ -172,6 +180,7 @@ def scan(body: str, xs: torch.Tensor, init: torch.Tensor, *, num_checkpoints: in
     keeps k snapshots and recomputes the rest (binomial checkpointing)."""
     if num_checkpoints < 0:
         raise ValueError("num_checkpoints must be >= 0")
+    _refuse_forward_mode("scan", xs, init)
     if torch.is_grad_enabled() and (xs.requires_grad or init.requires_grad):
         return ScanFunction.apply(body, xs, init, num_checkpoints)
     return capi.scan_fwd(body, xs.contiguous(), init.contiguous())
@@ -219,6 +228,7 @@ def gated_deltanet2(query, key, value, erase, write, log_decay, initial_state, *
     faster forward; low_memory=True runs the kernel that needs no memory
     beyond the outputs instead."""
     ins = (query, key, value, erase, write, log_decay, initial_state)
+    _refuse_forward_mode("gated_deltanet2", *ins)
     if torch.is_grad_enabled() and any(t.requires_grad for t in ins):
         return GatedDeltaNet2Function.apply(*ins, chunk)
     context, state, _ = capi.gdn2_fwd(*[t.contiguous() for t in ins], chunk=chunk, want_boundary=not low_memory)
@@ -230,13 +240,6 @@ def gated_deltanet2(query, key, value, erase, write, log_decay, initial_state, *
 
 def _grads_wanted(*tensors) -> bool:
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
-
-
-def _refuse_forward_mode(name, *tensors):
-    """A dual tensor of forward-mode differentiation does not require a gradient: without this its tangent would be
-    dropped in silence."""
-    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
-        raise NotImplementedError(f"{name} has no forward-mode derivative")
 
 
 def _last_dense(t):

@@ -41,3 +41,22 @@ def test_forward_mode_is_refused_and_not_dropped(tracked):
                 autograd.qk_norm_rotate(dual(q), k)
         with pytest.raises(ValueError, match="GPU"):       # a level without a dual tensor is no matter
             autograd.qk_norm_rotate(q, k)
+
+
+def test_forward_mode_is_refused_by_the_scans_and_by_gated_deltanet2():
+    q, init = torch.zeros(1, 2, 1, 1, 4), torch.zeros(1, 1, 1, 4)
+    xs, start = torch.zeros(1, 2, 3, 4), torch.zeros(1, 3, 4)
+    row, dense, state = torch.zeros(1, 1, 16, 8), torch.zeros(1, 1, 16, 8), torch.zeros(1, 1, 8, 8)
+    with forward_ad.dual_level():
+        for a, b in ((dual(q), init), (q, dual(init))):
+            with pytest.raises(NotImplementedError, match="forward"):
+                autograd.quat_cumprod(a, b)
+            with pytest.raises(NotImplementedError, match="forward"):
+                autograd.quat_cumprod_with_final(a, b)
+        for a, b in ((dual(xs), start), (xs, dual(start))):
+            with pytest.raises(NotImplementedError, match="forward"):
+                autograd.scan("quat", a, b)
+        with pytest.raises(NotImplementedError, match="forward"):
+            autograd.gated_deltanet2(row, row, dual(dense), row, dense, row, state, chunk=16)
+        with pytest.raises(NotImplementedError, match="forward"):
+            autograd.gated_deltanet2(row, row, dense, row, dense, row, dual(state), chunk=16)
