@@ -39,9 +39,11 @@
  * and value are rounded once to the dtype.  Results do not depend on what else
  * runs, bit for bit.
  *
- * Limits: 1 <= K <= 128, 1 <= V <= 1024, Hv a multiple of Hk, B, T, N >= 0,
- * element counts below 2^40; chunks of 64 tokens in all sequences times Hv,
- * and N Hv (V + 15) / 16, below 2^23 (gdr_step: N Hv (V + 31) / 32 up to 2^25).
+ * Limits: 1 <= K <= 128, 1 <= V <= 1024, Hv a multiple of Hk and at most 2^20,
+ * B, T, N >= 0, T below 2^31, element counts at most 2^40.  gdr_fwd, gdr_bwd:
+ * Hv times the chunks of 64 tokens (N ceil(T / 64); with offsets T / 64 + N)
+ * below 2^23, and N Hk rounded up to a multiple of 8, times Hv / Hk ceil(V / 16),
+ * below 2^23.  gdr_step: N Hv ceil(V / 32) up to 2^25.
  *
  * Conventions: as in gdn2.h.  Device pointers are the caller's; the library
  * never allocates, frees or keeps one.  Validation is on the host, before any

@@ -11,7 +11,7 @@ struct Plan {
     int64_t slots, tokens, vp;
     int64_t saved_s, saved_u;                  // bytes of the two parts of the saved buffer
     int64_t krec, hrec, x, ds;                 // bytes of the workspace's parts
-    int64_t q_bytes, v_bytes_q, v_bytes, gates, states, out;
+    int64_t q_bytes, gates, states, out;
 };
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -30,8 +30,9 @@ Plan plan(const gdr_dims* dims) {
     p.slots = d.packed ? d.T / kChunk + d.N : count(d.N, per);
     // Grids stay below 2^32 threads: 512 to a block.
     if (p.slots < 0 || count(p.slots, d.Hv) < 0 || p.slots * d.Hv >= (int64_t(1) << 23)) return p;
-    const int64_t units = count(d.N, d.Hv);
-    if (units < 0 || count(units + 8 * d.Hv, p.vp / 16) < 0 || (units + 8 * d.Hv) * (p.vp / 16) >= (int64_t(1) << 23)) return p;
+    const int64_t units = count(d.N, d.Hk);
+    const int64_t blocks = units < 0 ? -1 : count((units + 7) / 8 * 8, d.Hv / d.Hk * (p.vp / 16));
+    if (blocks < 0 || blocks >= (int64_t(1) << 23)) return p;
     if (!d.T) p.slots = 0;
     p.tokens = d.B * d.T;
     const int64_t heads = p.slots * d.Hv;

@@ -226,8 +226,9 @@ extern "C" int gdr_step(const gdr_dims* dims, const void* query, const void* key
     const int64_t extent = n_slots ? qc::count(n_slots - 1, slot_stride) : 0;
     if (extent < 0 || (!slots && n_slots < d.N)) return QC_ERR_SHAPE;
     const int tiles = int((d.V + qc::kCols - 1) / qc::kCols);
-    const int64_t heads = qc::count(d.N, d.Hv), blocks = heads < 0 ? -1 : qc::count((heads + 7) / 8 * 8, tiles);
-    if (blocks < 0 || blocks > (int64_t(1) << 25)) return QC_ERR_SHAPE;   // 64 threads each, below 2^32 in all
+    const int64_t heads = qc::count(d.N, d.Hv), used = heads < 0 ? -1 : qc::count(heads, tiles);
+    if (used < 0 || used > (int64_t(1) << 25)) return QC_ERR_SHAPE;
+    const int64_t blocks = (heads + 7) / 8 * 8 * tiles;      // 64 threads each: below 2^32 in all
     const size_t e = qc::dtype_bytes(d.dtype);
     for (const void* p : {query, key, value, static_cast<const void*>(out)})
         if (!qc::aligned_to(p, e)) return QC_ERR_ALIGN;
