@@ -1,0 +1,79 @@
+"""Memory that the language-model operators may not touch, and sizes whose offsets need 64 bits (needs an MI355X)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import lm_ops as ref
+from quaternion_cumprod_autodiff_amd import capi, gated_delta_step
+from test_gpu_lm_ops import check_norm, close, f64, norm_inputs, randn, unit
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+
+
+# ------------------------------------------------------------------ nothing beside the tensors is written
+
+class Arena:
+    """Tensors inside one buffer, between bands that hold a pattern."""
+    BAND = 1 << 16
+
+    def __init__(self, nbytes):
+        self.buf = torch.full((nbytes,), 0xA5, dtype=torch.uint8, device=DEV)
+        self.at, self.used = self.BAND, []
+
+    def new(self, nbytes):
+        start = self.at
+        self.used.append((start, start + nbytes))
+        self.at = (start + nbytes + 255) // 256 * 256 + self.BAND
+        assert self.at <= self.buf.numel()
+        return self.buf.data_ptr() + start
+
+    def put(self, t):
+        p = self.new(t.numel() * t.element_size())
+        lo, hi = self.used[-1]
+        self.buf[lo:hi].copy_(t.contiguous().view(-1).view(torch.uint8))
+        return p
+
+    def bands_whole(self):
+        edges = [0] + [x for lo, hi in self.used for x in (lo, hi)] + [self.buf.numel()]
+        return all(bool((self.buf[a:b] == 0xA5).all()) for a, b in zip(edges[::2], edges[1::2]))
+
+
+def offset_lists():
+    rng = np.random.default_rng(4)
+    top = 2 ** 31 - 1
+    fixed = [[0, 150, 100, 50], [-5, 70, 90, 150], [0, 70, 90, 10 ** 9], [150, 100, 50, 0], [top] * 4, [-top - 1] * 4, [-top - 1, top, -top - 1, top],
+             [top, -top - 1, top, 0], [0, 0, 0, 150], [149, 150, 151, 152], [0, 150, 0, 150], [64, 128, 64, 128]]
+    return fixed + [rng.integers(-40, 200, 4).tolist() for _ in range(12)]
+
+
+@pytest.mark.parametrize("K,V,Hk,Hv,dtype", [(32, 16, 1, 2, BF16), (128, 40, 2, 2, F32), (50, 100, 1, 3, F16)], ids=str)
+def test_no_offsets_reach_beyond_the_tensors(K, V, Hk, Hv, dtype):
+    """The kernels clamp offsets and take every slot of their buffers from the clamped ones: whatever they hold, only
+    the outputs, the saved state and the workspace are written."""
+    gen = torch.Generator(device=DEV).manual_seed(K)
+    T, N = 150, 3
+    lib, e = capi.load(), torch.finfo(dtype).bits // 8
+    q, k, v = unit(gen, (1, T, Hk, K), dtype), unit(gen, (1, T, Hk, K), dtype), randn(gen, (1, T, Hv, V), dtype)
+    g, b = -torch.rand(1, T, Hv, generator=gen, device=DEV), torch.rand(1, T, Hv, generator=gen, device=DEV)
+    s, d_out, d_fin = randn(gen, (N, Hv, K, V)), randn(gen, (1, T, Hv, V), dtype), randn(gen, (N, Hv, K, V))
+    d = capi.GdrDims(1, T, Hk, Hv, K, V, N)
+    for st, t in ((d.q_stride, q), (d.k_stride, k), (d.v_stride, v)):
+        st[:] = t.stride()[:3]
+    d.dtype, d.scale, d.packed = capi._LM_DTYPES[dtype], 0.5, 1
+    stream = torch.cuda.current_stream().cuda_stream
+    sizes = [lib.gdr_saved_bytes(d), lib.gdr_workspace_bytes(d, 0), lib.gdr_workspace_bytes(d, 1)]
+    for offsets in offset_lists():
+        print(f"[offsets {offsets}]", flush=True)
+        inputs = [q, k, v, g, b, torch.tensor(offsets, dtype=torch.int32, device=DEV), s, d_out, d_fin]
+        arena = Arena(sum(sizes) + 64 * Arena.BAND + 4 * sum(t.numel() * 4 for t in inputs))
+        p = [arena.put(t) for t in inputs]
+        out, fin, saved, ws, ws2 = (arena.new(n) for n in (T * Hv * V * e, N * Hv * K * V * 4, *sizes))
+        grads = [arena.new(n) for n in (T * Hk * K * e, T * Hk * K * e, T * Hv * V * e, T * Hv * 4, T * Hv * 4, N * Hv * K * V * 4)]
+        assert lib.gdr_fwd(d, *p[:6], p[6], out, fin, saved, ws, sizes[1], stream) == 0
+        assert lib.gdr_bwd(d, *p[:6], saved, p[7], p[8], *grads, ws2, sizes[2], stream) == 0
+        torch.cuda.synchronize()
+        assert arena.bands_whole(), offsets
+        for t, (lo, hi) in zip(inputs, arena.used):
+            assert torch.equal(arena.buf[lo:hi], t.contiguous().view(-1).view(torch.uint8)), offsets
