@@ -77,3 +77,32 @@ def test_no_offsets_reach_beyond_the_tensors(K, V, Hk, Hv, dtype):
         assert arena.bands_whole(), offsets
         for t, (lo, hi) in zip(inputs, arena.used):
             assert torch.equal(arena.buf[lo:hi], t.contiguous().view(-1).view(torch.uint8)), offsets
+
+
+# ------------------------------------------------------------------ repeated slots, far rows
+
+def test_step_skips_rows_of_a_slot_named_far_before():
+    """Rows are looked through 64 at a time: repeats on both sides of that, of the first row, of a padding row."""
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    B, Hk, Hv, K, V, n_slots = 211, 1, 2, 24, 20, 190
+    q, k, v = unit(gen, (B, 1, Hk, K), BF16), unit(gen, (B, 1, Hk, K), BF16), randn(gen, (B, 1, Hv, V), BF16)
+    g, b = -torch.rand(B, 1, Hv, generator=gen, device=DEV), torch.rand(B, 1, Hv, generator=gen, device=DEV)
+    state = randn(gen, (n_slots, Hv, K, V))
+    slots = torch.randperm(n_slots, generator=gen, device=DEV).to(torch.int32).cpu()
+    slots = torch.cat([slots, slots[:21]])                            # rows 190.. repeat rows 0..20
+    slots[[64, 65, 128, 129, 200]] = slots[[0, 1, 63, 64, 199]]
+    slots[[70, 150]] = -1
+    seen, run = set(), []
+    for i, x in enumerate(slots.tolist()):
+        if x >= 0 and x not in seen:
+            run.append(i)
+        seen.add(x)
+    before, at = state.clone(), slots[run].long()
+    out = gated_delta_step(q, k, v, g, b, state, slots=slots.to(DEV))
+    want, fin = ref.gdr_fwd(*(f64(x)[run] for x in (q, k, v, g, b)), f64(before)[at.numpy()], K ** -0.5)
+    close("out", out[run], want)
+    close("state", state[at.to(DEV)], fin)
+    rest = sorted(set(range(B)) - set(run))
+    assert len(rest) >= 26 and not out[rest].any()
+    untouched = sorted(set(range(n_slots)) - set(at.tolist()))
+    assert torch.equal(state[untouched], before[untouched])
