@@ -106,3 +106,15 @@ def test_step_skips_rows_of_a_slot_named_far_before():
     assert len(rest) >= 26 and not out[rest].any()
     untouched = sorted(set(range(n_slots)) - set(at.tolist()))
     assert torch.equal(state[untouched], before[untouched])
+
+
+# ------------------------------------------------------------------ four heads in a row
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=str)
+@pytest.mark.parametrize("kind,interleaved", [("rms", False), ("rms", True), ("l2", False), ("l2", True)])
+@pytest.mark.parametrize("size", [(1, 1700, 3, 2, 90, 42, 300), (1, 9400, 5, 2, 128, 64, 300), (2, 4100, 4, 4, 128, 128, 50), (3, 3001, 1, 3, 240, 16, 9)],
+                         ids=str)
+def test_norm_of_many_heads(size, kind, interleaved, dtype):
+    """Calls of so many heads that a group takes four of a token in a row, in every type, kind and order of pairs."""
+    print(f"[norm {size} {kind} {interleaved} {dtype}]", flush=True)
+    check_norm(*norm_inputs(*size, dtype, kind == "rms", seed=size[1]), kind=kind, interleaved=interleaved)
