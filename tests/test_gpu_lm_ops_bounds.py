@@ -118,3 +118,75 @@ def test_norm_of_many_heads(size, kind, interleaved, dtype):
     """Calls of so many heads that a group takes four of a token in a row, in every type, kind and order of pairs."""
     print(f"[norm {size} {kind} {interleaved} {dtype}]", flush=True)
     check_norm(*norm_inputs(*size, dtype, kind == "rms", seed=size[1]), kind=kind, interleaved=interleaved)
+
+
+# ------------------------------------------------------------------ offsets beyond 2^31 elements
+
+@pytest.fixture
+def much_memory():
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_step_on_a_pool_of_more_than_2_to_the_31_elements(much_memory):
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    B, Hk, Hv, K, V, n_slots = 5, 2, 32, 128, 128, 4200
+    q, k, v = unit(gen, (B, 2, Hk, K), BF16), unit(gen, (B, 2, Hk, K), BF16), randn(gen, (B, 2, Hv, V), BF16)
+    g, b = -torch.rand(B, 2, Hv, generator=gen, device=DEV), torch.rand(B, 2, Hv, generator=gen, device=DEV)
+    pool = torch.full((n_slots, Hv, K, V), 3.0, device=DEV)
+    slots = torch.tensor([4199, 0, 4096, 4095, 2048], dtype=torch.int32, device=DEV)
+    near = randn(gen, (B, Hv, K, V))
+    pool[slots.long()] = near
+    out = gated_delta_step(q, k, v, g, b, pool, slots=slots)
+    want = gated_delta_step(q, k, v, g, b, near)
+    assert torch.equal(out, want) and torch.equal(pool[slots.long()], near)
+    for n in (1, 2047, 2049, 4094, 4097, 4198):
+        assert (pool[n] == 3.0).all()
+
+
+def test_rule_of_more_than_2_to_the_31_elements(much_memory):
+    """A training step of 65 sequences of 8192 tokens of 32 heads of 128, against some of its sequences alone, bit for bit."""
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    B, T, H, K, V = 65, 8192, 32, 128, 128
+    new = lambda *s: torch.empty(s, dtype=BF16, device=DEV).normal_(generator=gen)
+    q, k, v, d_out = new(B, T, H, K).mul_(K ** -0.5), new(B, T, H, K).mul_(K ** -0.5), new(B, T, H, V), new(B, T, H, V)
+    g, b = -torch.rand(B, T, H, generator=gen, device=DEV), torch.rand(B, T, H, generator=gen, device=DEV)
+    s, d_fin = randn(gen, (B, H, K, V)), randn(gen, (B, H, K, V))
+    assert v.numel() > 2 ** 31
+    out, state, saved = capi.gdr_fwd(q, k, v, g, b, s, want_saved=True)
+    grads = capi.gdr_bwd(q, k, v, g, b, saved, d_out, d_fin)
+    del saved
+    for n in (0, 31, 63, 64):
+        one = [t[n:n + 1] for t in (q, k, v, g, b, s)]
+        o, st, sv = capi.gdr_fwd(*one, want_saved=True)
+        gr = capi.gdr_bwd(*one[:5], sv, d_out[n:n + 1], d_fin[n:n + 1])
+        for name, x, y in zip(("out", "state", "query", "key", "value", "log_decay", "beta", "initial"), (out, state, *grads), (o, st, *gr)):
+            assert torch.equal(x[n:n + 1], y), (n, name)
+
+
+def test_norm_of_more_than_2_to_the_31_heads_and_elements(much_memory):
+    """Numbers of heads beyond 31 bits (64-bit divisions) on more blocks than a launch has, and offsets beyond 2^31."""
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    B, T, Hq, Hk, D = 2, 179_000_003, 5, 1, 2
+    new = lambda *s: torch.empty(s, dtype=BF16, device=DEV).normal_(generator=gen)
+    q, k = new(B, T, Hq, D), new(B, T, Hk, D)
+    assert B * T * (Hq + Hk) >= 2 ** 31 and q.numel() > 2 ** 31
+    angle = randn(gen, (1000, 1))
+    pos = torch.randint(0, 1000, (B, T), generator=gen, device=DEV, dtype=torch.int32)
+    w = randn(gen, (D,), BF16)
+    cuts = [(0, 0), (0, T // 2), (0, T - 300), (1, 0), (1, 2 ** 31 // (Hq * D) - T - 150), (1, T - 300)]
+    qo, ko = capi.qkn_fwd(q, k, w, None, angle.cos(), angle.sin(), pos)
+    how = lambda b, c: (f64(angle.cos()), f64(angle.sin()), pos[b:b + 1, c].cpu().numpy(), "rms", 1e-6, False)
+    for b, t in cuts:
+        c = slice(t, t + 300)
+        close(f"query {b} {t}", qo[b:b + 1, c], ref.qkn_fwd(f64(q[b:b + 1, c]), f64(w), *how(b, c)))
+        close(f"key {b} {t}", ko[b:b + 1, c], ref.qkn_fwd(f64(k[b:b + 1, c]), None, *how(b, c)))
+    dq, dk, _, _ = capi.qkn_bwd(q, k, w, None, angle.cos(), angle.sin(), pos, qo, ko, want=(True, True, False, False))
+    for b, t in cuts:
+        c = slice(t, t + 300)
+        for name, got, x, wt, dy in (("query", dq, q, w, qo), ("key", dk, k, None, ko)):
+            x, dy, wt = f64(x[b:b + 1, c]), f64(dy[b:b + 1, c]), None if wt is None else f64(wt)
+            r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-6)
+            # the gradient's two terms cancel: the bound is of the largest of them (see the norm's other tests)
+            top = float((2 * r * np.abs(dy).max(-1, keepdims=True) * (1 if wt is None else np.abs(wt).max())).max())
+            close(f"gradient of {name} {b} {t}", got[b:b + 1, c], ref.qkn_bwd(x, wt, *how(b, c), dy)[0], top=top)
