@@ -35,6 +35,11 @@
  * bfloat16 parts that hold its whole significand (three for float32), and are
  * summed in float32: float32 accuracy for every dtype.  Decays are cumulated
  * in float64.  log_decay of -inf clears a finite state, as exp(-inf) = 0 says.
+ * A key, gate (other than -inf) or value that is not finite makes the outputs
+ * of its own and all later tokens of its sequence NaN, in the heads that read
+ * it (a value: in its column), and the final state; a query its own token's;
+ * what comes before is as without it.  The backward pass may return NaN for
+ * any token of such a sequence.
  * States and gate gradients are float32; out and the gradients of query, key
  * and value are rounded once to the dtype.  Results do not depend on what else
  * runs, bit for bit.

@@ -284,8 +284,10 @@ def gated_delta_rule(query, key, value, log_decay, beta, initial_state=None, *, 
     Without ``offsets`` N = B.  With them (int32 [N + 1] on the GPU, ascending,
     within 0 .. T), B is 1 and sequence n is rows offsets[n] .. offsets[n + 1]
     - 1, of any length down to zero; rows of no sequence have zero out and zero
-    gradients.  A non-finite input spreads at most through its own sequence, in
-    the outputs from its chunk of 64 tokens on.
+    gradients.  A key, gate or value that is not finite makes the outputs of its
+    own and all later tokens of its sequence NaN, in the heads that read it (a
+    value: in its column), and the final state; a query its own token's.  What
+    comes before is as without it.  Gradients: anywhere in its sequence.
 
     Forward and backward can be captured into a graph.  As for every autograd
     function, no eager graph of the same leaves may be alive at the capture of

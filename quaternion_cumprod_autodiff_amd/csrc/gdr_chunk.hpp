@@ -21,6 +21,12 @@
 //     dg_t = gamma_last <S0, dS1> + sum_{i >= t} gamma_i (scale q_i.(dO S0^T)_i - b_i k_i.(X S0^T)_i)
 //            + sum_{j < t} eta_j k_j.(U dS1^T)_j + sum_{i >= t > j} M_ij,
 //     M_ij = scale (dO_i.U_j) P_ij - b_i (X_i.U_j) L_ij
+// Non-finite inputs, forward.  In these products a token's NaN or infinity
+// would meet the zeros across the diagonal and reach the tokens before it.  So
+// a key, gate or value that is not finite enters as zero, and the places it
+// reaches by the recurrence, its own token and all later ones (a value: in its
+// column), become NaN at the end: poison in Gates, and the forward pass'
+// memory wave.  Queries reach their own token alone as it is.
 // All exponents are of differences that decays keep at or below zero.  Every
 // term of dg_t carries exp(g_t): with q_i.dQ_i + k_i.dKr_i - k_i.dKw_i summed
 // over i >= t, terms of order 1 would have to cancel, and a strong decay's
@@ -74,6 +80,7 @@ constexpr int64_t krec_bytes(int kb, int npi) { return 3 * set_frags(kb, npi) * 
 constexpr int64_t kTriFrags = 6 * kParts;
 struct Gates {
     float gamma[kChunk], eta[kChunk], beta[kChunk];
+    float poison[kChunk];        // forward: NaN from the first token on whose key or gates are not finite, else 0
     double cum[kChunk];
 };
 constexpr int64_t kGateOffset = 2 * kTriFrags * kFrag * 2;
@@ -211,6 +218,16 @@ __device__ __forceinline__ void mma(f32x4& acc, const bf16x8 (&a)[NA], const bf1
 // register per lane serves all).
 __device__ __forceinline__ bf16x8 fragment(const char* base, int64_t f, int lane) {
     return reinterpret_cast<const bf16x8*>(base + f * (kFrag * 2))[uint32_t(lane)];
+}
+
+// Whether any of eight bfloat16 is infinite or NaN: 0x7f80, their exponent bits, plus 0x80 is 0x8000.
+__device__ __forceinline__ bool not_finite(const bf16x8& x) {
+    typedef uint32_t Words __attribute__((ext_vector_type(4)));
+    const Words u = __builtin_bit_cast(Words, x);
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top |= (u[i] & 0x7f807f80u) + 0x00800080u;
+    return top & 0x80008000u;
 }
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }

@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(256) gdr_factor_kernel(GdrArgs a) {
     float* mx = sh.inverse;
     __shared__ double cum[64];
     __shared__ __align__(16) float beta[64];
+    __shared__ int first_bad[5];      // of a row tile's keys and of the gates: the first token that is not finite
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 15, g = lane >> 4;
     const int hv = int(blockIdx.x % a.Hv);
     const int64_t slot = blockIdx.x / a.Hv;
@@ -86,11 +87,37 @@ __global__ void __launch_bounds__(256) gdr_factor_kernel(GdrArgs a) {
             load_parts<DT>(qp + c, left, a.vec_qk, qa[b]);
         }
     }
+    if constexpr (!BWD) {
+        bool bad = false;
+#pragma unroll
+        for (int b = 0; b < KB; ++b) bad |= not_finite(ka[b][0]);
+        const uint64_t mask = __ballot(bad);
+        int first = kChunk;
+        if (mask) {
+            const uint32_t rows = uint32_t(mask | mask >> 16 | mask >> 32 | mask >> 48) & 0xffffu;
+            first = tile_index(w, __builtin_ctz(rows));
+            if (rows >> m & 1)
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int p = 0; p < NPI; ++p)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) ka[b][p][j] = __bf16(0.f);
+        }
+        if (lane == 0) first_bad[w] = first;
+    }
     // Gates: decays cumulated in 64 bits.  -2000 stands for every decay below it: exp() of it is 0, and sums with it
     // leave the differences behind it exact to 1e-11.
     if (w == 0) {
         const bool in = lane < rem;
-        const float gt = in ? g_raw : 0.f, bt = in ? b_raw : 0.f;
+        float gt = in ? g_raw : 0.f, bt = in ? b_raw : 0.f;
+        if constexpr (!BWD) {
+            const bool bad = !(gt < __builtin_inff()) || !(fabsf(bt) < __builtin_inff());
+            const uint64_t mask = __ballot(bad);
+            gt = bad ? 0.f : gt;
+            bt = bad ? 0.f : bt;
+            if (lane == 0) first_bad[4] = mask ? __builtin_ctzll(mask) : kChunk;
+        }
         double c = gt < -2000.f ? -2000.0 : double(gt);
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
@@ -114,6 +141,12 @@ __global__ void __launch_bounds__(256) gdr_factor_kernel(GdrArgs a) {
             if constexpr (BWD) qf[w][b][p][lane] = qa[b][p];
         }
     __syncthreads();
+    if (!BWD && w == 0) {
+        int first = first_bad[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) first = first_bad[i] < first ? first_bad[i] : first;
+        reinterpret_cast<Gates*>(hr + kGateOffset)->poison[lane] = lane >= first ? __builtin_nanf("") : 0.f;
+    }
     // K (backward: Q too) transposed: tiles of K, blocks of tokens.
     if (lead) {
         const __bf16* ks = reinterpret_cast<const __bf16*>(&kf);

@@ -34,6 +34,7 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
     __shared__ __align__(16) bf16x8 sf_[NS][KB][kParts][64], rf_[NS][2][kParts][64], ef_[NS][2][kParts][64], uf_[NS][2][kParts][64];
     __shared__ __align__(16) float vb_[NS][16 * kColRow], ob_[NS][16 * kColRow], sb_[NS][SAVE ? 2 * KB * kTile : 4], ub_[NS][SAVE ? 4 * kTile : 4];
     __shared__ __align__(16) float gates_[NS][2][2][64];      // gamma and eta of this chunk and the next
+    __shared__ float last_[NS][2][16];                        // gamma_last by column: NaN where an input is not finite
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
     const int sub = NS == 1 ? 0 : wave < 4 * NS ? wave >> 2 : wave - 4 * NS;      // which of the block's strips
     auto& sf = sf_[sub];
@@ -45,6 +46,7 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
     auto& sb = sb_[sub];
     auto& ub = ub_[sub];
     auto& gates = gates_[sub];
+    auto& last = last_[sub];
     const int m = lane & 15, g = lane >> 4;
     int64_t n;
     int hv, strip;
@@ -67,13 +69,43 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
             const int i = c * kChunk + lane;
             x.load(v + (i < s.len ? i : s.len - 1) * v_step, strip * 16, a.V);
         };
-        auto put_v = [&](int c) {
+        float gamma, eta, key_poison;
+        // Columns (bits) in which this lane's token comes at or behind an input that is not finite: of the chunk whose
+        // outputs are stored next, of the one in work, of the one to come.
+        uint32_t gone_out = 0, gone = 0, gone_next = 0;
+        // V as it enters, columns and tokens that are none as zero.  With one strip to a block this is done in phase 1, where
+        // the memory wave is early, with two in phase 2, where the strips' waves hide it and phase 1 would wait for V:
+        // 8192 tokens of 32 heads 255 us so and 272 the other way, 12001 packed tokens of 16 heads 216 and 220, 4 x 4096 of
+        // 32 heads, saving states, 542 and 552.
+        float f[16], of_column;
+        auto take_v = [&](int c) {
             const bool in = c * kChunk + lane < s.len;
+            float sum[4] = {key_poison, 0.f, 0.f, 0.f};
+            of_column = __shfl(gamma, kChunk - 1, 64);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const float f = x.at(j);
-                vb[j * kColRow + lane] = in && (VEC || strip * 16 + j < a.V) ? f : 0.f;
+                const float z = x.at(j);
+                f[j] = in && (VEC || strip * 16 + j < a.V) ? z : 0.f;
+                sum[j % 4] = fmaf(f[j], 0.f, sum[j % 4]);
             }
+            gone_next = 0;
+            if (__any(sum[0] + sum[1] + (sum[2] + sum[3]) != 0.f)) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const bool bad = fmaf(f[j], 0.f, key_poison) != 0.f;      // NaN too
+                    const uint64_t mask = __ballot(bad);
+                    if (mask) {
+                        gone_next |= uint32_t(lane >= __builtin_ctzll(mask)) << j;
+                        f[j] = f[j] * 0.f == 0.f ? f[j] : 0.f;
+                        if (lane == j) of_column = __builtin_nanf("");
+                    }
+                }
+            }
+        };
+        auto put_v = [&](int c) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) vb[j * kColRow + lane] = f[j];
+            if (lane < 16) last[c & 1][lane] = of_column;
         };
         float y[16];
         auto read_out = [&] {
@@ -82,13 +114,16 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
         };
         auto store_out = [&](int c) {
             const int i = c * kChunk + lane;
+            if (__any(gone_out))
+#pragma unroll
+                for (int j = 0; j < 16; ++j) y[j] = gone_out >> j & 1 ? __builtin_nanf("") : y[j];
             if (i < s.len) store_columns<E, VEC>(out + i * o_step, strip * 16, a.V, y);
         };
-        float gamma, eta;
         auto load_gates = [&](int c) {
             const Gates* p = reinterpret_cast<const Gates*>(hr + c * kHrecBytes + kGateOffset);
             gamma = p->gamma[lane];
             eta = p->eta[lane];
+            key_poison = p->poison[lane];
         };
         auto put_gates = [&](int c) {
             gates[c & 1][0][lane] = gamma;
@@ -98,7 +133,9 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
         if (chunks) {
             load_v(0);
             load_gates(0);
+            take_v(0);
             put_v(0);
+            gone = gone_next;
             put_gates(0);
             load_v(chunks > 1 ? 1 : 0);
             load_gates(chunks > 1 ? 1 : 0);
@@ -116,10 +153,12 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
         }
         for (int c = 0; c < chunks; ++c) {
             if (c) read_out();
+            if (NS == 1 && c + 1 < chunks) take_v(c + 1);
             if constexpr (SAVE) states.read(sb, lane);
             __syncthreads();
             ahead.done();
             if (c + 1 < chunks) {
+                if (NS == 2) take_v(c + 1);
                 put_v(c + 1);
                 put_gates(c + 1);
                 const int then = c + 2 < chunks ? c + 2 : c + 1;
@@ -133,7 +172,17 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
                 if (c) updates.store(to_u + int64_t(c - 1) * strips * 1024, lane);
             }
             __syncthreads();
-            if constexpr (SAVE) updates.read(ub, lane);
+            if constexpr (SAVE) {
+                if (__any(gone)) {      // U as the backward pass has to find it
+                    float* row = &ub[(2 * (lane >> 5) + ((lane >> 2) & 1)) * kTile + 4 * ((lane & 31) >> 3) + (lane & 3)];      // token `lane`
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (gone >> j & 1) row[j * kTileRow] = __builtin_nanf("");
+                }
+                updates.read(ub, lane);
+            }
+            gone_out = gone;
+            gone = gone_next;
             __syncthreads();
         }
         if (chunks) {
@@ -237,6 +286,7 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
             }
             __syncthreads();
             // Phase 2.
+            const float gamma_last = last[c & 1][m];
             load_kt(c);
             load_p(c);
             {
@@ -264,7 +314,7 @@ __global__ void __launch_bounds__(320 * NS, NS == 2 ? 3 : 1) gdr_fwd_kernel(GdrA
             load_rows(next, 0, ka);
             load_rows(next, 1, qa);
 #pragma unroll
-            for (int y = 0; y < ST; ++y) st[y] *= gc[kChunk - 1];
+            for (int y = 0; y < ST; ++y) st[y] *= gamma_last;
             {
                 bf16x8 y[2][kParts];
 #pragma unroll

@@ -177,3 +177,73 @@ def test_given_outputs_count_as_modified():
     n = out._version
     capi.gdr_step(q, k, v, g, b, torch.zeros(2, 2, 16, 8, device=DEV), out=out)
     assert out._version > n
+
+
+# ------------------------------------------------------------------ inputs that are not finite
+
+def rule_inputs(B, T, Hk, Hv, K, V, dtype, seed):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    return [unit(gen, (B, T, Hk, K), dtype), unit(gen, (B, T, Hk, K), dtype), randn(gen, (B, T, Hv, V), dtype),
+            -torch.rand(B, T, Hv, generator=gen, device=DEV), torch.rand(B, T, Hv, generator=gen, device=DEV), randn(gen, (B, Hv, K, V))]
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("dtype,K,V,Hk,Hv", [(F32, 40, 24, 1, 2), (BF16, 128, 32, 2, 4), (F16, 64, 50, 1, 3), (BF16, 20, 64, 1, 80)], ids=str)
+def test_what_is_not_finite_reaches_no_earlier_token(dtype, K, V, Hk, Hv, saved):
+    """out of token t depends on tokens up to t: what comes before a NaN or an infinity keeps its bits, and from there on
+    its head (a value: its column; a query: its token) is not finite, the final state neither."""
+    T = 150
+    clean = rule_inputs(1, T, Hk, Hv, K, V, dtype, K)
+    run = lambda a: capi.gdr_fwd(*a, want_saved=saved)[:2]
+    want, want_state = run(clean)
+    group = Hv // Hk
+    for t, bad in ((0, float("nan")), (5, float("inf")), (17, float("nan")), (31, -float("inf")), (63, float("nan")), (64, float("inf")), (149, float("nan"))):
+        for which in range(5):
+            args = [x.clone() for x in clean]
+            h, c = (t + which) % args[which].shape[2], (7 * t + which) % args[which].shape[-1]
+            if which < 3:
+                args[which][0, t, h, c] = bad
+            else:
+                args[which][0, t, h] = float("nan") if which == 3 else bad      # a decay of -inf is an input like others
+            out, state = run(args)
+            hit = torch.zeros(T, Hv, V, dtype=torch.bool, device=DEV)
+            heads = slice(h * group, (h + 1) * group) if which < 2 else h
+            if which == 0:
+                hit[t, heads] = True
+            elif which == 2:
+                hit[t:, h, c] = True
+            else:
+                hit[t:, heads] = True
+            assert torch.equal(out[0][~hit], want[0][~hit]), (t, which)
+            assert not out[0][hit].isfinite().any(), (t, which)
+            gone = hit[T - 1][:, None].expand(Hv, K, V) if which else torch.zeros_like(state[0], dtype=torch.bool)
+            assert torch.equal(state[0][~gone], want_state[0][~gone]) and not state[0][gone].isfinite().any(), (t, which)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+def test_a_batch_with_garbage_behind_each_end(dtype):
+    """Rows of a padded batch that hold anything: the tokens before keep their bits."""
+    clean = rule_inputs(3, 140, 1, 2, 64, 48, dtype, 1)
+    ends = [1, 77, 130]
+    args = [x.clone() for x in clean]
+    for n, end in enumerate(ends):
+        for x, junk in zip(args[:5], (float("nan"), float("inf"), float("nan"), float("nan"), -float("inf"))):
+            x[n, end:] = junk
+    out, want = gated_delta_rule(*args)[0], gated_delta_rule(*clean)[0]
+    for n, end in enumerate(ends):
+        assert torch.equal(out[n, :end], want[n, :end]) and not out[n, end:].isfinite().any()
+
+
+def test_gradients_of_what_is_not_finite_are_not_finite():
+    """Entering as zero is the forward pass' way alone: a loss that saw a NaN has no finite gradients of what led to it."""
+    for which in (1, 2, 4):
+        args = rule_inputs(1, 100, 1, 2, 32, 16, F32, which)
+        with torch.no_grad():
+            args[which].view(100, -1)[40, 0] = float("nan")
+        leaves = [t.requires_grad_() for t in args]
+        out, state = gated_delta_rule(*leaves)
+        for y in (out, state):
+            grads = torch.autograd.grad(y.sum(), leaves, retain_graph=True)
+            for i, name in ((1, "key"), (4, "beta"), (5, "initial_state")):
+                if which != 2 or i == 4:              # a value's NaN is in the gradients that it multiplies
+                    assert not grads[i].isfinite().all(), (which, name)
