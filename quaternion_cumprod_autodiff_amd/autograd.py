@@ -289,6 +289,10 @@ def gated_delta_rule(query, key, value, log_decay, beta, initial_state=None, *, 
     value: in its column), and the final state; a query its own token's.  What
     comes before is as without it.  Gradients: anywhere in its sequence.
 
+    With gradients, the float32 states and updates of every chunk of 64 tokens
+    are kept from forward to backward: N ceil(T / 64) Hv (K' + 64) V' 4 bytes,
+    K' = 32, 64 or 128 and V' a multiple of 16.
+
     Forward and backward can be captured into a graph.  As for every autograd
     function, no eager graph of the same leaves may be alive at the capture of
     a backward pass: drop the warm-up's outputs first."""

@@ -9,7 +9,8 @@
 // with a barrier after each.  The memory wave brings dO, as the operands dO and
 // scale gamma dO, and takes dS1, X and dV = b X away.  Bound by the chain of
 // chunks as the forward pass is: 4 x 4096 tokens of 32 heads of 128, bfloat16,
-// 510 us; 8 x 2048 tokens of 16 heads of 64 by 128, float32, 315.
+// 507 us, matrix units 19% in use, LDS 33%, waves at a wait or a barrier 58% of
+// the time; 8 x 2048 tokens of 16 heads of 64 by 128, float32, 303.
 #include "gdr_chunk.hpp"
 
 namespace qc {

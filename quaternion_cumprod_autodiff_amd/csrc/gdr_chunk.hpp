@@ -287,19 +287,21 @@ __device__ __forceinline__ void put_parts(bf16x8* frag, int stride, int lane, in
     for (int n = 0; n < NP; ++n) reinterpret_cast<bf16x4*>(frag + n * stride + lane)[half] = p[n];
 }
 
-// Strips of 16 columns to a block of the passes over a sequence.  One at a time
-// a CU holds one block (five waves, registers for two to a SIMD), and a block's
-// waves wait for each other three times a chunk.  So where strips are more than
-// CUs and pair up, a block takes two, ten waves in step, three to a SIMD; the
-// second strip finds the operands in L1.  One and two, bfloat16, heads of 128:
-// 4 x 4096 tokens of 32 heads with gradients (1024 strips) forward 595 us and
-// 515, backward 685 and 510; 12001 tokens of 16 heads in 29 packed sequences
-// 237 and 216.  8 x 2048 tokens of 16 heads with the factors, float32, K = 32:
-// 400 and 326, backward 420 and 345; K = 64: 475 and 447, 479 and 432; float16
-// K = 64: 358 and 339, 395 and 344; K = 128 backward 575 and 516.  Up to 256
+// Strips of 16 columns to a block of the passes over a sequence.  With one, five
+// waves are all that a busy CU was measured to hold (forward, K = 128: registers
+// for two waves to a SIMD; backward: a second block's registers and LDS would
+// fit), and they wait for each other three times a chunk.  So where strips are
+// more than CUs and pair up, a block takes two, ten waves in step, and the
+// second strip finds operands in L1: of 4 x 4096 tokens of 32 heads of 128,
+// bfloat16, saving states, 56 million reads go on to L2 with one strip, 31 with
+// two.  Kernels, one strip and two: that forward pass 606 us and 526, its
+// backward 663 and 507; 12001 tokens of 16 heads in 29 packed sequences 255 and
+// 216; 8 x 2048 tokens of 16 heads, V = 128, forward and backward, float32
+// K = 32: 281 and 246, 338 and 276; K = 64: 321 and 310, 347 and 303; float16
+// K = 64: 287 and 258, 321 and 265; K = 128 backward 415 and 359.  Up to 256
 // strips each has a CU to itself, and two to a block would leave CUs idle.
-// fits: three waves to a SIMD have the registers they need, 168; more parts of
-// longer keys take up to 256.
+// fits: three waves to a SIMD have the registers they need, 168 (float32 K = 64
+// spills 3 where no states are saved); more parts of longer keys take up to 256.
 inline int strips_per_block(const GdrArgs& a, int strips, bool fits) {
     return fits && strips % 2 == 0 && a.N * a.Hv * strips > 256 ? 2 : 1;
 }

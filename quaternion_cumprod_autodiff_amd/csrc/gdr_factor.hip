@@ -12,10 +12,12 @@
 // accuracy.
 //
 // Bound by the latency of its steps in a row (loads, product, substitution of
-// 16 rows, three block rows), which three blocks to a CU hide in part: 8192
-// tokens of 32 heads of 128, bfloat16, 79 us; 4 x 4096, 148 us before the
-// forward pass and 154 before the backward one; 8 x 2048 tokens of 16 heads of
-// 64, float32, 128 and 137.
+// 16 rows, three block rows), which the blocks of a CU hide in part: three, by
+// LDS; two for float32 K = 64 and float16 K = 128, one for float32 K = 128.
+// Matrix units 9% in use, waves at a wait or a barrier half of the time.  8192
+// tokens of 32 heads of 128, bfloat16, 77 us; 4 x 4096, 143 us before the
+// forward pass and 152 before the backward one; 8 x 2048 tokens of 16 heads of
+// 64, float32, 129 and 137.
 #include "gdr_chunk.hpp"
 
 namespace qc {

@@ -15,12 +15,15 @@
 //
 // Bound by the chain of a sequence's chunks, not by bytes: a chunk is three
 // barriers with reads of LDS, MFMAs and splits of their results between them,
-// about 2 us for heads of 128 in bfloat16.  8192 tokens of 32 heads, 128 chunks
-// in line, 250 us; 12001 tokens of 16 heads in 29 packed sequences 216;
-// 4 x 4096 of 32 heads, saving states, 515, two rounds of blocks.  Set aside: eight waves of
-// half the columns' rows (more reads of LDS for the same products, slower);
-// no touches (431 us became 480 with the factors); 128 registers, for two
-// blocks to a CU (spills: 515 became 780).
+// about 2 us for heads of 128 in bfloat16.  Counters: matrix units 21% in use,
+// LDS 26%, waves at a wait or a barrier 43% of the time (two strips to a block:
+// 20, 31 and 60%).  8192 tokens of 32 heads, 128 chunks in line, 255 us; 12001
+// tokens of 16 heads in 29 packed sequences 216; 4 x 4096 of 32 heads, saving
+// states, 526, two rounds of blocks.  Registers: K = 128 in float32 spills 19 to
+// 27.  Set aside, measured on earlier forms of this kernel: eight waves of half
+// the columns' rows (more reads of LDS for the same products, slower); no
+// touches (431 us became 480 with the factors); 128 registers, for two blocks
+// to a CU (spills: 515 became 780).
 #include "gdr_chunk.hpp"
 
 namespace qc {

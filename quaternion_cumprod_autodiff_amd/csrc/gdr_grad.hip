@@ -9,13 +9,15 @@
 // half rh of the tokens; the 64 x 64 products X U^T, dO U^T are dealt by row
 // tiles.
 //
-// One block to a CU (its operand parts fill LDS).  It reads what the two passes
-// left, S0, dS1, U and X in float32: at 4 x 4096 tokens of 32 heads of 128 that
-// is 1.6 GB, 290 us at the rate of a copy, and the kernel takes 839 us
-// (8 x 2048 tokens of 16 heads of 64 by 128, float32: 428): bound by the phases of a block, loads and
-// splits, products, row sums, which one block to a CU does not overlap.  With
-// operands staged as plain rows and gathered, and row sums through LDS, it took
-// twice that.
+// One block to a CU: its operand parts fill LDS, and a wave takes up to all 256
+// registers (K = 128 spills: bfloat16 2, float16 22, float32 76).  It reads what
+// the two passes left, S0, dS1, U and X in float32: at 4 x 4096 tokens of 32
+// heads of 128 that is 1.6 GB, 290 us at the rate of a copy, and the kernel takes
+// 825 us (8 x 2048 tokens of 16 heads of 64 by 128, float32: 459): bound by the
+// phases of a block, loads and splits, products, row sums, which one block to a
+// CU does not overlap (matrix units 22% in use, LDS 18%, waves at a wait or a
+// barrier half of the time).  With operands staged as plain rows and gathered,
+// and row sums through LDS, it took twice that.
 #include "gdr_chunk.hpp"
 
 namespace qc {
