@@ -39,7 +39,9 @@
  * of its own and all later tokens of its sequence NaN, in the heads that read
  * it (a value: in its column), and the final state; a query its own token's;
  * what comes before is as without it.  The backward pass may return NaN for
- * any token of such a sequence.
+ * any token of such a sequence, and so may the forward pass for the tokens
+ * before in a chunk of 64 whose products leave the range of float32 (keys of
+ * 1e19, say).
  * States and gate gradients are float32; out and the gradients of query, key
  * and value are rounded once to the dtype.  Results do not depend on what else
  * runs, bit for bit.

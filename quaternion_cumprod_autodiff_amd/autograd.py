@@ -287,7 +287,9 @@ def gated_delta_rule(query, key, value, log_decay, beta, initial_state=None, *, 
     gradients.  A key, gate or value that is not finite makes the outputs of its
     own and all later tokens of its sequence NaN, in the heads that read it (a
     value: in its column), and the final state; a query its own token's.  What
-    comes before is as without it.  Gradients: anywhere in its sequence.
+    comes before is as without it, but in a chunk of 64 tokens whose products
+    leave the range of float32 (keys of 1e19, say).  Gradients: anywhere in its
+    sequence.
 
     With gradients, the float32 states and updates of every chunk of 64 tokens
     are kept from forward to backward: N ceil(T / 64) Hv (K' + 64) V' 4 bytes,

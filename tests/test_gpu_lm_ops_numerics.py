@@ -234,6 +234,19 @@ def test_a_batch_with_garbage_behind_each_end(dtype):
         assert torch.equal(out[n, :end], want[n, :end]) and not out[n, end:].isfinite().any()
 
 
+def test_a_packed_sequence_that_is_not_finite_leaves_the_others_alone():
+    clean = rule_inputs(1, 200, 2, 4, 40, 32, BF16, 2)
+    offsets = torch.tensor([0, 70, 71, 139, 200], dtype=torch.int32, device=DEV)
+    clean[5] = torch.cat([clean[5] * (n + 1) for n in range(4)])
+    want, want_state = gated_delta_rule(*clean, offsets=offsets)
+    args = [x.clone() for x in clean]
+    for x in args[:5]:
+        x[0, 71:139] = float("nan")
+    out, state = gated_delta_rule(*args, offsets=offsets)
+    assert torch.equal(out[:, :71], want[:, :71]) and torch.equal(out[:, 139:], want[:, 139:]) and out[:, 71:139].isnan().all()
+    assert torch.equal(state[[0, 1, 3]], want_state[[0, 1, 3]]) and state[2].isnan().all()
+
+
 def test_gradients_of_what_is_not_finite_are_not_finite():
     """Entering as zero is the forward pass' way alone: a loss that saw a NaN has no finite gradients of what led to it."""
     for which in (1, 2, 4):
