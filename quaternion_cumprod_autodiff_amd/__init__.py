@@ -16,7 +16,8 @@ def __getattr__(name):
     if name in ("quat_cumprod", "quat_cumprod_with_final", "QuatCumprodFunction", "scan", "ScanFunction",
                 "gated_deltanet2", "GatedDeltaNet2Function", "gated_delta_rule", "GatedDeltaRuleFunction",
                 "gated_delta_step", "qk_norm_rotate",
-                "QkNormRotateFunction"):
+                "QkNormRotateFunction", "decay_attention", "DecayAttentionFunction", "decay_attention_step", "layer_norm",
+                "LayerNormFunction"):
         from . import autograd
         return getattr(autograd, name)
     raise AttributeError(name)

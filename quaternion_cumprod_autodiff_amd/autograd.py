@@ -236,7 +236,8 @@ def gated_deltanet2(query, key, value, erase, write, log_decay, initial_state, *
 
 
 # ---------------------------------------------------------------------------
-# Language-model operators (include/gated_delta.h, include/qk_norm.h).
+# Language-model operators (include/gated_delta.h, include/qk_norm.h,
+# include/decay_attention.h, include/layer_norm.h).
 
 def _grads_wanted(*tensors) -> bool:
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
@@ -362,3 +363,117 @@ def qk_norm_rotate(query, key, query_weight=None, key_weight=None, cos=None, sin
     if _grads_wanted(query, key, query_weight, key_weight):
         return QkNormRotateFunction.apply(query, key, query_weight, key_weight, cos, sin, positions, kind, eps, interleaved)
     return capi.qkn_fwd(query, key, query_weight, key_weight, cos, sin, positions, kind=kind, eps=eps, interleaved=interleaved)
+
+
+class DecayAttentionFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, query, key, value, log_decay, initial_state, scale, offsets):
+        out, state, saved = capi.dca_fwd(query, key, value, log_decay, initial_state, scale=scale, offsets=offsets,
+                                         want_saved=True)
+        ctx.scale = scale
+        ctx.save_for_backward(query, key, value, log_decay, offsets, saved)
+        ctx.set_materialize_grads(False)
+        return out, state
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_out, d_state):
+        query, key, value, log_decay, offsets, saved = ctx.saved_tensors
+        if d_out is None and d_state is None:
+            return (None,) * 7
+        d_out = torch.zeros(value.shape, dtype=value.dtype, device=value.device) if d_out is None else d_out.contiguous()
+        grads = capi.dca_bwd(query, key, value, log_decay, saved, d_out,
+                             None if d_state is None else d_state.contiguous(), scale=ctx.scale, offsets=offsets,
+                             want=ctx.needs_input_grad[:5])
+        return (*grads, None, None)
+
+
+def decay_attention(query, key, value, log_decay, initial_state=None, *, scale=None, offsets=None):
+    """(out [B, T, Hv, V], final states [N, Hv, K, V]) of linear attention with
+    decays, differentiable in its five tensors.  Per sequence and value head h,
+    which reads query and key head h // (Hv / Hk):
+
+        S = exp(log_decay_t) S + key_t value_t^T;  out_t = scale S^T query_t
+
+    query, key [B, T, Hk, K] and value [B, T, Hv, V]: float32, bfloat16 or
+    float16, any strides; log_decay (at most zero; -inf clears a finite state)
+    [B, T, Hv], or [Hv] for one decay of each head, initial_state
+    [N, Hv, K, V] (None: zeros) and the final states float32; K <= 128,
+    V <= 1024.  scale defaults to K ** -0.5.
+
+    Without ``offsets`` N = B.  With them (int32 [N + 1] on the GPU, ascending,
+    within 0 .. T), B is 1 and sequence n is rows offsets[n] .. offsets[n + 1]
+    - 1, of any length down to zero; rows of no sequence have zero out and zero
+    gradients.  A key, decay or value that is not finite reaches its own and
+    later tokens of its sequence and the final state, in the heads that read it
+    (a value: in its column); a query its own token; what comes before is as
+    without it.  Gradients: anywhere in its sequence.
+
+    With gradients, the float32 states of every chunk of 64 tokens (bfloat16;
+    32 for the other types) are kept from forward to backward:
+    N ceil(T / 64) Hv K' V' 4 bytes, K' = 32, 64 or 128 and V' a multiple of 64
+    (of 128 from 65 on); the backward pass takes as much again while it runs.
+
+    Forward and backward can be captured into a graph, as for
+    :func:`gated_delta_rule`."""
+    _refuse_forward_mode("decay_attention", query, key, value, log_decay, initial_state)
+    query, key, value, log_decay = _last_dense(query), _last_dense(key), _last_dense(value), log_decay.contiguous()
+    scale = None if scale is None else float(scale)
+    if initial_state is not None:
+        initial_state = initial_state.contiguous()
+    if _grads_wanted(query, key, value, log_decay, initial_state):
+        return DecayAttentionFunction.apply(query, key, value, log_decay, initial_state, scale, offsets)
+    return capi.dca_fwd(query, key, value, log_decay, initial_state, scale=scale, offsets=offsets)[:2]
+
+
+def decay_attention_step(query, key, value, log_decay, state, *, slots=None, scale=None):
+    """One or a few new tokens of linear attention with decays
+    (:func:`decay_attention`) for each batch row, for decoding: query, key
+    [B, T, Hk, K], value [B, T, Hv, V], log_decay [B, T, Hv] or [Hv] float32.
+    ``state``, a pool [slots, Hv, K, V] float32, is updated in place; row n
+    uses state slots[n] (int32; without ``slots`` state n).  Returns out
+    [B, T, Hv, V].  A row whose slot is outside the pool (-1 for padding) or
+    named by an earlier row is not run: its out is zero.  Not differentiable; a
+    graph that saved the pool before raises in its backward pass, as after any
+    operation in place."""
+    _refuse_forward_mode("decay_attention_step", query, key, value, log_decay, state)
+    if _grads_wanted(query, key, value, log_decay, state):
+        raise ValueError("decay_attention_step updates its states in place and has no gradient: use decay_attention")
+    return capi.dca_step(query, key, value, log_decay, state, slots, scale=scale)
+
+
+class LayerNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, stats = capi.lnm_fwd(x, weight, bias, eps=eps, want_stats=True)
+        ctx.eps = eps
+        ctx.save_for_backward(x, weight, bias, stats)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_y):
+        x, weight, bias, stats = ctx.saved_tensors
+        return (*capi.lnm_bwd(x, weight, bias, stats, d_y.contiguous(), eps=ctx.eps, want=ctx.needs_input_grad[:3]), None)
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
+    """(x - mean) / sqrt(variance + eps) * weight + bias over x's last axis, in
+    one pass, differentiable in its three tensors.
+
+    x: float32, bfloat16 or float16, any strides (views of a fused projection
+    are read in place), rows of 1 to 16384 elements; weight and bias of the
+    same dtype, [D], or [H, D] for an x [.., H, D] whose heads have weights of
+    their own (both alike); None: ones, zeros.  Statistics are float32, the
+    variance from the differences to the mean.  Capturing a backward pass: as
+    for :func:`gated_delta_rule`."""
+    _refuse_forward_mode("layer_norm", x, weight, bias)
+    x, eps = _last_dense(x), float(eps)
+    shape = x.shape
+    if x.dim() > 4:
+        x = x.reshape(-1, *shape[-3:])
+    if _grads_wanted(x, weight, bias):
+        y = LayerNormFunction.apply(x, weight, bias, eps)
+    else:
+        y = capi.lnm_fwd(x, weight, bias, eps=eps)[0]
+    return y if len(shape) <= 4 else y.reshape(shape)

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libquatcumprod.so")
 SOURCES = ["qc_kernels.hip", "qc_abi.cpp", "qc_scan.hip", "qc_scan_schedule.cpp", "gdn2.hip", "gdn2_wy.hip", "qc_copy.hip", "qc_noalloc.hip",
-           "gdr_api.cpp", "gdr_factor.hip", "gdr_fwd.hip", "gdr_bwd.hip", "gdr_grad.hip", "gdr_step.hip", "qk_norm.hip"]
+           "gdr_api.cpp", "gdr_factor.hip", "gdr_fwd.hip", "gdr_bwd.hip", "gdr_grad.hip", "gdr_step.hip", "qk_norm.hip",
+           "dca_api.cpp", "dca_fwd.hip", "dca_state.hip", "dca_grad.hip", "dca_step.hip", "layer_norm.hip"]
 ARCH = "gfx950"
 NOISE = "is not a recognized feature for this target"
 

@@ -50,6 +50,9 @@ EXPORTS = (
 # Of the language-model operators: include/gated_delta.h and include/qk_norm.h.
 LM_EXPORTS = ("gdr_saved_bytes", "gdr_workspace_bytes", "gdr_fwd", "gdr_bwd", "gdr_step", "qkn_fwd", "qkn_workspace_bytes", "qkn_bwd")
 
+# And of include/decay_attention.h and include/layer_norm.h.
+LAYER_EXPORTS = ("dca_saved_bytes", "dca_workspace_bytes", "dca_fwd", "dca_bwd", "dca_step", "lnm_fwd", "lnm_workspace_bytes", "lnm_bwd")
+
 
 class QcOptions(ctypes.Structure):
     _fields_ = [("path", ctypes.c_int32), ("lookback", ctypes.c_int32), ("leaves", ctypes.c_int32),
@@ -72,6 +75,18 @@ class QknDims(ctypes.Structure):
         ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
         ("dtype", ctypes.c_int32), ("kind", ctypes.c_int32), ("interleaved", ctypes.c_int32),
         ("positions64", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class DcaDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "Hk", "Hv", "K", "V", "N")] + [
+        ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("packed", ctypes.c_int32), ("head_decay", ctypes.c_int32)]
+
+
+class LnmDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "H", "D")] + [
+        ("x_stride", ctypes.c_int64 * 3), ("dtype", ctypes.c_int32), ("by_head", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("reserved", ctypes.c_int32)]
 
 
 class QuatCumprodError(RuntimeError):
@@ -169,6 +184,23 @@ def load(path: str | None = None):
         lib.qkn_workspace_bytes.restype = sz
         lib.qkn_bwd.argtypes = [qkn] + [vp] * 14 + [sz, vp]
         lib.qkn_bwd.restype = ctypes.c_int
+        dca, lnm = ctypes.POINTER(DcaDims), ctypes.POINTER(LnmDims)
+        lib.dca_saved_bytes.argtypes = [dca]
+        lib.dca_saved_bytes.restype = sz
+        lib.dca_workspace_bytes.argtypes = [dca, i32]
+        lib.dca_workspace_bytes.restype = sz
+        lib.dca_fwd.argtypes = [dca] + [vp] * 10 + [sz, vp]
+        lib.dca_fwd.restype = ctypes.c_int
+        lib.dca_bwd.argtypes = [dca] + [vp] * 14 + [sz, vp]
+        lib.dca_bwd.restype = ctypes.c_int
+        lib.dca_step.argtypes = [dca] + [vp] * 5 + [i64, i64] + [vp] * 3
+        lib.dca_step.restype = ctypes.c_int
+        lib.lnm_fwd.argtypes = [lnm] + [vp] * 6
+        lib.lnm_fwd.restype = ctypes.c_int
+        lib.lnm_workspace_bytes.argtypes = [lnm]
+        lib.lnm_workspace_bytes.restype = sz
+        lib.lnm_bwd.argtypes = [lnm] + [vp] * 8 + [sz, vp]
+        lib.lnm_bwd.restype = ctypes.c_int
         if path is None:
             _lib = lib
         return lib
@@ -1032,4 +1064,208 @@ def qkn_bwd(query, key, query_weight, key_weight, cos, sin, positions, d_query_o
                         _data_ptr(sin), _data_ptr(positions), d_query_out.data_ptr(), d_key_out.data_ptr(),
                         *[_data_ptr(g) for g in grads], _data_ptr(ws), nbytes, torch.cuda.current_stream(device).cuda_stream)
     _check(rc, "qkn_bwd")
+    return tuple(grads)
+
+
+# ---------------------------------------------------------------------------
+# Linear attention with a decay for each head (include/decay_attention.h) and
+# layer norm (include/layer_norm.h), with the same conventions.
+
+def _dca_dims(query, key, value, n, scale, head_decay):
+    like = _gdr_dims(query, key, value, n, scale)          # the gated delta rule's shapes and checks
+    d = DcaDims(*[getattr(like, x) for x in ("B", "T", "Hk", "Hv", "K", "V", "N")])
+    d.q_stride, d.k_stride, d.v_stride = like.q_stride, like.k_stride, like.v_stride
+    d.dtype, d.scale, d.packed, d.head_decay = like.dtype, like.scale, like.packed, int(head_decay)
+    return d
+
+
+def _dca_plan(query, key, value, log_decay, n, scale):
+    scale = None if scale is None else float(scale)
+    by_head = log_decay.dim() == 1
+    d = _lm_plan((2, query.shape, key.shape, value.shape, query.stride(), key.stride(), value.stride(), query.dtype,
+                  key.dtype, value.dtype, query.device, key.device, value.device, n, scale, by_head),
+                 lambda: _dca_dims(query, key, value, n, scale, by_head))
+    _lm_dense("log_decay", log_decay, (d.Hv,) if by_head else (d.B, d.T, d.Hv), torch.float32, query.device)
+    return d
+
+
+def _dca_whole(query, key, value, log_decay, offsets, scale):
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.numel() < 1:
+            raise ValueError(f"offsets must hold a number more than there are sequences, got {tuple(offsets.shape)}")
+        _lm_dense("offsets", offsets, (offsets.numel(),), torch.int32, query.device)
+    return _dca_plan(query, key, value, log_decay, None if offsets is None else offsets.numel() - 1, scale)
+
+
+def dca_fwd(query, key, value, log_decay, initial_state=None, *, scale=None, offsets=None, want_saved=False, out=None,
+            stream=None):
+    """(out, final states [N, Hv, K, V], saved state for dca_bwd or None) of
+    linear attention with decays, log_decay [B, T, Hv] or [Hv].  With
+    ``offsets`` (int32 [N + 1]) B is 1 and the rows are packed sequences; rows
+    of none are left as they were in a given ``out``, and zero in a new one."""
+    device = query.device
+    if query.is_cuda and _lm_elsewhere(device, stream):
+        return _lm_there(device, stream, dca_fwd, query, key, value, log_decay, initial_state, scale=scale,
+                         offsets=offsets, want_saved=want_saved, out=out)
+    d = _dca_whole(query, key, value, log_decay, offsets, scale)
+    states = (d.N, d.Hv, d.K, d.V)
+    if initial_state is not None:
+        _lm_dense("initial_state", initial_state, states, torch.float32, device)
+    lib = load()
+    ws_bytes = lib.dca_workspace_bytes(d, 0)
+    if ws_bytes == 0:
+        raise QuatCumprodError(-2, "dca_fwd")
+    shape, given = (d.B, d.T, d.Hv, d.V), out
+    if out is None:
+        out = (torch.empty if offsets is None else torch.zeros)(shape, dtype=query.dtype, device=device)
+    else:
+        _lm_dense("out", out, shape, query.dtype, device)
+    fin = torch.empty(states, dtype=torch.float32, device=device)
+    saved = torch.empty(lib.dca_saved_bytes(d), dtype=torch.uint8, device=device) if want_saved else None
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    rc = lib.dca_fwd(d, query.data_ptr(), key.data_ptr(), value.data_ptr(), log_decay.data_ptr(), _data_ptr(offsets),
+                     _data_ptr(initial_state), out.data_ptr(), fin.data_ptr(), _data_ptr(saved), ws.data_ptr(), ws_bytes,
+                     torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, "dca_fwd")
+    _lm_written(given)
+    return out, fin, saved
+
+
+def dca_bwd(query, key, value, log_decay, saved, d_out, d_final_state=None, *, scale=None, offsets=None,
+            want=(True,) * 5, stream=None):
+    """Gradients (query, key, value, log_decay, initial_state); those not
+    wanted are None.  ``saved`` is dca_fwd's third output for the same inputs.
+    Rows of no sequence have zero gradients."""
+    device = query.device
+    if query.is_cuda and _lm_elsewhere(device, stream):
+        return _lm_there(device, stream, dca_bwd, query, key, value, log_decay, saved, d_out, d_final_state, scale=scale,
+                         offsets=offsets, want=want)
+    d = _dca_whole(query, key, value, log_decay, offsets, scale)
+    states = (d.N, d.Hv, d.K, d.V)
+    _lm_dense("d_out", d_out, (d.B, d.T, d.Hv, d.V), query.dtype, device)
+    if d_final_state is not None:
+        _lm_dense("d_final_state", d_final_state, states, torch.float32, device)
+    lib = load()
+    _lm_dense("saved", saved, (lib.dca_saved_bytes(d),), torch.uint8, device)
+    new = torch.empty if offsets is None else torch.zeros
+    grads = [new(t.shape, dtype=t.dtype, device=device) if w else None
+             for t, w in zip((query, key, value, log_decay), want)]
+    grads.append(torch.empty(states, dtype=torch.float32, device=device) if want[4] else None)
+    ws_bytes = lib.dca_workspace_bytes(d, 1)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    rc = lib.dca_bwd(d, query.data_ptr(), key.data_ptr(), value.data_ptr(), log_decay.data_ptr(), _data_ptr(offsets),
+                     saved.data_ptr(), d_out.data_ptr(), _data_ptr(d_final_state), *[_data_ptr(g) for g in grads],
+                     ws.data_ptr(), ws_bytes, torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, "dca_bwd")
+    return tuple(grads)
+
+
+def dca_step(query, key, value, log_decay, state, slots=None, *, scale=None, out=None, stream=None):
+    """One or a few tokens of linear attention with decays for each batch row,
+    on a pool of states [slots, Hv, K, V] float32 that is updated in place;
+    returns out [B, T, Hv, V].  log_decay [B, T, Hv] or [Hv].  Slots as for
+    gdr_step."""
+    device = query.device
+    if query.is_cuda and _lm_elsewhere(device, stream):
+        return _lm_there(device, stream, dca_step, query, key, value, log_decay, state, slots, scale=scale, out=out)
+    d = _dca_plan(query, key, value, log_decay, None, scale)
+    if (state.dim() != 4 or state.shape[1:] != (d.Hv, d.K, d.V) or state.dtype != torch.float32 or state.device != device
+            or not (state.is_contiguous() or (state.shape[0] > 0 and state[0].is_contiguous()))):
+        raise ValueError(f"state must be float32 [slots, {d.Hv}, {d.K}, {d.V}] on {device} with dense slots, "
+                         f"got {state.dtype} {tuple(state.shape)} on {state.device}")
+    if slots is not None:
+        _lm_dense("slots", slots, (d.B,), torch.int32, device)
+    elif state.shape[0] < d.B:
+        raise ValueError(f"state must have a slot for each of {d.B} rows, got {state.shape[0]}")
+    shape, given = (d.B, d.T, d.Hv, d.V), out
+    if out is None:
+        out = torch.empty(shape, dtype=query.dtype, device=device)
+    else:
+        _lm_dense("out", out, shape, query.dtype, device)
+    rc = load().dca_step(d, query.data_ptr(), key.data_ptr(), value.data_ptr(), log_decay.data_ptr(), state.data_ptr(),
+                         state.shape[0], state.stride(0) if state.shape[0] > 1 else d.Hv * d.K * d.V, _data_ptr(slots),
+                         out.data_ptr(), torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, "dca_step")
+    _lm_written(state, given)
+    return out
+
+
+def _lnm_dims(x, by_head, eps):
+    if x.dim() < 1 or x.dim() > 4:
+        raise ValueError(f"x must have one to four axes, got {tuple(x.shape)}")
+    if x.dtype not in _LM_DTYPES:
+        raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
+    if x.shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError("x must be dense along its last axis")
+    if not x.is_cuda:
+        raise ValueError("x must live on the GPU: there is no CPU path")
+    if not 1 <= x.shape[-1] <= 16384:
+        raise ValueError(f"rows must have 1..16384 elements, got {x.shape[-1]}")
+    if not eps >= 0:
+        raise ValueError(f"eps must be >= 0, got {eps}")
+    if by_head and x.dim() < 2:
+        raise ValueError(f"weights of heads need an x [.., heads, elements], got {tuple(x.shape)}")
+    # [B, T, H, D]: heads of their own weights are the third axis, and so is the axis of a fourth; otherwise H is 1.
+    lead, st = list(x.shape[:-1]), list(x.stride()[:-1])
+    if not by_head and len(lead) < 3:
+        lead, st = lead + [1], st + [x.shape[-1]]
+    while len(lead) < 3:
+        lead, st = [1] + lead, [0] + st
+    d = LnmDims(*lead, x.shape[-1])
+    d.x_stride[:] = st
+    d.dtype, d.by_head, d.eps = _LM_DTYPES[x.dtype], int(by_head), eps
+    return d
+
+
+def _lnm_plan(x, weight, bias, eps):
+    eps, first = float(eps), weight if weight is not None else bias
+    by_head = first is not None and first.dim() == 2
+    d = _lm_plan((3, x.shape, x.stride(), x.dtype, x.device, by_head, eps), lambda: _lnm_dims(x, by_head, eps))
+    shape = (d.H, d.D) if by_head else (d.D,)
+    for name, w in (("weight", weight), ("bias", bias)):
+        if w is not None:
+            _lm_dense(name, w, shape, x.dtype, x.device)
+    return d
+
+
+def lnm_fwd(x, weight=None, bias=None, *, eps=1e-5, want_stats=False, out=None, stream=None):
+    """(y, stats for lnm_bwd or None): layer norm over x's last axis, see
+    include/layer_norm.h.  x has one to four axes, its last dense; weight and
+    bias [D], or [H, D] for an x [.., H, D].  y is contiguous."""
+    device = x.device
+    if x.is_cuda and _lm_elsewhere(device, stream):
+        return _lm_there(device, stream, lnm_fwd, x, weight, bias, eps=eps, want_stats=want_stats, out=out)
+    d = _lnm_plan(x, weight, bias, eps)
+    given = out
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+    else:
+        _lm_dense("out", out, x.shape, x.dtype, device)
+    stats = torch.empty((d.B * d.T * d.H, 4), dtype=torch.float32, device=device) if want_stats else None
+    rc = load().lnm_fwd(d, x.data_ptr(), _data_ptr(weight), _data_ptr(bias), out.data_ptr(), _data_ptr(stats),
+                        torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, "lnm_fwd")
+    _lm_written(given)
+    return out, stats
+
+
+def lnm_bwd(x, weight, bias, stats, d_out, *, eps=1e-5, want=(True, True, True), stream=None):
+    """Gradients (x, weight, bias) of lnm_fwd; those not wanted, and those of
+    an absent weight or bias, are None.  ``stats`` is lnm_fwd's second output
+    for the same x."""
+    device = x.device
+    if x.is_cuda and _lm_elsewhere(device, stream):
+        return _lm_there(device, stream, lnm_bwd, x, weight, bias, stats, d_out, eps=eps, want=want)
+    d = _lnm_plan(x, weight, bias, eps)
+    _lm_dense("d_out", d_out, x.shape, x.dtype, device)
+    _lm_dense("stats", stats, (d.B * d.T * d.H, 4), torch.float32, device)
+    grads = [torch.empty(t.shape, dtype=t.dtype, device=device) if t is not None and w else None
+             for t, w in zip((x, weight, bias), want)]
+    ws, nbytes = None, 0
+    if grads[1] is not None or grads[2] is not None:
+        nbytes = int(load().lnm_workspace_bytes(d))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    rc = load().lnm_bwd(d, x.data_ptr(), _data_ptr(weight), stats.data_ptr(), d_out.data_ptr(),
+                        *[_data_ptr(g) for g in grads], _data_ptr(ws), nbytes, torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, "lnm_bwd")
     return tuple(grads)

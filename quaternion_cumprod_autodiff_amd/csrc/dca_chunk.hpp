@@ -1,0 +1,303 @@
+// dca_chunk.hpp -- the chunked form of linear attention with decays
+// (include/decay_attention.h): its mathematics, its internal formats and the
+// device helpers that its kernels share.  Not installed.
+//
+// Chunks of C tokens, 64 for bfloat16 and 32 for the types of several parts.
+// With G_i the log decays cumulated from the chunk's start, gamma_i = exp(G_i),
+// eta_i = exp(G_last - G_i), Gam_ij = exp(G_i - G_j), and S0 the state before
+// the chunk,
+//     P_ij = Gam_ij q_i.k_j (i >= j)
+//     out = scale (gamma (Q S0) + P V)
+//     S1  = gamma_last S0 + K^T (eta V)
+// and, for cotangents dO of out (O = scale dO) and dS1 of S1,
+//     Phi_ij = Gam_ij O_i.V_j (i >= j)
+//     dQ  = gamma (O S0^T) + Phi K
+//     dK  = eta (V dS1^T) + Phi^T Q
+//     dV  = eta (K dS1) + P^T O
+//     dS0 = gamma_last dS1 + Q^T (gamma O)
+//     dg_t = gamma_last <S0, dS1> + sum_{i >= t} gamma_i q_i.(O S0^T)_i
+//            + sum_{j < t} eta_j k_j.(V dS1^T)_j + sum_{i >= t > j} Phi_ij q_i.k_j
+// All exponents are of differences that decays keep at or below zero, and every
+// term of dg_t carries exp(g_t): by additions alone a strong decay's gradient
+// is not the rounding of larger terms that cancel.
+//
+// Nothing in a chunk but S0 depends on the chunk before, and S0 linearly.  So
+// where sequences and heads alone leave CUs idle, a sequence is cut into
+// segments of whole chunks: dca_state sums what each segment adds to a state
+// that starts from zero, dca_join carries the states over the segments, and
+// then every segment runs from its own.  dca_fwd passes over a segment with S
+// in registers (and leaves S0 of every chunk for a backward pass), dca_state
+// likewise with dS from its end, dca_grad takes every chunk at once.
+//
+// Arithmetic.  All products are v_mfma_f32_16x16x32_bf16 on operands split into
+// bfloat16 parts: inputs whole (one part for bfloat16, two for float16, three
+// for float32), computed operands in three, or in two on the way to an output
+// that is rounded to 16 bits.
+//
+// Layouts.  A lane l = 16 g + m holds of an operand fragment row m (A) or column
+// m (B) and the 8 consecutive indices 32 b + 8 g + .. of the contracted axis'
+// block b; of a product column m and rows 4 g + 0..3.  Rows of tiles 2b and
+// 2b + 1 stand for the indices 8 (m / 4) + 4 (tile % 2) + m % 4 of block b, so
+// that a lane's accumulators of both are 8 consecutive indices: results become
+// operands without a transpose.  In LDS lie the chunk's rows as they come, token
+// by token, each part for itself, 16-byte pieces swapped within a row so that
+// 16 rows' pieces lie in all banks; fragments along a row are 16-byte reads,
+// those across tokens two transposing reads of 4 tokens each.
+#pragma once
+
+#include "decay_attention.h"
+#include "gdr_chunk.hpp"
+
+namespace qc {
+
+constexpr int dca_chunk(int dt) { return dt == 1 ? 64 : 32; }
+constexpr int dca_parts(int dt) { return dt == 0 ? 3 : 2; }        // of operands computed on the way to an output
+
+struct DcaArgs {
+    const void *q, *k, *v;
+    const float *g, *s0;
+    const int32_t* offsets;
+    void* out;
+    float* fin;
+    float* save;                        // S0 of every chunk: [slots][Hv][KP][VP] (or null)
+    float* seg;                         // workspace: states at segments' starts (backward: dS at their ends), as save
+    float* seg_decay;                   // workspace: [segment slots][Hv]
+    const void* d_out;
+    const float* d_fin;
+    void *dq, *dk, *dv;
+    float *dg, *ds0;
+    float* ds;                          // workspace: dS1 of every chunk
+    float* dg_part;                     // workspace: sums of dg over chunks [slots][Hv], for decays of the head alone
+    int64_t qs[3], ks[3], vs[3], gs[3]; // gs: of log_decay, zeros for batch and token where it is of the head alone
+    int64_t T, N, chunks, segs;         // chunks, segs: per sequence, without offsets
+    int64_t slots, seg_slots, seg_tokens;
+    int Hk, Hv, group, K, V, VP, tiles; // tiles: blocks of 64 CT columns of V
+    int vec_qk, vec_v, vec_o;           // rows on 16 bytes and sizes multiples of 8
+    float scale;
+};
+
+hipError_t launch_dca_fwd(int dt, int kb, int ct, const DcaArgs& a, hipStream_t st);
+hipError_t launch_dca_state(int dt, int kb, int ct, bool rev, bool sum, const DcaArgs& a, hipStream_t st);
+hipError_t launch_dca_join(int dt, int kb, bool rev, const DcaArgs& a, hipStream_t st);
+hipError_t launch_dca_grad(int dt, int kb, int ct, const DcaArgs& a, hipStream_t st);
+hipError_t launch_dca_heads(const DcaArgs& a, float* out, hipStream_t st);
+
+// Calls f(dtype, blocks of K, column tiles of a wave) with all as constants.
+template <class F>
+hipError_t by_dca_shape(int dt, int kb, int ct, F&& f) {
+    return by_dtype_kb(dt, kb, [&](auto d, auto k) {
+        return ct == 1 ? f(d, k, std::integral_constant<int, 1>{}) : f(d, k, std::integral_constant<int, 2>{});
+    });
+}
+
+// Device helpers ----------------------------------------------------------------
+
+struct Span {
+    int64_t b, t0, slot, seg;          // first token, first chunk's slot, first segment's slot
+    int len;
+};
+
+template <int C>
+__device__ __forceinline__ Span span_of(const DcaArgs& a, int64_t n) {
+    if (!a.offsets) return {n, 0, n * a.chunks, n * a.segs, int(a.T)};
+    int64_t lo = a.offsets[n], hi = a.offsets[n + 1];
+    lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
+    hi = hi < lo ? lo : hi > a.T ? a.T : hi;
+    // Consecutive sequences' slots cannot meet: floor((lo + len) / s) + 1 >= floor(lo / s) + max(1, ceil(len / s)).
+    return {0, lo, lo / C + n, lo / a.seg_tokens + n, int(hi - lo)};
+}
+
+__device__ __forceinline__ int segments_of(const DcaArgs& a, const Span& s) {
+    const int n = int((s.len + a.seg_tokens - 1) / a.seg_tokens);
+    return n > 1 ? n : 1;
+}
+
+// The last sequence whose first slot (of chunks, or of segments) is at or before this one.
+template <int C, bool SEG>
+__device__ __forceinline__ int64_t owner(const DcaArgs& a, int64_t slot) {
+    if (!a.offsets) return slot / (SEG ? a.segs : a.chunks);
+    int64_t lo = 0, hi = a.N - 1;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) / 2;
+        const Span s = span_of<C>(a, mid);
+        if ((SEG ? s.seg : s.slot) <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Blocks that share a key head's rows run on one XCD (block % 8), next to each other in time.
+__device__ __forceinline__ bool dca_unit(int64_t units, int per, int64_t& u, int& s) {
+    u = blockIdx.x / (8 * int64_t(per)) * 8 + blockIdx.x % 8;
+    s = int(blockIdx.x / 8 % per);
+    return u < units;
+}
+
+// W columns of C tokens in LDS: the byte of piece `p` (8 columns) of a token.
+template <int W>
+__device__ __forceinline__ int lds_piece(int token, int p) {
+    constexpr int kPieces = W / 8, kRows = kPieces >= 16 ? 1 : 16 / kPieces;
+    return token * (W * 2) + ((p ^ ((token / kRows) & (kPieces - 1))) << 4);
+}
+
+// A fragment along a row: pieces 4 b + g of a token, every part.
+template <int C, int W, int NP>
+__device__ __forceinline__ void row_fragment(const char* t, int token, int b, int g, bf16x8 (&x)[NP]) {
+    const int at = lds_piece<W>(token, 4 * b + g);
+#pragma unroll
+    for (int n = 0; n < NP; ++n) x[n] = *reinterpret_cast<const bf16x8*>(t + n * (C * W * 2) + at);
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Four rows' element of column m, from pieces of 4 columns: lane 4 r + q names piece q of row r.
+__device__ __forceinline__ s16x4 read_transposed(const char* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
+}
+
+__device__ __forceinline__ bf16x8 joined(s16x4 lo, s16x4 hi) {
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+}
+
+// A fragment across tokens 32 b + 8 g + ..: `col` is the first of the four columns of the piece that this
+// lane names, m % 4; it gets column m % 4 of piece m / 4.
+template <int C, int W, int NP>
+__device__ __forceinline__ void col_fragment(const char* t, int b, int g, int m, int col, bf16x8 (&x)[NP]) {
+    const int t0 = 32 * b + 8 * g + (m >> 2);
+    const int lo = lds_piece<W>(t0, col >> 3) + (col & 7) * 2, hi = lds_piece<W>(t0 + 4, col >> 3) + (col & 7) * 2;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) x[n] = joined(read_transposed(t + n * (C * W * 2) + lo), read_transposed(t + n * (C * W * 2) + hi));
+}
+
+// Fragments of P and Phi in LDS: row tile i (16 tokens) and block b (32 tokens) at or before it.
+constexpr int dca_tri(int c) { return c == 64 ? 6 : 2; }
+__device__ __forceinline__ int tri_of(int i, int b) { return i < 2 ? i : 2 * i - 2 + b; }
+
+// The same across rows: column tile j's tokens 16 j + m, rows 32 b + 8 g + .. .
+template <int NP>
+__device__ __forceinline__ void tri_cols(const bf16x8 (*p)[NP][64], int b, int g, int m, int j, bf16x8 (&x)[NP]) {
+    const int i = 32 * b + 8 * g + (m >> 2), col = 16 * j + 4 * (m & 3);
+    const bf16x8(*f)[64] = p[tri_of(i >> 4, j >> 1)];
+    const int at = (((col >> 3) & 3) * 16 + (i & 15)) * 16 + (col & 4) * 2;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        const char* s = reinterpret_cast<const char*>(f[n]) + at;
+        x[n] = joined(read_transposed(s), read_transposed(s + 64));
+    }
+}
+
+// C tokens of W columns on their way from memory to LDS, by 256 threads: loaded
+// in one place, taken apart and stored in a later one.  Tokens from `rem` on and
+// columns from `width` on are zero.  vec: rows on 16 bytes, width a multiple of 8.
+template <int DT, int C, int W>
+struct Rows {
+    using E = typename Storage<DT>::type;
+    static constexpr int kAll = C * W / 8, kMine = (kAll + 255) / 256, kWords = 8 * sizeof(E) / 16, kPer = 16 / sizeof(E);
+    typedef E Piece __attribute__((ext_vector_type(16 / sizeof(E))));
+    Piece x[kMine][kWords];
+
+    __device__ __forceinline__ void load(const E* p, int64_t stride, int rem, int width, bool vec, int tid) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int at = tid + i * 256, token = at / (W / 8), c = at % (W / 8) * 8;
+            const bool in = (kAll % 256 == 0 || at < kAll) && token < rem && c < width;
+            const E* s = p + token * stride + c;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                if (vec) {
+                    x[i][w] = in ? reinterpret_cast<const Piece*>(s)[w] : Piece(E(0.f));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) x[i][w][j] = in && c + w * kPer + j < width ? s[w * kPer + j] : E(0.f);
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store(char* t, int tid) const {
+        constexpr int NP = parts_of(DT);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int at = tid + i * 256, token = at / (W / 8), c = at % (W / 8);
+            if (kAll % 256 && at >= kAll) continue;
+            bf16x8 y[NP];
+            if constexpr (DT == 1) {
+                y[0] = x[i][0];
+            } else {
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = float(x[i][j / kPer][j % kPer]);
+                split<NP, 8>(f, y);
+            }
+#pragma unroll
+            for (int n = 0; n < NP; ++n) *reinterpret_cast<bf16x8*>(t + n * (C * W * 2) + lds_piece<W>(token, c)) = y[n];
+        }
+    }
+};
+
+// A chunk's decays, in LDS.  cum is in units of log 2, for exp2.
+template <int C>
+struct Decays {
+    double cum[C];
+    float gamma[C], eta[C];
+};
+
+__device__ __forceinline__ float exp2_of(double x) { return __builtin_amdgcn_exp2f(float(x)); }
+
+// Lane t's cumulated log2 decay from its token's log decay.
+template <int C>
+__device__ __forceinline__ double cumulated(float g, int lane) {
+    double x = double(g < -1e4f ? -1e4f : g) * 1.4426950408889634;
+#pragma unroll
+    for (int i = 1; i < C; i *= 2) {
+        const double y = __shfl_up(x, i, 64);
+        if (lane >= i) x += y;
+    }
+    return x;
+}
+
+// One wave: lane t's token (lanes from C on: none, g zero).  Returns the chunk's whole log2 decay.
+template <int C>
+__device__ __forceinline__ double put_decays(Decays<C>& d, float g, int lane) {
+    const double x = cumulated<C>(g, lane), last = __shfl(x, C - 1, 64);
+    if (lane < C) {
+        d.cum[lane] = x;
+        d.gamma[lane] = exp2_of(x);
+        d.eta[lane] = exp2_of(last - x);
+    }
+    return last;
+}
+
+// Eight consecutive floats of LDS.
+__device__ __forceinline__ void read8(const float* p, float (&x)[8]) {
+    const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[j] = a[j];
+        x[4 + j] = b[j];
+    }
+}
+
+// The sum of an operand's parts, element by element: exact.
+template <int NP>
+__device__ __forceinline__ void whole(const bf16x8 (&p)[NP], float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        x[j] = float(p[NP - 1][j]);
+#pragma unroll
+        for (int n = NP - 2; n >= 0; --n) x[j] += float(p[n][j]);
+    }
+}
+
+// gamma-weighted pairs of row tile i and block b from their products (pt: tiles 2 b and 2 b + 1, tokens 32 b + 8 g
+// + .. by row, 16 i + m by column): what lies above the diagonal is zero, whatever the product.
+template <int C>
+__device__ __forceinline__ void decayed_pairs(const Decays<C>& d, const f32x4 (&pt)[2], int i, int b, int g, int m, float factor, float (&x)[8]) {
+    const int row = 16 * i + m, first = 32 * b + 8 * g;
+    const double at = d.cum[row];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = first + j <= row ? exp2_of(at - d.cum[first + j]) * (pt[j >> 2][j & 3] * factor) : 0.f;
+}
+
+}  // namespace qc

@@ -1,0 +1,448 @@
+// layer_norm.hip -- layer norm over the last axis and its VJP (include/layer_norm.h).
+//
+// Forward, per row x [D]: mean = sum x / D, d = x - mean, m = sum d / D (what
+// rounding left in the mean), v = sum d^2 / D - m^2, r = 1 / sqrt(v + eps),
+// h = (d - m) r, y = h w + b.  VJP, with the cotangent g of y: dh = g w,
+//     dx = r (dh - sum(dh) / D - h sum(dh h) / D),   dw = sum of g h,   db = sum of g
+// over the rows.  Statistics and sums are float32; the mean is kept as (mean, m),
+// so that rows far from zero have the forward's differences in the VJP.
+//
+// Bound by memory: every element is read once (twice as x and g in the VJP) and
+// written once, so TR threads hold a row in registers between the sums and the
+// result, S runs of W consecutive elements each: W = 8 where rows lie on 16
+// bytes, else 1.  Rows of up to 512 elements (W = 8) share a wave with others.
+#include "layer_norm.h"
+#include "lm_common.hpp"
+#include "qc_internal.hpp"
+#include "quat_cumprod.h"
+
+#include <type_traits>
+
+namespace qc {
+namespace {
+
+constexpr int kLnThreads = 256;                // threads of a block, or TR if that is more
+constexpr int kLnMaxD = 16384;
+// Blocks that share a weight gradient's sum, for all heads together: enough to
+// fill 256 CUs several times, few enough that their partial sums are short.
+constexpr int64_t kLnPartials = 1024;
+
+struct LnArgs {
+    const void *x, *w, *b, *gy;
+    void* y;                       // forward: y; VJP: dx (may be null)
+    float* stats;                  // [rows][4]: mean, m, r, 0
+    float* part;                   // VJP: partial sums [blocks][heads][2][D] (null: no gradient of weight or bias)
+    int64_t xs[3];
+    int64_t T, H, rows;            // rows of a head (by_head), or all
+    int64_t blocks;                // of a head
+    int D, heads, flat, small;     // heads: H with by_head, else 1
+    float eps, inv;
+};
+
+__device__ __forceinline__ int64_t ln_quotient(int64_t n, int64_t d, bool small) {
+    return small ? int64_t(uint32_t(n) / uint32_t(d)) : n / d;
+}
+
+// Sums over a row's TR threads, in each of them.  Every thread of the block calls it.
+template <int TR, int N>
+__device__ __forceinline__ void row_sums(float (&x)[N], float (*red)[N]) {
+#pragma unroll
+    for (int m = 1; m < (TR < 64 ? TR : 64); m *= 2)
+#pragma unroll
+        for (int n = 0; n < N; ++n) x[n] += __shfl_xor(x[n], m, 64);
+    if constexpr (TR > 64) {
+        __syncthreads();
+        if (threadIdx.x % 64 == 0)
+#pragma unroll
+            for (int n = 0; n < N; ++n) red[threadIdx.x / 64][n] = x[n];
+        __syncthreads();
+        const int w0 = threadIdx.x / TR * (TR / 64);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            x[n] = 0.f;
+#pragma unroll
+            for (int w = 0; w < TR / 64; ++w) x[n] += red[w0 + w][n];
+        }
+    }
+}
+
+template <int DT, int W, int S, int TR, bool BWD>
+__global__ void __launch_bounds__(TR > kLnThreads ? TR : kLnThreads) ln_kernel(LnArgs a) {
+    using E = typename Storage<DT>::type;
+    constexpr int kBlock = TR > kLnThreads ? TR : kLnThreads, kGroups = kBlock / TR;
+    const int lane = threadIdx.x % TR, group = threadIdx.x / TR;
+    const int D = a.D, head = int(blockIdx.x % a.heads);
+    const int64_t block = blockIdx.x / a.heads;
+    const bool small = a.small != 0;
+    __shared__ float red1[kBlock / 64][1], red2[kBlock / 64][2];
+    float w[S][W], b[S][W];                    // forward: weight and bias; VJP: weight, and sums of g
+    float sw[BWD ? S : 1][W];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int at = (s * TR + lane) * W;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            w[s][j] = 1.f;
+            b[s][j] = 0.f;
+            if constexpr (BWD) sw[s][j] = 0.f;
+        }
+        if (at < D) {
+            if (a.w) load_floats<W>(static_cast<const E*>(a.w) + int64_t(head) * D + at, w[s]);
+            if (!BWD && a.b) load_floats<W>(static_cast<const E*>(a.b) + int64_t(head) * D + at, b[s]);
+        }
+    }
+    // (Every group of a block takes as many turns as the first: the sums over more than a wave are the block's.)
+    for (int64_t r0 = block * kGroups; r0 < a.rows; r0 += a.blocks * kGroups) {
+        const bool in = r0 + group < a.rows;
+        const int64_t i = in ? r0 + group : a.rows - 1;
+        // Row i of a head is token i; without heads, row i is head i % H of token i / H.
+        int64_t row = i, src;
+        if (a.heads > 1) {
+            row = i * a.H + head;
+            if (a.flat) {
+                src = i * a.xs[1] + head * a.xs[2];
+            } else {
+                const int64_t bt = ln_quotient(i, a.T, small);
+                src = bt * a.xs[0] + (i - bt * a.T) * a.xs[1] + head * a.xs[2];
+            }
+        } else if (a.flat) {
+            src = i * a.xs[2];
+        } else {
+            const int64_t token = ln_quotient(i, a.H, small), bt = ln_quotient(token, a.T, small);
+            src = bt * a.xs[0] + (token - bt * a.T) * a.xs[1] + (i - token * a.H) * a.xs[2];
+        }
+        const E* px = static_cast<const E*>(a.x) + src;
+        float x[S][W], g[BWD ? S : 1][W];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int at = (s * TR + lane) * W;
+            if (at < D) {
+                load_floats<W>(px + at, x[s]);
+                if constexpr (BWD) load_floats<W>(static_cast<const E*>(a.gy) + row * D + at, g[s]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    x[s][j] = 0.f;
+                    if constexpr (BWD) g[s][j] = 0.f;
+                }
+            }
+        }
+        if constexpr (!BWD) {
+            float one[1] = {0.f}, two[2] = {0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int j = 0; j < W; ++j) one[0] += x[s][j];
+            row_sums<TR, 1>(one, red1);
+            const float mean = one[0] * a.inv;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const bool on = (s * TR + lane) * W < D;
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    x[s][j] = on ? x[s][j] - mean : 0.f;
+                    two[0] += x[s][j];
+                    two[1] += x[s][j] * x[s][j];
+                }
+            }
+            row_sums<TR, 2>(two, red2);
+            const float m = two[0] * a.inv;
+            const float v = two[1] * a.inv - m * m, r = 1.f / sqrtf((v > 0.f ? v : v == v ? 0.f : v) + a.eps);
+            if (in && a.stats && lane == 0) *reinterpret_cast<f32x4*>(a.stats + row * 4) = f32x4{mean, m, r, 0.f};
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const int at = (s * TR + lane) * W;
+#pragma unroll
+                for (int j = 0; j < W; ++j) x[s][j] = (x[s][j] - m) * r * w[s][j] + b[s][j];
+                if (in && at < D) store_floats<W>(static_cast<E*>(a.y) + row * D + at, x[s]);
+            }
+        } else {
+            const f32x4 st = *reinterpret_cast<const f32x4*>(a.stats + row * 4);
+            const float mean = st[0], m = st[1], r = st[2];
+            float two[2] = {0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const bool on = (s * TR + lane) * W < D;
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    x[s][j] = on ? (x[s][j] - mean - m) * r : 0.f;
+                    if (in) {
+                        sw[s][j] += g[s][j] * x[s][j];
+                        b[s][j] += g[s][j];
+                    }
+                    g[s][j] *= w[s][j];
+                    two[0] += g[s][j];
+                    two[1] += g[s][j] * x[s][j];
+                }
+            }
+            if (!a.y) continue;
+            row_sums<TR, 2>(two, red2);
+            const float c0 = two[0] * a.inv, c1 = two[1] * a.inv;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const int at = (s * TR + lane) * W;
+#pragma unroll
+                for (int j = 0; j < W; ++j) x[s][j] = r * (g[s][j] - c0 - x[s][j] * c1);
+                if (in && at < D) store_floats<W>(static_cast<E*>(a.y) + row * D + at, x[s]);
+            }
+        }
+    }
+    if constexpr (BWD) {
+        if (!a.part) return;
+        // The block's sums in a fixed order: groups of a wave by shuffles, waves through LDS.
+        float* part = a.part + (block * a.heads + head) * 2 * int64_t(D);
+        if constexpr (kGroups == 1) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const int at = (s * TR + lane) * W;
+                if (at < D)
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        part[at + j] = sw[s][j];
+                        part[D + at + j] = b[s][j];
+                    }
+            }
+        } else {
+            constexpr int kSum = TR < 64 ? TR : 64, kWaves = kBlock / 64, kPer = TR < 64 ? kWaves : kBlock / TR;
+            __shared__ float red[kWaves][S * W * 2][kSum];
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+#pragma unroll
+                    for (int m = TR; m < 64; m *= 2) {
+                        sw[s][j] += __shfl_xor(sw[s][j], m, 64);
+                        b[s][j] += __shfl_xor(b[s][j], m, 64);
+                    }
+                    if (threadIdx.x % 64 < kSum) {
+                        red[threadIdx.x / 64][(s * W + j) * 2][threadIdx.x % 64] = sw[s][j];
+                        red[threadIdx.x / 64][(s * W + j) * 2 + 1][threadIdx.x % 64] = b[s][j];
+                    }
+                }
+            __syncthreads();
+            if (threadIdx.x < TR) {
+                constexpr int kStep = TR < 64 ? 1 : TR / 64;       // waves that hold the same elements are kStep apart
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const int at = (s * TR + lane) * W;
+                    if (at < D)
+#pragma unroll
+                        for (int j = 0; j < W; ++j) {
+                            float tw = 0.f, tb = 0.f;
+#pragma unroll
+                            for (int c = 0; c < kPer; ++c) {
+                                tw += red[threadIdx.x / 64 + c * kStep][(s * W + j) * 2][threadIdx.x % 64];
+                                tb += red[threadIdx.x / 64 + c * kStep][(s * W + j) * 2 + 1][threadIdx.x % 64];
+                            }
+                            part[at + j] = tw;
+                            part[D + at + j] = tb;
+                        }
+                }
+            }
+        }
+    }
+}
+
+// The weights' gradients from the blocks' partial sums: 16 columns and 64 runs
+// of blocks to a block of threads, the runs joined in order.
+constexpr int kLnRuns = 64;
+
+template <int DT>
+__global__ void __launch_bounds__(16 * kLnRuns) ln_weight_kernel(const float* part, int64_t n, int heads, int D, void* dw, void* db) {
+    using E = typename Storage<DT>::type;
+    E* out = static_cast<E*>(blockIdx.y ? db : dw);
+    if (!out) return;
+    const int64_t col = int64_t(blockIdx.x) * 16 + threadIdx.x % 16, all = int64_t(heads) * D;
+    const int run = threadIdx.x / 16;
+    __shared__ float red[kLnRuns][17];
+    float s = 0.f;
+    if (col < all) {
+        const float* p = part + (col / D * 2 + blockIdx.y) * D + col % D;
+#pragma unroll 4
+        for (int64_t i = run; i < n; i += kLnRuns) s += p[i * 2 * all];
+    }
+    red[run][threadIdx.x % 16] = s;
+    __syncthreads();
+    if (threadIdx.x < 16 && col < all) {
+        float t = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < kLnRuns; ++i) t += red[i][threadIdx.x];
+        out[col] = E(t);
+    }
+}
+
+struct LnShape {
+    bool wide;          // W = 8
+    int tr, s;          // threads of a row, runs of a thread
+};
+
+LnShape ln_shape(int64_t D, bool wide) {
+    LnShape sh{wide, 4, 1};
+    if (wide) {
+        const int64_t runs = (D + 7) / 8;
+        while (sh.tr < 1024 && sh.tr < runs) sh.tr *= 2;
+        if (sh.tr >= 128) {          // two runs to a thread: half as many waves to join
+            sh.tr /= 2;
+            sh.s = 2;
+        }
+        if (sh.tr * sh.s < runs) sh.tr *= 2;
+    } else {
+        sh.tr = D <= 1024 ? 64 : D <= 4096 ? 256 : 1024;
+        while (sh.tr * sh.s < D) sh.s *= 2;
+    }
+    return sh;
+}
+
+int ln_groups(const LnShape& sh) { return sh.tr > kLnThreads ? 1 : kLnThreads / sh.tr; }
+
+template <class F>
+hipError_t ln_by_dtype(int dt, F&& f) {
+    if (dt == 0) return f(std::integral_constant<int, 0>{});
+    if (dt == 1) return f(std::integral_constant<int, 1>{});
+    return f(std::integral_constant<int, 2>{});
+}
+
+template <int DT, bool BWD>
+const void* ln_kernel_of(const LnShape& sh) {
+#define LN_WIDE(s_, tr_) \
+    if (sh.wide && sh.s == s_ && sh.tr == tr_) return reinterpret_cast<const void*>(&ln_kernel<DT, 8, s_, tr_, BWD>);
+#define LN_NARROW(s_, tr_) \
+    if (!sh.wide && sh.s == s_ && sh.tr == tr_) return reinterpret_cast<const void*>(&ln_kernel<DT, 1, s_, tr_, BWD>);
+    LN_WIDE(1, 4) LN_WIDE(1, 8) LN_WIDE(1, 16) LN_WIDE(1, 32) LN_WIDE(1, 64)
+    LN_WIDE(2, 64) LN_WIDE(2, 128) LN_WIDE(2, 256) LN_WIDE(2, 512) LN_WIDE(2, 1024)
+    LN_NARROW(1, 64) LN_NARROW(2, 64) LN_NARROW(4, 64) LN_NARROW(8, 64) LN_NARROW(16, 64)
+    LN_NARROW(8, 256) LN_NARROW(16, 256) LN_NARROW(8, 1024) LN_NARROW(16, 1024)
+#undef LN_WIDE
+#undef LN_NARROW
+    return nullptr;
+}
+
+template <bool BWD>
+hipError_t ln_launch(int dt, const LnShape& sh, const LnArgs& a, hipStream_t st) {
+    return ln_by_dtype(dt, [&](auto t) {
+        const void* fn = ln_kernel_of<decltype(t)::value, BWD>(sh);
+        if (!fn) return hipErrorInvalidConfiguration;
+        LnArgs args = a;
+        void* params[] = {&args};
+        return hipLaunchKernel(fn, dim3(unsigned(a.blocks * a.heads)), dim3(unsigned(sh.tr > kLnThreads ? sh.tr : kLnThreads)), params, 0, st);
+    });
+}
+
+int ln_check(const lnm_dims* d) {
+    if (!d) return QC_ERR_NULL;
+    if (d->dtype < 0 || d->dtype > 2) return QC_ERR_DTYPE;
+    if (d->B < 0 || d->T < 0 || d->H < 0 || d->D < 1 || d->D > kLnMaxD || d->H > (1 << 20)) return QC_ERR_SHAPE;
+    if (count(count(d->B, d->T), count(d->H, d->D)) < 0) return QC_ERR_SHAPE;
+    if (d->by_head && d->H * d->D >= (int64_t(1) << 31)) return QC_ERR_SHAPE;
+    if (strided_bytes(d->B, d->T, d->H, d->D, d->x_stride, dtype_bytes(d->dtype)) < 0) return QC_ERR_SHAPE;
+    if (!(d->eps >= 0.f)) return QC_ERR_OPTION;
+    return QC_OK;
+}
+
+int64_t ln_heads(const lnm_dims& d) { return d.by_head && d.H ? d.H : 1; }
+int64_t ln_rows(const lnm_dims& d) { return d.by_head ? d.B * d.T : d.B * d.T * d.H; }
+
+// Blocks of a head whose partial sums are kept: no more than there are rows, nor than fill the card.
+int64_t ln_partials(const lnm_dims& d) {
+    const int64_t share = kLnPartials / ln_heads(d), most = share > 1 ? share : 1, rows = ln_rows(d);
+    return rows < most ? rows : most;
+}
+
+LnArgs ln_arguments(const lnm_dims& d, const void* x, const void* w) {
+    LnArgs a{};
+    a.x = x; a.w = w;
+    for (int i = 0; i < 3; ++i) a.xs[i] = d.x_stride[i];
+    a.T = d.T; a.H = d.H; a.rows = ln_rows(d);
+    a.D = int(d.D); a.heads = int(ln_heads(d));
+    const bool tokens = d.B <= 1 || d.x_stride[0] == d.T * d.x_stride[1];
+    a.flat = a.heads > 1 ? tokens : (d.H <= 1 && d.T <= 1) ? d.B <= 1 : tokens && (d.H <= 1 || d.x_stride[1] == d.H * d.x_stride[2]);
+    // One row to a token: tokens' stride is the rows'.
+    if (a.heads == 1 && d.H == 1) a.xs[2] = d.T > 1 ? d.x_stride[1] : d.x_stride[0];
+    if (a.heads == 1 && d.H == 1 && d.T <= 1) a.flat = 1;
+    a.small = d.B * d.T * d.H < (int64_t(1) << 31);
+    a.eps = d.eps;
+    a.inv = 1.f / float(d.D);
+    return a;
+}
+
+}  // namespace
+}  // namespace qc
+
+extern "C" {
+
+int lnm_fwd(const lnm_dims* dims, const void* x, const void* weight, const void* bias, void* y, float* stats, void* stream) {
+    const int rc = qc::ln_check(dims);
+    if (rc != QC_OK) return rc;
+    const lnm_dims& d = *dims;
+    const int64_t rows = d.B * d.T * d.H;
+    if (!rows) return QC_OK;
+    if (!x || !y) return QC_ERR_NULL;
+    const size_t e = qc::dtype_bytes(d.dtype), w = size_t(qc::ln_heads(d) * d.D) * e;
+    for (const void* p : {x, weight, bias, static_cast<const void*>(y)})
+        if (!qc::aligned_to(p, e)) return QC_ERR_ALIGN;
+    if (!qc::aligned_to(stats, 16)) return QC_ERR_ALIGN;
+    const qc::ByteSpan sp[] = {{y, size_t(rows * d.D) * e}, {stats, size_t(rows) * 16},
+                               {x, size_t(qc::strided_bytes(d.B, d.T, d.H, d.D, d.x_stride, e))}, {weight, w}, {bias, w}};
+    if (qc::outputs_overlap(sp, 2, 5)) return QC_ERR_ALIAS;
+    qc::LnArgs a = qc::ln_arguments(d, x, weight);
+    a.b = bias; a.y = y; a.stats = stats;
+    const bool wide = d.D % 8 == 0 && qc::rows_on_16(x, d.x_stride, e) && qc::aligned_to(y, 16) && qc::aligned_to(weight, 16) && qc::aligned_to(bias, 16);
+    const qc::LnShape sh = qc::ln_shape(d.D, wide);
+    const int64_t groups = qc::ln_groups(sh), most = (int64_t(1) << 20) / a.heads + 1, n = (a.rows + groups - 1) / groups;
+    a.blocks = n < most ? n : most;
+    const hipError_t err = qc::ln_launch<false>(d.dtype, sh, a, static_cast<hipStream_t>(stream));
+    return err == hipSuccess ? QC_OK : qc::record_hip_error(err);
+}
+
+size_t lnm_workspace_bytes(const lnm_dims* dims) {
+    if (qc::ln_check(dims) != QC_OK) return 0;
+    return size_t(qc::ln_partials(*dims) * qc::ln_heads(*dims) * 2 * dims->D) * 4 + 16;
+}
+
+int lnm_bwd(const lnm_dims* dims, const void* x, const void* weight, const float* stats, const void* d_y, void* d_x, void* d_weight,
+            void* d_bias, void* workspace, size_t workspace_bytes, void* stream) {
+    const int rc = qc::ln_check(dims);
+    if (rc != QC_OK) return rc;
+    const lnm_dims& d = *dims;
+    if ((!d_x && !d_weight && !d_bias) || (d.by_head && !d.H)) return QC_OK;
+    const int64_t rows = d.B * d.T * d.H;
+    const bool sums = d_weight || d_bias;
+    if (rows && (!x || !stats || !d_y)) return QC_ERR_NULL;
+    if (d_weight && !weight) return QC_ERR_NULL;
+    const size_t need = lnm_workspace_bytes(dims);
+    if (sums && (!workspace || workspace_bytes < need)) return QC_ERR_WORKSPACE;
+    if (sums && !qc::aligned_to(workspace, 16)) return QC_ERR_ALIGN;
+    const size_t e = qc::dtype_bytes(d.dtype), w = size_t(qc::ln_heads(d) * d.D) * e;
+    bool wide = d.D % 8 == 0 && qc::rows_on_16(x, d.x_stride, e) && qc::aligned_to(weight, 16);
+    for (const void* p : {d_y, static_cast<const void*>(d_x)}) wide = wide && qc::aligned_to(p, 16);
+    for (const void* p : {x, weight, d_y, static_cast<const void*>(d_x), static_cast<const void*>(d_weight), static_cast<const void*>(d_bias)})
+        if (!qc::aligned_to(p, e)) return QC_ERR_ALIGN;
+    if (!qc::aligned_to(stats, 16)) return QC_ERR_ALIGN;
+    const qc::ByteSpan sp[] = {{d_x, size_t(rows * d.D) * e}, {d_weight, w}, {d_bias, w}, {sums ? workspace : nullptr, need},
+                               {x, size_t(qc::strided_bytes(d.B, d.T, d.H, d.D, d.x_stride, e))}, {weight, w},
+                               {stats, size_t(rows) * 16}, {d_y, size_t(rows * d.D) * e}};
+    if (qc::outputs_overlap(sp, 4, 8)) return QC_ERR_ALIAS;
+    qc::LnArgs a = qc::ln_arguments(d, x, weight);
+    a.gy = d_y; a.y = d_x; a.stats = const_cast<float*>(stats);
+    a.part = sums ? static_cast<float*>(workspace) : nullptr;
+    const qc::LnShape sh = qc::ln_shape(d.D, wide);
+    const int64_t groups = qc::ln_groups(sh), n = (a.rows + groups - 1) / groups, most = sums ? qc::ln_partials(d) : (int64_t(1) << 20) / a.heads + 1;
+    a.blocks = n < most ? n : most;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t err = hipSuccess;
+    if (a.blocks * a.heads) err = qc::ln_launch<true>(d.dtype, sh, a, st);
+    if (err == hipSuccess && sums) {
+        err = qc::ln_by_dtype(d.dtype, [&](auto t) {
+            const float* part = a.part;
+            int64_t blocks = a.blocks;
+            int heads = a.heads, D = a.D;
+            void *dw = d_weight, *db = d_bias;
+            void* params[] = {&part, &blocks, &heads, &D, &dw, &db};
+            return hipLaunchKernel(reinterpret_cast<const void*>(&qc::ln_weight_kernel<decltype(t)::value>),
+                                   dim3(unsigned((int64_t(heads) * D + 15) / 16), 2), dim3(16 * qc::kLnRuns), params, 0, st);
+        });
+    }
+    return err == hipSuccess ? QC_OK : qc::record_hip_error(err);
+}
+
+}  // extern "C"

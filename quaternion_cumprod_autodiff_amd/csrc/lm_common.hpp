@@ -1,4 +1,4 @@
-// lm_common.hpp -- what the gated-delta and query/key-norm kernels share:
+// lm_common.hpp -- what the kernels of language-model operators share:
 // storage types, loads of several elements, host-side argument checks.  Not
 // installed.
 #pragma once
@@ -56,6 +56,32 @@ __device__ __forceinline__ void store_floats(E* p, const float (&x)[W]) {
         }
     }
 }
+
+// N consecutive elements as they lie in memory: taken apart where they are used,
+// so that the next token's are on their way during this one's work.  VEC: pieces
+// of up to 16 bytes, each inside or outside `left` as a whole.
+template <class E, int N, bool VEC>
+struct Held {
+    static constexpr int kPer = N * sizeof(E) >= 16 ? 16 / sizeof(E) : N;
+    typedef E Vec __attribute__((ext_vector_type(kPer)));
+    Vec x[N / kPer];
+
+    __device__ __forceinline__ void load(const E* p, int left) {
+#pragma unroll
+        for (int i = 0; i < N / kPer; ++i) {
+            if constexpr (VEC) {
+                x[i] = i * kPer < left ? reinterpret_cast<const Vec*>(p)[i] : Vec(E(0.f));
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) x[i][j] = i * kPer + j < left ? p[i * kPer + j] : E(0.f);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&y)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = float(x[i / kPer][i % kPer]);
+    }
+};
 
 // Host checks -----------------------------------------------------------------
 
