@@ -150,6 +150,16 @@ __device__ __forceinline__ void row_fragment(const char* t, int token, int b, in
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// TIGHT: a lane's number that the compiler takes for a new one.  Addresses made of it are made again in each phase of a
+// chunk, a few instructions, instead of being held over all of them, in registers that the state needs (bfloat16, 128 x
+// 128, forward: 272 bytes a lane spilled and 160 us, none and 97; but where nothing spills 142 us become 160, float32
+// 64 x 128).
+template <bool TIGHT>
+__device__ __forceinline__ int fresh(int x) {
+    if constexpr (TIGHT) asm volatile("" : "+v"(x));
+    return x;
+}
+
 // Four rows' element of column m, from pieces of 4 columns: lane 4 r + q names piece q of row r.
 __device__ __forceinline__ s16x4 read_transposed(const char* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));

@@ -15,9 +15,12 @@ template <int DT, int KB, int CT, bool SAVE>
 __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
     using E = typename Storage<DT>::type;
     constexpr int C = dca_chunk(DT), NP = parts_of(DT), PP = dca_parts(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 64 * CT, KT = 2 * KB;
-    __shared__ __align__(16) char lq[NP * C * KP * 2], lk[NP * C * KP * 2], lv[NP * C * VW * 2];
+    // Rows of Q, K and V; between chunks, a wave's columns of S on their way to memory.
+    __shared__ __align__(16) char rows[NP * C * (2 * KP + VW) * 2];
+    char *lq = rows, *lk = lq + NP * C * KP * 2, *lv = lk + NP * C * KP * 2;
     __shared__ __align__(16) bf16x8 lp[dca_tri(C)][PP][64];
     __shared__ __align__(16) Decays<C> dec;
+    constexpr bool kTight = KB == 4 && CT == 2;
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), g = lane / 16, m = lane % 16;
     int64_t u;
     int part;
@@ -61,32 +64,55 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
     auto load = [&](int c) {
         const int64_t t = int64_t(c) * C;
         const int rem = int(s.len - t);
-        rq.load(q + t * a.qs[1], a.qs[1], rem, a.K, a.vec_qk, tid);
-        rk.load(k + t * a.ks[1], a.ks[1], rem, a.K, a.vec_qk, tid);
-        rv.load(v + t * a.vs[1], a.vs[1], rem, a.V - v0, a.vec_v, tid);
+        const int id = fresh<kTight>(tid);
+        rq.load(q + t * a.qs[1], a.qs[1], rem, a.K, a.vec_qk, id);
+        rk.load(k + t * a.ks[1], a.ks[1], rem, a.K, a.vec_qk, id);
+        rv.load(v + t * a.vs[1], a.vs[1], rem, a.V - v0, a.vec_v, id);
         rg = lane < C && lane < rem ? gd[(t + lane) * a.gs[1]] : 0.f;
     };
     if (first < last) load(first);
     for (int chunk = first; chunk < last; ++chunk) {
         const int rem = s.len - chunk * C;
         __syncthreads();
-        rq.store(lq, tid);
-        rk.store(lk, tid);
-        rv.store(lv, tid);
-        if (wave == 0) put_decays<C>(dec, rg, lane);
         if constexpr (SAVE) {
-            float* dst = a.save + ((s.slot + chunk) * a.Hv + h) * int64_t(KP) * a.VP;
+            // S0, 32 rows at a time: lanes hold a column's, memory wants a row's.  (Stored as they are, four bytes a lane,
+            // 4 x 4096 tokens of 32 heads of 128 took 560 us instead of 287.)
+            constexpr int kStep = 36, kLanes = 4 * CT;
+            static_assert(4 * 16 * CT * kStep * 4 <= sizeof(rows), "the columns' place");
+            const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
+            float* t = reinterpret_cast<float*>(rows) + wave * (16 * CT * kStep);
+            float* dst = a.save + ((s.slot + chunk) * a.Hv + h) * int64_t(KP) * a.VP + int64_t(l / kLanes) * a.VP + vw + l % kLanes * 4;
 #pragma unroll
-            for (int r = 0; r < KT; ++r)
+            for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int c = 0; c < CT; ++c) dst[int64_t(acc_index(r, g) + i) * a.VP + column(c)] = S[r][c][i];
+                    for (int c = 0; c < CT; ++c)
+                        *reinterpret_cast<f32x4*>(t + (CT == 2 ? 8 * (m >> 2) + 4 * c + (m & 3) : m) * kStep + 8 * g + 4 * e) = S[2 * kb + e][c];
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int p = 0; p < 32 * kLanes / 64; ++p) {
+                    f32x4 x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = t[(l % kLanes * 4 + j) * kStep + p * (64 / kLanes) + l / kLanes];
+                    *reinterpret_cast<f32x4*>(dst + int64_t(32 * kb + p * (64 / kLanes)) * a.VP) = x;
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+            __syncthreads();
         }
+        {
+            const int id = fresh<kTight>(tid);
+            rq.store(lq, id);
+            rk.store(lk, id);
+            rv.store(lv, id);
+        }
+        if (wave == 0) put_decays<C>(dec, rg, lane);
         __syncthreads();
         if (chunk + 1 < last) load(chunk + 1);
 
         if (wave < TT) {
+            const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
 #pragma unroll
             for (int b = 0; b < JB; ++b) {
                 if (b > (wave >> 1)) continue;
@@ -110,11 +136,13 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
                 for (int j = 0; j < PP; ++j) lp[tri_of(wave, b)][j][lane] = p[j];
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         f32x4 o[CT][TT];
 #pragma unroll
         for (int c = 0; c < CT; ++c)
 #pragma unroll
             for (int t = 0; t < TT; ++t) o[c][t] = zero4();
+        const int l1 = fresh<kTight>(lane), g1 = l1 / 16, m1 = l1 % 16;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             bf16x8 sf[CT][PP];
@@ -127,10 +155,11 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
                 bf16x8 qf[NP];
-                row_fragment<C, KP>(lq, 16 * t + m, kb, g, qf);
+                row_fragment<C, KP>(lq, 16 * t + m1, kb, g1, qf);
 #pragma unroll
                 for (int c = 0; c < CT; ++c) mma(o[c][t], sf[c], qf);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
@@ -141,6 +170,7 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
 
         bf16x8 vf[CT][JB][NP];
         auto values = [&] {
+            const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -199,11 +229,11 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
                 }
             values();
         }
-        const int col = vw + 4 * CT * g;
+        const int l2 = fresh<kTight>(lane), g2 = l2 / 16, m2 = l2 % 16, col = vw + 4 * CT * g2;
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            if (16 * t + m >= rem) continue;
-            E* p = out + (int64_t(chunk) * C + 16 * t + m) * a.Hv * a.V + col;
+            if (16 * t + m2 >= rem) continue;
+            E* p = out + (int64_t(chunk) * C + 16 * t + m2) * a.Hv * a.V + col;
             float x[4 * CT];
 #pragma unroll
             for (int c = 0; c < CT; ++c)
@@ -218,7 +248,9 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
             }
         }
 
+        __builtin_amdgcn_sched_barrier(0);
         const float keep = dec.gamma[C - 1];
+        const int l3 = fresh<kTight>(lane), g3 = l3 / 16, m3 = l3 % 16;
 #pragma unroll
         for (int r = 0; r < KT; ++r)
 #pragma unroll
@@ -226,7 +258,7 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
 #pragma unroll
         for (int b = 0; b < JB; ++b) {
             float eta[8];
-            read8(dec.eta + 32 * b + 8 * g, eta);
+            read8(dec.eta + 32 * b + 8 * g3, eta);
             bf16x8 yf[CT][kParts];
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
@@ -239,9 +271,10 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
 #pragma unroll
             for (int r = 0; r < KT; ++r) {
                 bf16x8 kf[NP];
-                col_fragment<C, KP>(lk, b, g, m, 32 * (r >> 1) + 8 * (m & 3) + 4 * (r & 1), kf);
+                col_fragment<C, KP>(lk, b, g3, m3, 32 * (r >> 1) + 8 * (m3 & 3) + 4 * (r & 1), kf);
 #pragma unroll
                 for (int c = 0; c < CT; ++c) mma(S[r][c], kf, yf[c]);
+                if (r % 2) __builtin_amdgcn_sched_barrier(0);
             }
         }
     }

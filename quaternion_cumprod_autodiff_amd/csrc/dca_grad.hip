@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(256, DT == 0 ? 1 : 2) dca_grad_kernel(DcaArgs 
     };
     static_assert(sizeof(Sums) <= sizeof(lo), "the sums take the cotangents' place");
     Sums& sum = *reinterpret_cast<Sums*>(lo);
+    constexpr bool kTight = true;
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), g = lane / 16, m = lane % 16;
     const int64_t slot = blockIdx.x / a.Hk;
     const int hk = int(blockIdx.x % a.Hk);
@@ -46,9 +47,8 @@ __global__ void __launch_bounds__(256, DT == 0 ? 1 : 2) dca_grad_kernel(DcaArgs 
     const int64_t t0 = s.t0 + chunk * C, size = int64_t(KP) * a.VP;
     const bool want_dg = a.dg || a.dg_part;
 
-    // K rows of the wave's tile e, lane m (as operand), and its tokens' tile t.
+    // The wave's first K row and first tile of tokens.
     const int k0 = KB == 4 ? 32 * wave : KB == 2 ? 16 * wave : 16 * (wave & 1), tt0 = KB == 1 ? (wave >> 1) * TW : 0;
-    auto krow = [&](int e) { return KW == 2 ? k0 + 8 * (m >> 2) + 4 * e + (m & 3) : k0 + m; };
     const int kacc = k0 + 4 * KW * g;                     // the 4 KW rows of a lane's accumulators
     {
         Rows<DT, C, KP> rq, rk;
@@ -95,16 +95,18 @@ __global__ void __launch_bounds__(256, DT == 0 ? 1 : 2) dca_grad_kernel(DcaArgs 
             const int v0 = tile * VW;
             {
                 Rows<DT, C, VW> rv, ro;
-                rv.load(static_cast<const E*>(a.v) + s.b * a.vs[0] + t0 * a.vs[1] + h * a.vs[2] + v0, a.vs[1], rem, a.V - v0, a.vec_v, tid);
-                ro.load(static_cast<const E*>(a.d_out) + ((s.b * a.T + t0) * a.Hv + h) * int64_t(a.V) + v0, int64_t(a.Hv) * a.V, rem, a.V - v0, a.vec_o, tid);
+                const int id = fresh<kTight>(tid);
+                rv.load(static_cast<const E*>(a.v) + s.b * a.vs[0] + t0 * a.vs[1] + h * a.vs[2] + v0, a.vs[1], rem, a.V - v0, a.vec_v, id);
+                ro.load(static_cast<const E*>(a.d_out) + ((s.b * a.T + t0) * a.Hv + h) * int64_t(a.V) + v0, int64_t(a.Hv) * a.V, rem, a.V - v0, a.vec_o, id);
                 __syncthreads();                          // what read the rows before is done
-                rv.store(lv, tid);
-                ro.store(lo, tid);
+                rv.store(lv, id);
+                ro.store(lo, id);
             }
             if (tile == 0 && wave == 0)
                 put_decays<C>(dec, lane < C && lane < rem ? a.g[s.b * a.gs[0] + (t0 + lane) * a.gs[1] + h * a.gs[2]] : 0.f, lane);
             __syncthreads();
             if (tile == 0 && wave < TT) {
+                const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
 #pragma unroll
                 for (int b = 0; b < JB; ++b) {
                     if (b > (wave >> 1)) continue;
@@ -117,6 +119,7 @@ __global__ void __launch_bounds__(256, DT == 0 ? 1 : 2) dca_grad_kernel(DcaArgs 
                 }
             }
             if (wave < TT) {
+                const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
 #pragma unroll
                 for (int b = 0; b < JB; ++b) {
                     if (b > (wave >> 1)) continue;
@@ -133,70 +136,74 @@ __global__ void __launch_bounds__(256, DT == 0 ? 1 : 2) dca_grad_kernel(DcaArgs 
                     }
                 }
             }
-            // O S0^T and V dS1^T, over this block's columns of V.
-            f32x4 rd[KW][TW], wr[KW][TW];
+            // O S0^T, then V dS1^T, over this block's columns of V: gamma and eta of them, and what dg needs.
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int e = 0; e < KW; ++e)
+            for (int side = 0; side < 2; ++side) {
+                const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
+                const char* rows = side ? lv : lo;
+                f32x4 acc[KW][TW];
 #pragma unroll
-                for (int t = 0; t < TW; ++t) rd[e][t] = wr[e][t] = zero4();
+                for (int e = 0; e < KW; ++e)
 #pragma unroll
-            for (int x = 0; x < 2 * CT; ++x) {
-                bf16x8 sf[KW][kParts], df[KW][kParts];
+                    for (int t = 0; t < TW; ++t) acc[e][t] = zero4();
+                const int64_t place = int64_t(KW == 2 ? k0 + 8 * (m >> 2) + (m & 3) : k0 + m) * a.VP + v0 + 8 * g;
+                const float *p0 = (side ? D1 : S0) + place, *p1 = S0 + place;
 #pragma unroll
-                for (int e = 0; e < KW; ++e) {
-                    const int64_t at = int64_t(krow(e)) * a.VP + v0 + 32 * x + 8 * g;
-                    float y[8], z[8];
-                    read8(S0 + at, y);
-                    read8(D1 + at, z);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) dot += y[i] * z[i];
-                    split<kParts, 8>(y, sf[e]);
-                    split<kParts, 8>(z, df[e]);
-                }
-#pragma unroll
-                for (int t = 0; t < TW; ++t) {
-                    bf16x8 of[NP], vf[NP];
-                    row_fragment<C, VW>(lo, 16 * (tt0 + t) + m, x, g, of);
-                    row_fragment<C, VW>(lv, 16 * (tt0 + t) + m, x, g, vf);
+                for (int x = 0; x < 2 * CT; ++x) {
+                    bf16x8 sf[KW][kParts];
 #pragma unroll
                     for (int e = 0; e < KW; ++e) {
-                        mma(rd[e][t], sf[e], of);
-                        mma(wr[e][t], df[e], vf);
+                        float y[8];
+                        read8(p0 + int64_t(4 * e) * a.VP + 32 * x, y);
+                        if (side && want_dg) {
+                            float z[8];
+                            read8(p1 + int64_t(4 * e) * a.VP + 32 * x, z);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) dot += y[i] * z[i];
+                        }
+                        split<kParts, 8>(y, sf[e]);
                     }
+#pragma unroll
+                    for (int t = 0; t < TW; ++t) {
+                        bf16x8 rf[NP];
+                        row_fragment<C, VW>(rows, 16 * (tt0 + t) + m, x, g, rf);
+#pragma unroll
+                        for (int e = 0; e < KW; ++e) mma(acc[e][t], sf[e], rf);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-            }
+                const int kacc = k0 + 4 * KW * g;
 #pragma unroll
-            for (int t = 0; t < TW; ++t) {
-                const int token = 16 * (tt0 + t) + m;
-                const float gamma = dec.gamma[token] * a.scale, eta = dec.eta[token];
-                const int at = lds_piece<KP>(token, kacc >> 3) + (kacc & 7) * 2;
+                for (int t = 0; t < TW; ++t) {
+                    const int token = 16 * (tt0 + t) + m;
+                    const float w = side ? dec.eta[token] : dec.gamma[token] * a.scale;
+                    const char* at = (side ? lk : lq) + lds_piece<KP>(token, kacc >> 3) + (kacc & 7) * 2;
+                    float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < KW; ++e) {
-                    rd[e][t] *= gamma;
-                    wr[e][t] *= eta;
-                    dq[e][t] += rd[e][t];
-                    dk[e][t] += wr[e][t];
-                    if (want_dg) {
-                        float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+                    for (int e = 0; e < KW; ++e) {
+                        acc[e][t] *= w;
+                        if (side) dk[e][t] += acc[e][t];
+                        else dq[e][t] += acc[e][t];
+                        if (want_dg) {
+                            float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int p = NP - 1; p >= 0; --p) {
-                            const bf16x4 qp = *reinterpret_cast<const bf16x4*>(lq + p * (C * KP * 2) + at + 8 * e);
-                            const bf16x4 kp = *reinterpret_cast<const bf16x4*>(lk + p * (C * KP * 2) + at + 8 * e);
+                            for (int p = NP - 1; p >= 0; --p) {
+                                const bf16x4 part = *reinterpret_cast<const bf16x4*>(at + p * (C * KP * 2) + 8 * e);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                x[i] += float(qp[i]);
-                                y[i] += float(kp[i]);
+                                for (int i = 0; i < 4; ++i) x[i] += float(part[i]);
                             }
-                        }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            reads[t] += x[i] * rd[e][t][i];
-                            writes[t] += y[i] * wr[e][t][i];
+                            for (int i = 0; i < 4; ++i) sum += x[i] * acc[e][t][i];
                         }
                     }
+                    if (side) writes[t] += sum;
+                    else reads[t] += sum;
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (a.dv) {
+                const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
                 f32x4 dv[CT][TT];
 #pragma unroll
                 for (int c = 0; c < CT; ++c)
@@ -221,6 +228,7 @@ __global__ void __launch_bounds__(256, DT == 0 ? 1 : 2) dca_grad_kernel(DcaArgs 
 #pragma unroll
                         for (int c = 0; c < CT; ++c) mma(dv[c][t], df[c], kf);
                     }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
@@ -265,6 +273,7 @@ __global__ void __launch_bounds__(256, DT == 0 ? 1 : 2) dca_grad_kernel(DcaArgs 
         }
         __syncthreads();                                  // P and the cotangents are done with
         if (wave < TT) {
+            const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
             f32x4 before[TT];                             // [t][i]: sum over j < t of M_ij
 #pragma unroll
             for (int t = 0; t < TT; ++t) before[t] = zero4();
@@ -327,6 +336,7 @@ __global__ void __launch_bounds__(256, DT == 0 ? 1 : 2) dca_grad_kernel(DcaArgs 
         }
         __syncthreads();
         if (a.dq || a.dk) {
+            const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
 #pragma unroll
             for (int b = 0; b < JB; ++b) {
                 bf16x8 kf[KW][NP], qf[KW][NP];

@@ -18,6 +18,7 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
     constexpr int C = dca_chunk(DT), NP = parts_of(DT), JB = C / 32, KP = 32 * KB, VW = 64 * CT, KT = 2 * KB;
     __shared__ __align__(16) char lx[NP * C * KP * 2], ly[NP * C * VW * 2];
     __shared__ __align__(16) Decays<C> dec;
+    constexpr bool kTight = DT == 1 && KB == 4 && CT == 2 && !SUM;
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), g = lane / 16, m = lane % 16;
     int64_t u;
     int part;
@@ -63,8 +64,9 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
     auto load = [&](int c) {
         const int64_t t = int64_t(c) * C;
         const int rem = int(s.len - t);
-        rx.load(x + t * xs[1], xs[1], rem, a.K, a.vec_qk, tid);
-        ry.load(y + t * ys, ys, rem, a.V - v0, REV ? a.vec_o : a.vec_v, tid);
+        const int id = fresh<kTight>(tid);
+        rx.load(x + t * xs[1], xs[1], rem, a.K, a.vec_qk, id);
+        ry.load(y + t * ys, ys, rem, a.V - v0, REV ? a.vec_o : a.vec_v, id);
         rg = lane < C && lane < rem ? gd[(t + lane) * a.gs[1]] : 0.f;
     };
     double decay = 0.;
@@ -72,15 +74,16 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
     for (int step = 0; step < last - first; ++step) {
         const int chunk = REV ? last - 1 - step : first + step;
         __syncthreads();
-        rx.store(lx, tid);
-        ry.store(ly, tid);
+        const int id = fresh<kTight>(tid), l = id % 64, g = l / 16, m = l % 16;
+        rx.store(lx, id);
+        ry.store(ly, id);
         if (wave == 0) decay += put_decays<C>(dec, rg, lane);
         if constexpr (!SUM) {
-            float* dst = a.ds + ((s.slot + chunk) * a.Hv + h) * size + v0 + row;
+            float* dst = a.ds + ((s.slot + chunk) * a.Hv + h) * size + int64_t(m) * a.VP + v0 + wave * 16 * CT + 4 * CT * g;
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
-                for (int r = 0; r < KT; ++r) *reinterpret_cast<f32x4*>(dst + int64_t(16 * r + m) * a.VP + 4 * c) = X[c][r];
+                for (int r = 0; r < KT; ++r) *reinterpret_cast<f32x4*>(dst + int64_t(16 * r) * a.VP + 4 * c) = X[c][r];
         }
         __syncthreads();
         if (step + 1 < last - first) load(REV ? chunk - 1 : chunk + 1);
