@@ -7,9 +7,9 @@ namespace {
 
 struct DcaPlan {
     int rc;
-    int kb, ct, chunk;
+    int kb, ct, block;
     int64_t slots, seg_slots, segs, seg_tokens, tokens, vp;
-    int64_t states, seg, decays, part;         // bytes of S0 (or dS1) of every chunk, and of the workspace's parts
+    int64_t states, seg, decays, part;         // bytes of S0 (or dS1) of every block, and of the workspace's parts
     int64_t q_bytes, out, gates, fin;
 };
 
@@ -17,8 +17,8 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 // Blocks that a pass over a sequence wants: two to each of 256 CUs.
 constexpr int64_t kBlocks = 512;
-// Chunks to a segment, at least: shorter ones cost more in states through memory than they gain.
-constexpr int64_t kLeast = 4;
+// Tokens to a segment, at least: shorter ones cost more in states through memory than they gain.
+constexpr int64_t kLeast = 128;
 
 DcaPlan dca_plan(const dca_dims* dims) {
     DcaPlan p{};
@@ -34,19 +34,19 @@ DcaPlan dca_plan(const dca_dims* dims) {
     if (blocks < 0 || blocks >= (int64_t(1) << 23)) return p;
     p.kb = d.K <= 32 ? 1 : d.K <= 64 ? 2 : 4;
     p.ct = d.V <= 64 ? 1 : 2;
-    p.chunk = dca_chunk(d.dtype);
+    p.block = dca_block(d.dtype, p.kb);
     p.vp = (d.V + 64 * p.ct - 1) / (64 * p.ct) * (64 * p.ct);
-    const int64_t per = (d.T + p.chunk - 1) / p.chunk;
-    p.slots = !d.T || !d.N ? 0 : d.packed ? d.T / p.chunk + d.N : d.N * per;
+    const int64_t per = (d.T + p.block - 1) / p.block;
+    p.slots = !d.T || !d.N ? 0 : d.packed ? d.T / p.block + d.N : d.N * per;
     // Segments: as many as fill the card where sequences, heads and columns do not.
     const int64_t wide = d.Hv * (p.vp / (64 * p.ct));
     int64_t len = per > 0 ? per : 1;
     if (d.N && d.N * wide < kBlocks) {
         const int64_t share = (d.packed ? per : d.N * per) * wide / kBlocks + 1;
-        len = share > kLeast ? share : kLeast;
+        len = share * p.block > kLeast ? share : kLeast / p.block;
         if (len > per) len = per > 0 ? per : 1;
     }
-    p.seg_tokens = len * p.chunk;
+    p.seg_tokens = len * p.block;
     p.segs = per > len ? (per + len - 1) / len : 1;
     p.seg_slots = d.packed ? d.T / p.seg_tokens + d.N : d.N * p.segs;
     p.tokens = d.B * d.T;
@@ -75,7 +75,7 @@ DcaArgs arguments(const dca_dims& d, const DcaPlan& p, const void* q, const void
     a.gs[0] = d.head_decay ? 0 : d.T * d.Hv;
     a.gs[1] = d.head_decay ? 0 : d.Hv;
     a.gs[2] = 1;
-    a.T = d.T; a.N = d.N; a.chunks = (d.T + p.chunk - 1) / p.chunk; a.segs = p.segs;
+    a.T = d.T; a.N = d.N; a.blocks = (d.T + p.block - 1) / p.block; a.segs = p.segs;
     a.slots = p.slots; a.seg_slots = p.seg_slots; a.seg_tokens = p.seg_tokens;
     a.Hk = int(d.Hk); a.Hv = int(d.Hv); a.group = int(d.Hv / d.Hk); a.K = int(d.K); a.V = int(d.V); a.VP = int(p.vp);
     a.tiles = int(p.vp / (64 * p.ct));
@@ -143,7 +143,7 @@ int dca_fwd(const dca_dims* dims, const void* query, const void* key, const void
     hipError_t err = hipSuccess;
     if (p.segs > 1) {
         err = qc::launch_dca_state(d.dtype, p.kb, p.ct, false, true, a, st);
-        if (err == hipSuccess) err = qc::launch_dca_join(d.dtype, p.kb, false, a, st);
+        if (err == hipSuccess) err = qc::launch_dca_join(p.kb, false, a, st);
     }
     if (err == hipSuccess) err = qc::launch_dca_fwd(d.dtype, p.kb, p.ct, a, st);
     return err == hipSuccess ? QC_OK : qc::record_hip_error(err);
@@ -192,10 +192,10 @@ int dca_bwd(const dca_dims* dims, const void* query, const void* key, const void
     if (d.N) {
         if (p.segs > 1) {
             err = qc::launch_dca_state(d.dtype, p.kb, p.ct, true, true, a, st);
-            if (err == hipSuccess) err = qc::launch_dca_join(d.dtype, p.kb, true, a, st);
+            if (err == hipSuccess) err = qc::launch_dca_join(p.kb, true, a, st);
         }
         if (err == hipSuccess) err = qc::launch_dca_state(d.dtype, p.kb, p.ct, true, false, a, st);
-        if (err == hipSuccess && (d_query || d_key || d_value || d_log_decay)) err = qc::launch_dca_grad(d.dtype, p.kb, p.ct, a, st);
+        if (err == hipSuccess && (d_query || d_key || d_value || d_log_decay)) err = qc::launch_dca_grad(d.dtype, p.kb, a, st);
     }
     // (Without tokens there are no sums, and a head's decay has a gradient of zero.)
     if (err == hipSuccess && heads) err = qc::launch_dca_heads(a, d_log_decay, st);

@@ -51,6 +51,8 @@
 namespace qc {
 
 constexpr int dca_chunk(int dt) { return dt == 1 ? 64 : 32; }
+// Tokens to a block of dca_grad, with the states at whose ends the other passes leave to it: whole chunks.
+constexpr int dca_block(int dt, int) { return dca_chunk(dt); }
 constexpr int dca_parts(int dt) { return dt == 0 ? 3 : 2; }        // of operands computed on the way to an output
 
 struct DcaArgs {
@@ -59,17 +61,17 @@ struct DcaArgs {
     const int32_t* offsets;
     void* out;
     float* fin;
-    float* save;                        // S0 of every chunk: [slots][Hv][KP][VP] (or null)
+    float* save;                        // S0 of every block of dca_block tokens: [slots][Hv][KP][VP] (or null)
     float* seg;                         // workspace: states at segments' starts (backward: dS at their ends), as save
     float* seg_decay;                   // workspace: [segment slots][Hv]
     const void* d_out;
     const float* d_fin;
     void *dq, *dk, *dv;
     float *dg, *ds0;
-    float* ds;                          // workspace: dS1 of every chunk
-    float* dg_part;                     // workspace: sums of dg over chunks [slots][Hv], for decays of the head alone
+    float* ds;                          // workspace: dS1 of every block
+    float* dg_part;                     // workspace: sums of dg over blocks [slots][Hv], for decays of the head alone
     int64_t qs[3], ks[3], vs[3], gs[3]; // gs: of log_decay, zeros for batch and token where it is of the head alone
-    int64_t T, N, chunks, segs;         // chunks, segs: per sequence, without offsets
+    int64_t T, N, blocks, segs;         // blocks, segs: per sequence, without offsets
     int64_t slots, seg_slots, seg_tokens;
     int Hk, Hv, group, K, V, VP, tiles; // tiles: blocks of 64 CT columns of V
     int vec_qk, vec_v, vec_o;           // rows on 16 bytes and sizes multiples of 8
@@ -78,8 +80,8 @@ struct DcaArgs {
 
 hipError_t launch_dca_fwd(int dt, int kb, int ct, const DcaArgs& a, hipStream_t st);
 hipError_t launch_dca_state(int dt, int kb, int ct, bool rev, bool sum, const DcaArgs& a, hipStream_t st);
-hipError_t launch_dca_join(int dt, int kb, bool rev, const DcaArgs& a, hipStream_t st);
-hipError_t launch_dca_grad(int dt, int kb, int ct, const DcaArgs& a, hipStream_t st);
+hipError_t launch_dca_join(int kb, bool rev, const DcaArgs& a, hipStream_t st);
+hipError_t launch_dca_grad(int dt, int kb, const DcaArgs& a, hipStream_t st);
 hipError_t launch_dca_heads(const DcaArgs& a, float* out, hipStream_t st);
 
 // Calls f(dtype, blocks of K, column tiles of a wave) with all as constants.
@@ -93,18 +95,19 @@ hipError_t by_dca_shape(int dt, int kb, int ct, F&& f) {
 // Device helpers ----------------------------------------------------------------
 
 struct Span {
-    int64_t b, t0, slot, seg;          // first token, first chunk's slot, first segment's slot
+    int64_t b, t0, slot, seg;          // first token, first block's slot, first segment's slot
     int len;
 };
 
-template <int C>
+// BL: tokens to a block.
+template <int BL>
 __device__ __forceinline__ Span span_of(const DcaArgs& a, int64_t n) {
-    if (!a.offsets) return {n, 0, n * a.chunks, n * a.segs, int(a.T)};
+    if (!a.offsets) return {n, 0, n * a.blocks, n * a.segs, int(a.T)};
     int64_t lo = a.offsets[n], hi = a.offsets[n + 1];
     lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
     hi = hi < lo ? lo : hi > a.T ? a.T : hi;
     // Consecutive sequences' slots cannot meet: floor((lo + len) / s) + 1 >= floor(lo / s) + max(1, ceil(len / s)).
-    return {0, lo, lo / C + n, lo / a.seg_tokens + n, int(hi - lo)};
+    return {0, lo, lo / BL + n, lo / a.seg_tokens + n, int(hi - lo)};
 }
 
 __device__ __forceinline__ int segments_of(const DcaArgs& a, const Span& s) {
@@ -112,14 +115,14 @@ __device__ __forceinline__ int segments_of(const DcaArgs& a, const Span& s) {
     return n > 1 ? n : 1;
 }
 
-// The last sequence whose first slot (of chunks, or of segments) is at or before this one.
-template <int C, bool SEG>
+// The last sequence whose first slot (of blocks, or of segments) is at or before this one.
+template <int BL, bool SEG>
 __device__ __forceinline__ int64_t owner(const DcaArgs& a, int64_t slot) {
-    if (!a.offsets) return slot / (SEG ? a.segs : a.chunks);
+    if (!a.offsets) return slot / (SEG ? a.segs : a.blocks);
     int64_t lo = 0, hi = a.N - 1;
     while (lo < hi) {
         const int64_t mid = (lo + hi + 1) / 2;
-        const Span s = span_of<C>(a, mid);
+        const Span s = span_of<BL>(a, mid);
         if ((SEG ? s.seg : s.slot) <= slot) lo = mid;
         else hi = mid - 1;
     }
@@ -181,8 +184,8 @@ __device__ __forceinline__ void col_fragment(const char* t, int b, int g, int m,
 }
 
 // Fragments of P and Phi in LDS: row tile i (16 tokens) and block b (32 tokens) at or before it.
-constexpr int dca_tri(int c) { return c == 64 ? 6 : 2; }
-__device__ __forceinline__ int tri_of(int i, int b) { return i < 2 ? i : 2 * i - 2 + b; }
+constexpr int dca_tri(int c) { return (c / 32) * (c / 32 + 1); }
+__host__ __device__ constexpr int tri_of(int i, int b) { return ((i >> 1) + (i & 1)) * ((i >> 1) + 1) + b; }
 
 // The same across rows: column tile j's tokens 16 j + m, rows 32 b + 8 g + .. .
 template <int NP>
@@ -197,21 +200,21 @@ __device__ __forceinline__ void tri_cols(const bf16x8 (*p)[NP][64], int b, int g
     }
 }
 
-// C tokens of W columns on their way from memory to LDS, by 256 threads: loaded
+// C tokens of W columns on their way from memory to LDS, by NT threads: loaded
 // in one place, taken apart and stored in a later one.  Tokens from `rem` on and
 // columns from `width` on are zero.  vec: rows on 16 bytes, width a multiple of 8.
-template <int DT, int C, int W>
+template <int DT, int C, int W, int NT = 256>
 struct Rows {
     using E = typename Storage<DT>::type;
-    static constexpr int kAll = C * W / 8, kMine = (kAll + 255) / 256, kWords = 8 * sizeof(E) / 16, kPer = 16 / sizeof(E);
+    static constexpr int kAll = C * W / 8, kMine = (kAll + NT - 1) / NT, kWords = 8 * sizeof(E) / 16, kPer = 16 / sizeof(E);
     typedef E Piece __attribute__((ext_vector_type(16 / sizeof(E))));
     Piece x[kMine][kWords];
 
     __device__ __forceinline__ void load(const E* p, int64_t stride, int rem, int width, bool vec, int tid) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            const int at = tid + i * 256, token = at / (W / 8), c = at % (W / 8) * 8;
-            const bool in = (kAll % 256 == 0 || at < kAll) && token < rem && c < width;
+            const int at = tid + i * NT, token = at / (W / 8), c = at % (W / 8) * 8;
+            const bool in = (kAll % NT == 0 || at < kAll) && token < rem && c < width;
             const E* s = p + token * stride + c;
 #pragma unroll
             for (int w = 0; w < kWords; ++w) {
@@ -229,8 +232,8 @@ struct Rows {
         constexpr int NP = parts_of(DT);
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            const int at = tid + i * 256, token = at / (W / 8), c = at % (W / 8);
-            if (kAll % 256 && at >= kAll) continue;
+            const int at = tid + i * NT, token = at / (W / 8), c = at % (W / 8);
+            if (kAll % NT && at >= kAll) continue;
             bf16x8 y[NP];
             if constexpr (DT == 1) {
                 y[0] = x[i][0];
@@ -255,26 +258,29 @@ struct Decays {
 
 __device__ __forceinline__ float exp2_of(double x) { return __builtin_amdgcn_exp2f(float(x)); }
 
-// Lane t's cumulated log2 decay from its token's log decay.
+// One wave: lane l has the log decays of tokens l and, with C = 128, 64 + l (none: zero).  Returns the chunk's whole log2 decay.
 template <int C>
-__device__ __forceinline__ double cumulated(float g, int lane) {
-    double x = double(g < -1e4f ? -1e4f : g) * 1.4426950408889634;
+__device__ __forceinline__ double put_decays(Decays<C>& d, const float (&g)[C > 64 ? 2 : 1], int lane) {
+    constexpr int N = C > 64 ? 2 : 1, kLanes = C < 64 ? C : 64;
+    double x[N], last = 0.;
 #pragma unroll
-    for (int i = 1; i < C; i *= 2) {
-        const double y = __shfl_up(x, i, 64);
-        if (lane >= i) x += y;
+    for (int n = 0; n < N; ++n) {
+        x[n] = double(g[n] < -1e4f ? -1e4f : g[n]) * 1.4426950408889634;
+#pragma unroll
+        for (int i = 1; i < kLanes; i *= 2) {
+            const double y = __shfl_up(x[n], i, 64);
+            if (lane >= i) x[n] += y;
+        }
+        x[n] += last;
+        last = __shfl(x[n], kLanes - 1, 64);
     }
-    return x;
-}
-
-// One wave: lane t's token (lanes from C on: none, g zero).  Returns the chunk's whole log2 decay.
-template <int C>
-__device__ __forceinline__ double put_decays(Decays<C>& d, float g, int lane) {
-    const double x = cumulated<C>(g, lane), last = __shfl(x, C - 1, 64);
-    if (lane < C) {
-        d.cum[lane] = x;
-        d.gamma[lane] = exp2_of(x);
-        d.eta[lane] = exp2_of(last - x);
+    if (lane < kLanes) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            d.cum[64 * n + lane] = x[n];
+            d.gamma[64 * n + lane] = exp2_of(x[n]);
+            d.eta[64 * n + lane] = exp2_of(last - x[n]);
+        }
     }
     return last;
 }

@@ -14,7 +14,7 @@ namespace {
 template <int DT, int KB, int CT, bool SAVE>
 __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
     using E = typename Storage<DT>::type;
-    constexpr int C = dca_chunk(DT), NP = parts_of(DT), PP = dca_parts(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 64 * CT, KT = 2 * KB;
+    constexpr int C = dca_chunk(DT), BL = dca_block(DT, KB), NP = parts_of(DT), PP = dca_parts(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 64 * CT, KT = 2 * KB;
     // Rows of Q, K and V; between chunks, a wave's columns of S on their way to memory.
     __shared__ __align__(16) char rows[NP * C * (2 * KP + VW) * 2];
     char *lq = rows, *lk = lq + NP * C * KP * 2, *lv = lk + NP * C * KP * 2;
@@ -25,8 +25,8 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
     int64_t u;
     int part;
     if (!dca_unit(a.seg_slots * a.Hk, a.group * a.tiles, u, part)) return;
-    const int64_t seg_slot = u / a.Hk, n = owner<C, true>(a, seg_slot);
-    const Span s = span_of<C>(a, n);
+    const int64_t seg_slot = u / a.Hk, n = owner<BL, true>(a, seg_slot);
+    const Span s = span_of<BL>(a, n);
     const int hk = int(u % a.Hk), h = hk * a.group + part / a.tiles, v0 = part % a.tiles * VW;
     const int64_t seg = seg_slot - s.seg;
     const int segs = segments_of(a, s);
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
     E* out = static_cast<E*>(a.out) + ((s.b * a.T + s.t0) * a.Hv + h) * int64_t(a.V);
     Rows<DT, C, KP> rq, rk;
     Rows<DT, C, VW> rv;
-    float rg = 0.f;
+    float rg[1] = {0.f};
     auto load = [&](int c) {
         const int64_t t = int64_t(c) * C;
         const int rem = int(s.len - t);
@@ -68,20 +68,20 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
         rq.load(q + t * a.qs[1], a.qs[1], rem, a.K, a.vec_qk, id);
         rk.load(k + t * a.ks[1], a.ks[1], rem, a.K, a.vec_qk, id);
         rv.load(v + t * a.vs[1], a.vs[1], rem, a.V - v0, a.vec_v, id);
-        rg = lane < C && lane < rem ? gd[(t + lane) * a.gs[1]] : 0.f;
+        rg[0] = lane < C && lane < rem ? gd[(t + lane) * a.gs[1]] : 0.f;
     };
     if (first < last) load(first);
     for (int chunk = first; chunk < last; ++chunk) {
         const int rem = s.len - chunk * C;
         __syncthreads();
-        if constexpr (SAVE) {
+        if (SAVE && chunk % (BL / C) == 0) {
             // S0, 32 rows at a time: lanes hold a column's, memory wants a row's.  (Stored as they are, four bytes a lane,
             // 4 x 4096 tokens of 32 heads of 128 took 560 us instead of 287.)
             constexpr int kStep = 36, kLanes = 4 * CT;
             static_assert(4 * 16 * CT * kStep * 4 <= sizeof(rows), "the columns' place");
             const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
             float* t = reinterpret_cast<float*>(rows) + wave * (16 * CT * kStep);
-            float* dst = a.save + ((s.slot + chunk) * a.Hv + h) * int64_t(KP) * a.VP + int64_t(l / kLanes) * a.VP + vw + l % kLanes * 4;
+            float* dst = a.save + ((s.slot + chunk / (BL / C)) * a.Hv + h) * int64_t(KP) * a.VP + int64_t(l / kLanes) * a.VP + vw + l % kLanes * 4;
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll

@@ -1,340 +1,404 @@
-// dca_grad.hip -- gradients of linear attention with decays, chunk by chunk
+// dca_grad.hip -- gradients of linear attention with decays, block by block of tokens
 // (include/decay_attention.h; formulas and layouts in dca_chunk.hpp).
 #include "dca_chunk.hpp"
 
 namespace qc {
 namespace {
 
-// Sum over the 16 lanes that share lane / 16, in each of them.
-__device__ __forceinline__ float sum16(float x) {
-#pragma unroll
-    for (int i = 1; i < 16; i *= 2) x += __shfl_xor(x, i, 64);
-    return x;
+// x added over the lanes that share lane % 16, and over those that share lane / 16, in each of them.
+__device__ __forceinline__ float sum_over_rows(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const float y = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const uint32_t w = __float_as_uint(y);
+    const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+template <int N>
+__device__ __forceinline__ float turned(float x) {      // lane l's: that of lane l - N of its 16
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + N, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float sum_over_columns(float x) {
+    x += turned<1>(x);
+    x += turned<2>(x);
+    x += turned<4>(x);
+    return x + turned<8>(x);
 }
 
-// One chunk and key head to a block, its value heads one after the other, so
-// that a shared head's gradients are summed in registers in one order.  Four
-// waves.  P and Phi: a wave makes the 16 rows of its own tile.  dQ^T and dK^T
-// [KP, tokens]: a wave has a quarter of the rows (of 32 in all: half, and half
-// of the tokens); dV^T [64 CT, tokens]: a quarter.  S0 and dS1 come from memory
-// as rows, and as columns for dV.
-template <int DT, int KB, int CT>
-__global__ void __launch_bounds__(256, DT == 0 ? 1 : 2) dca_grad_kernel(DcaArgs a) {
+// One block of C = dca_block tokens and one key head to a thread block, its value
+// heads one after the other, so that a shared head's gradients are summed in
+// registers in one order, and 32 columns of V at a time.  P and Phi: pairs of a
+// 16-token tile of rows and a 32-token block of columns, each wave every fourth.
+// dQ^T and dK^T [KP, tokens]: a wave has a quarter of the rows (of 32 in all:
+// half, and half of the tokens).  dV^T [32, tokens]: 16 columns of V and half of
+// the tokens.  S0 and dS1 come from memory as rows, the next 32 columns' while
+// these are worked on; dV takes dS1's columns from LDS.
+template <int DT, int KB>
+__global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kernel(DcaArgs a) {
     using E = typename Storage<DT>::type;
-    constexpr int C = dca_chunk(DT), NP = parts_of(DT), PP = dca_parts(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 64 * CT;
-    constexpr int KW = KB == 4 ? 2 : 1, TW = KB == 1 ? TT / 2 : TT;       // a wave's tiles of K rows and of tokens
-    __shared__ __align__(16) char lq[NP * C * KP * 2], lk[NP * C * KP * 2], lv[NP * C * VW * 2], lo[NP * C * VW * 2];
-    __shared__ __align__(16) bf16x8 lp[dca_tri(C)][PP][64];
-    __shared__ __align__(16) Decays<C> dec;
+    constexpr int C = dca_block(DT, KB), NP = parts_of(DT), PP = dca_parts(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 32, KT = 2 * KB;
+    constexpr int NW = 4, NT = 64 * NW;
+    constexpr bool kTight = DT == 1 ? KB > 1 : DT == 2 && KB == 4;
+    constexpr int KW = KT / 4 > 0 ? KT / 4 : 1;                // a wave's tiles of K rows
+    constexpr int TW = KT / 4 > 0 ? TT : TT / 2, TV = TT / 2;  // and of tokens, of dQ and dK, and of dV
+    constexpr int kPairs = dca_tri(C), PW = (kPairs + NW - 1) / NW;
+    constexpr int kHalves = C > 64 ? 2 : 1;                    // of 64 tokens
     struct Sums {
-        float reads[4][C], writes[4][C], pairs[4][C], dot[4];
+        float reads[NW][C], writes[NW][C], pairs[NW][C], dot[NW], last;
     };
-    static_assert(sizeof(Sums) <= sizeof(lo), "the sums take the cotangents' place");
-    Sums& sum = *reinterpret_cast<Sums*>(lo);
-    constexpr bool kTight = true;
+    __shared__ __align__(16) char lq[NP * C * KP * 2], lk[NP * C * KP * 2], lv[NP * C * VW * 2], lo[NP * C * VW * 2], ld[PP * KP * VW * 2];
+    __shared__ __align__(16) bf16x8 lp[kPairs][PP][64];
+    __shared__ __align__(16) Decays<C> decays[2];              // of this value head and the next
+    __shared__ Sums sum;
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), g = lane / 16, m = lane % 16;
     const int64_t slot = blockIdx.x / a.Hk;
     const int hk = int(blockIdx.x % a.Hk);
     const int64_t n = owner<C, false>(a, slot);
     const Span s = span_of<C>(a, n);
-    const int64_t chunk = slot - s.slot;
-    if (chunk < 0 || chunk * C >= s.len) {
+    const int64_t block = slot - s.slot;
+    if (block < 0 || block * C >= s.len) {
         if (a.dg_part)
-            for (int j = tid; j < a.group; j += 256) a.dg_part[slot * a.Hv + hk * a.group + j] = 0.f;
+            for (int j = tid; j < a.group; j += NT) a.dg_part[slot * a.Hv + hk * a.group + j] = 0.f;
         return;
     }
-    const int rem = int(s.len - chunk * C);
-    const int64_t t0 = s.t0 + chunk * C, size = int64_t(KP) * a.VP;
+    const int rem = int(s.len - block * C);
+    const int64_t t0 = s.t0 + block * C, size = int64_t(KP) * a.VP;
     const bool want_dg = a.dg || a.dg_part;
+    const int vtiles = a.VP / VW;
 
-    // The wave's first K row and first tile of tokens.
-    const int k0 = KB == 4 ? 32 * wave : KB == 2 ? 16 * wave : 16 * (wave & 1), tt0 = KB == 1 ? (wave >> 1) * TW : 0;
-    const int kacc = k0 + 4 * KW * g;                     // the 4 KW rows of a lane's accumulators
-    {
-        Rows<DT, C, KP> rq, rk;
-        rq.load(static_cast<const E*>(a.q) + s.b * a.qs[0] + t0 * a.qs[1] + hk * a.qs[2], a.qs[1], rem, a.K, a.vec_qk, tid);
-        rk.load(static_cast<const E*>(a.k) + s.b * a.ks[0] + t0 * a.ks[1] + hk * a.ks[2], a.ks[1], rem, a.K, a.vec_qk, tid);
-        rq.store(lq, tid);
-        rk.store(lk, tid);
-    }
-    __syncthreads();
-    f32x4 qk[JB][2];                                      // q_i.k_j of the wave's row tile, as its pairs lie in P
+    const int k0 = wave % KT * 16 * KW, tt0 = wave / KT * TW;  // the wave's rows of K, and first tile of tokens
+    const int v_col = wave % 2 * 16, tv0 = wave / 2 * TV;
+    // The wave's pair number j: row tile i, block b.
+    auto pair = [&](int j, int& i, int& b) {
+        static_assert(kPairs <= 6, "six places");
+        const int p = wave + NW * j;
+        i = p < 2 ? p : p < 4 ? 2 : 3;
+        b = p < 2 ? 0 : p & 1;
+        return p < kPairs;
+    };
+    auto products = [&](const char* x, const char* y, int i, int b, int l, f32x4 (&pt)[2], auto width) {      // x_i.y_j
+        constexpr int W = decltype(width)::value;
+        const int g = l / 16, m = l % 16;
 #pragma unroll
-    for (int b = 0; b < JB; ++b) {
-        qk[b][0] = qk[b][1] = zero4();
-        if (wave >= TT || b > (wave >> 1)) continue;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            bf16x8 qf[NP];
-            row_fragment<C, KP>(lq, 16 * wave + m, kb, g, qf);
+        for (int kb = 0; kb < W / 32; ++kb) {
+            bf16x8 xf[NP];
+            row_fragment<C, W>(x, 16 * i + m, kb, g, xf);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                bf16x8 kf[NP];
-                row_fragment<C, KP>(lk, tile_index(2 * b + e, m), kb, g, kf);
-                mma(qk[b][e], kf, qf);
+                bf16x8 yf[NP];
+                row_fragment<C, W>(y, tile_index(2 * b + e, m), kb, g, yf);
+                mma(pt[e], yf, xf);
             }
         }
+    };
+    // Rows of value head j and V's columns from v0 on, and the wave's rows of its S0 and dS1.
+    Rows<DT, C, VW, NT> rv, ro;
+    f32x4 sr[KW][2], dr[KW][2];
+    auto load_rows = [&](int j, int v0) {
+        const int h = hk * a.group + j, id = fresh<kTight>(tid);
+        rv.load(static_cast<const E*>(a.v) + s.b * a.vs[0] + t0 * a.vs[1] + h * a.vs[2] + v0, a.vs[1], rem, a.V - v0, a.vec_v, id);
+        ro.load(static_cast<const E*>(a.d_out) + ((s.b * a.T + t0) * a.Hv + h) * int64_t(a.V) + v0, int64_t(a.Hv) * a.V, rem, a.V - v0, a.vec_o, id);
+    };
+    auto load_states = [&](int j, int v0) {
+        const int l = fresh<kTight>(lane);
+        const int64_t at = (slot * a.Hv + hk * a.group + j) * size + int64_t(k0 + l % 16) * a.VP + v0 + 8 * (l / 16);
+#pragma unroll
+        for (int e = 0; e < KW; ++e)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                sr[e][x] = *reinterpret_cast<const f32x4*>(a.save + at + int64_t(16 * e) * a.VP + 4 * x);
+                dr[e][x] = *reinterpret_cast<const f32x4*>(a.ds + at + int64_t(16 * e) * a.VP + 4 * x);
+            }
+    };
+    auto make_decays = [&](int j) {
+        const int h = hk * a.group + j;
+        float x[kHalves];
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i) {
+            const int t = 64 * i + lane;
+            x[i] = t < C && t < rem ? a.g[s.b * a.gs[0] + (t0 + t) * a.gs[1] + h * a.gs[2]] : 0.f;
+        }
+        put_decays<C>(decays[j & 1], x, lane);
+    };
+    // dg of value head j from its sums: what a token and later ones read of S0, what earlier ones leave in S1, and the
+    // pairs across it; a lane has tokens 64 i + lane.
+    auto finish = [&](int j) {
+        const int h = hk * a.group + j;
+        constexpr int kLanes = C < 64 ? C : 64;
+        float d[kHalves], z[kHalves], pairs[kHalves], x = 0.f;
+#pragma unroll
+        for (int c = 0; c < NW; ++c) x += sum.dot[c];
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i) {
+            d[i] = z[i] = pairs[i] = 0.f;
+            if (lane < kLanes)
+#pragma unroll
+                for (int c = 0; c < NW; ++c) {
+                    d[i] += sum.reads[c][64 * i + lane];
+                    z[i] += sum.writes[c][64 * i + lane];
+                    pairs[i] += sum.pairs[c][64 * i + lane];
+                }
+#pragma unroll
+            for (int k = 1; k < kLanes; k *= 2) {
+                const float y = __shfl_down(d[i], k, 64), w = __shfl_up(z[i], k, 64);
+                d[i] += lane + k < kLanes ? y : 0.f;
+                z[i] += lane >= k ? w : 0.f;
+            }
+        }
+        const float later = kHalves > 1 ? __shfl(d[kHalves - 1], 0, 64) : 0.f, sooner = __shfl(z[0], kLanes - 1, 64);
+        float all = 0.f;
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i) {
+            const int t = 64 * i + lane;
+            const float y = __shfl_up(z[i], 1, 64);
+            const float dg = sum.last * x + (d[i] + (i + 1 < kHalves ? later : 0.f)) + ((lane ? y : 0.f) + (i ? sooner : 0.f)) + pairs[i];
+            if (t < C && t < rem) {
+                if (a.dg) a.dg[(s.b * a.T + t0 + t) * a.Hv + h] = dg;
+                all += dg;
+            }
+        }
+        if (a.dg_part) {
+            all = sum_over_rows(sum_over_columns(all));
+            if (lane == 0) a.dg_part[slot * a.Hv + h] = all;
+        }
+    };
+
+    {
+        Rows<DT, C, KP, NT> rq, rk;
+        rq.load(static_cast<const E*>(a.q) + s.b * a.qs[0] + t0 * a.qs[1] + hk * a.qs[2], a.qs[1], rem, a.K, a.vec_qk, tid);
+        rk.load(static_cast<const E*>(a.k) + s.b * a.ks[0] + t0 * a.ks[1] + hk * a.ks[2], a.ks[1], rem, a.K, a.vec_qk, tid);
+        load_rows(0, 0);
+        load_states(0, 0);
+        if (wave == 0) make_decays(0);
+        rq.store(lq, tid);
+        rk.store(lk, tid);
     }
     f32x4 dq[KW][TW], dk[KW][TW];
 #pragma unroll
     for (int e = 0; e < KW; ++e)
 #pragma unroll
         for (int t = 0; t < TW; ++t) dq[e][t] = dk[e][t] = zero4();
-
     for (int j = 0; j < a.group; ++j) {
         const int h = hk * a.group + j;
-        const float* S0 = a.save + (slot * a.Hv + h) * size;
-        const float* D1 = a.ds + (slot * a.Hv + h) * size;
-        f32x4 ov[JB][2];
+        const Decays<C>& dec = decays[j & 1];
+        f32x4 ov[PW][2], rd[KW][TW], wr[KW][TW];              // O V^T; O S0^T and V dS1^T
 #pragma unroll
-        for (int b = 0; b < JB; ++b) ov[b][0] = ov[b][1] = zero4();
-        float reads[TW], writes[TW], dot = 0.f;
+        for (int p = 0; p < PW; ++p) ov[p][0] = ov[p][1] = zero4();
 #pragma unroll
-        for (int t = 0; t < TW; ++t) reads[t] = writes[t] = 0.f;
-        for (int tile = 0; tile < a.tiles; ++tile) {
+        for (int e = 0; e < KW; ++e)
+#pragma unroll
+            for (int t = 0; t < TW; ++t) rd[e][t] = wr[e][t] = zero4();
+        float dot = 0.f;
+        for (int tile = 0; tile < vtiles; ++tile) {
             const int v0 = tile * VW;
+            __syncthreads();                                  // what read the rows before is done
             {
-                Rows<DT, C, VW> rv, ro;
                 const int id = fresh<kTight>(tid);
-                rv.load(static_cast<const E*>(a.v) + s.b * a.vs[0] + t0 * a.vs[1] + h * a.vs[2] + v0, a.vs[1], rem, a.V - v0, a.vec_v, id);
-                ro.load(static_cast<const E*>(a.d_out) + ((s.b * a.T + t0) * a.Hv + h) * int64_t(a.V) + v0, int64_t(a.Hv) * a.V, rem, a.V - v0, a.vec_o, id);
-                __syncthreads();                          // what read the rows before is done
                 rv.store(lv, id);
                 ro.store(lo, id);
             }
-            if (tile == 0 && wave == 0)
-                put_decays<C>(dec, lane < C && lane < rem ? a.g[s.b * a.gs[0] + (t0 + lane) * a.gs[1] + h * a.gs[2]] : 0.f, lane);
             __syncthreads();
-            if (tile == 0 && wave < TT) {
-                const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
+            const bool more = tile + 1 < vtiles || j + 1 < a.group;
+            const int next_j = tile + 1 < vtiles ? j : j + 1, next_v = tile + 1 < vtiles ? v0 + VW : 0;
+            if (more) load_rows(next_j, next_v);
+            if (tile == 0) {                                  // (these waves have a pair less)
+                if (wave == NW - 1 && j && want_dg) finish(j - 1);
+                if (wave == NW - 2 && j + 1 < a.group) make_decays(j + 1);
+            }
 #pragma unroll
-                for (int b = 0; b < JB; ++b) {
-                    if (b > (wave >> 1)) continue;
+            for (int p = 0; p < PW; ++p) {
+                int i, b;
+                if (!pair(p, i, b)) continue;
+                const int l = fresh<kTight>(lane);
+                if (tile == 0) {
+                    f32x4 pt[2] = {zero4(), zero4()};
+                    products(lq, lk, i, b, l, pt, std::integral_constant<int, KP>{});
                     float x[8];
-                    decayed_pairs(dec, qk[b], wave, b, g, m, a.scale, x);
-                    bf16x8 p[PP];
-                    split<PP, 8>(x, p);
+                    decayed_pairs(dec, pt, i, b, l / 16, l % 16, a.scale, x);
+                    bf16x8 f[PP];
+                    split<PP, 8>(x, f);
 #pragma unroll
-                    for (int i = 0; i < PP; ++i) lp[tri_of(wave, b)][i][lane] = p[i];
+                    for (int q = 0; q < PP; ++q) lp[tri_of(i, b)][q][l] = f[q];
                 }
+                products(lo, lv, i, b, l, ov[p], std::integral_constant<int, VW>{});
+                __builtin_amdgcn_sched_barrier(0);
             }
-            if (wave < TT) {
-                const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
 #pragma unroll
-                for (int b = 0; b < JB; ++b) {
-                    if (b > (wave >> 1)) continue;
+            for (int e = 0; e < KW; ++e)
 #pragma unroll
-                    for (int x = 0; x < 2 * CT; ++x) {
-                        bf16x8 of[NP];
-                        row_fragment<C, VW>(lo, 16 * wave + m, x, g, of);
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            bf16x8 vf[NP];
-                            row_fragment<C, VW>(lv, tile_index(2 * b + e, m), x, g, vf);
-                            mma(ov[b][e], vf, of);
-                        }
-                    }
-                }
-            }
-            // O S0^T, then V dS1^T, over this block's columns of V: gamma and eta of them, and what dg needs.
-            __builtin_amdgcn_sched_barrier(0);
+                    for (int i = 0; i < 4; ++i) dot += sr[e][x][i] * dr[e][x][i];
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
                 const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
-                const char* rows = side ? lv : lo;
-                f32x4 acc[KW][TW];
+                bf16x8 sf[KW][kParts];
 #pragma unroll
-                for (int e = 0; e < KW; ++e)
+                for (int e = 0; e < KW; ++e) {
+                    const f32x4 &lo4 = side ? dr[e][0] : sr[e][0], &hi4 = side ? dr[e][1] : sr[e][1];
+                    const float y[8] = {lo4[0], lo4[1], lo4[2], lo4[3], hi4[0], hi4[1], hi4[2], hi4[3]};
+                    split<kParts, 8>(y, sf[e]);
+                    if (side && tt0 == 0) {
 #pragma unroll
-                    for (int t = 0; t < TW; ++t) acc[e][t] = zero4();
-                const int64_t place = int64_t(KW == 2 ? k0 + 8 * (m >> 2) + (m & 3) : k0 + m) * a.VP + v0 + 8 * g;
-                const float *p0 = (side ? D1 : S0) + place, *p1 = S0 + place;
-#pragma unroll
-                for (int x = 0; x < 2 * CT; ++x) {
-                    bf16x8 sf[KW][kParts];
-#pragma unroll
-                    for (int e = 0; e < KW; ++e) {
-                        float y[8];
-                        read8(p0 + int64_t(4 * e) * a.VP + 32 * x, y);
-                        if (side && want_dg) {
-                            float z[8];
-                            read8(p1 + int64_t(4 * e) * a.VP + 32 * x, z);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) dot += y[i] * z[i];
-                        }
-                        split<kParts, 8>(y, sf[e]);
+                        for (int p = 0; p < PP; ++p) *reinterpret_cast<bf16x8*>(ld + p * (KP * VW * 2) + lds_piece<VW>(k0 + 16 * e + m, g)) = sf[e][p];
                     }
-#pragma unroll
-                    for (int t = 0; t < TW; ++t) {
-                        bf16x8 rf[NP];
-                        row_fragment<C, VW>(rows, 16 * (tt0 + t) + m, x, g, rf);
-#pragma unroll
-                        for (int e = 0; e < KW; ++e) mma(acc[e][t], sf[e], rf);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
                 }
-                const int kacc = k0 + 4 * KW * g;
 #pragma unroll
                 for (int t = 0; t < TW; ++t) {
-                    const int token = 16 * (tt0 + t) + m;
-                    const float w = side ? dec.eta[token] : dec.gamma[token] * a.scale;
-                    const char* at = (side ? lk : lq) + lds_piece<KP>(token, kacc >> 3) + (kacc & 7) * 2;
-                    float sum = 0.f;
+                    bf16x8 rf[NP];
+                    row_fragment<C, VW>(side ? lv : lo, 16 * (tt0 + t) + m, 0, g, rf);
 #pragma unroll
-                    for (int e = 0; e < KW; ++e) {
-                        acc[e][t] *= w;
-                        if (side) dk[e][t] += acc[e][t];
-                        else dq[e][t] += acc[e][t];
-                        if (want_dg) {
-                            float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                            for (int p = NP - 1; p >= 0; --p) {
-                                const bf16x4 part = *reinterpret_cast<const bf16x4*>(at + p * (C * KP * 2) + 8 * e);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) x[i] += float(part[i]);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) sum += x[i] * acc[e][t][i];
-                        }
-                    }
-                    if (side) writes[t] += sum;
-                    else reads[t] += sum;
+                    for (int e = 0; e < KW; ++e) mma(side ? wr[e][t] : rd[e][t], sf[e], rf);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
+            if (more) load_states(next_j, next_v);
+            __syncthreads();                                  // P and dS1 are there
             if (a.dv) {
                 const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
-                f32x4 dv[CT][TT];
+                f32x4 dv[TV];
 #pragma unroll
-                for (int c = 0; c < CT; ++c)
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) dv[c][t] = zero4();
-                const int vw = wave * 16 * CT;
+                for (int t = 0; t < TV; ++t) dv[t] = zero4();
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
-                    bf16x8 df[CT][PP];
+                    bf16x8 df[PP];
+                    col_fragment<KP, VW>(ld, kb, g, m, v_col + 4 * (m & 3), df);
 #pragma unroll
-                    for (int c = 0; c < CT; ++c) {
-                        const float* p = D1 + int64_t(32 * kb + 8 * g) * a.VP + v0 + vw + (CT == 2 ? 8 * (m >> 2) + 4 * c + (m & 3) : m);
-                        float z[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) z[i] = p[int64_t(i) * a.VP];
-                        split<PP, 8>(z, df[c]);
-                    }
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) {
+                    for (int t = 0; t < TV; ++t) {
                         bf16x8 kf[NP];
-                        row_fragment<C, KP>(lk, 16 * t + m, kb, g, kf);
-#pragma unroll
-                        for (int c = 0; c < CT; ++c) mma(dv[c][t], df[c], kf);
+                        row_fragment<C, KP>(lk, 16 * (tv0 + t) + m, kb, g, kf);
+                        mma(dv[t], df, kf);
                     }
-                    __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    const float eta = dec.eta[16 * t + m];
-#pragma unroll
-                    for (int c = 0; c < CT; ++c) dv[c][t] *= eta;
-                }
-                if (tile == 0) __syncthreads();           // P is there
+                for (int t = 0; t < TV; ++t) dv[t] *= dec.eta[16 * (tv0 + t) + m];
 #pragma unroll
                 for (int b = 0; b < JB; ++b) {
-                    bf16x8 of[CT][NP];
+                    bf16x8 of[NP];
+                    col_fragment<C, VW>(lo, b, g, m, v_col + 4 * (m & 3), of);
 #pragma unroll
-                    for (int c = 0; c < CT; ++c) col_fragment<C, VW>(lo, b, g, m, vw + (CT == 2 ? 8 * (m & 3) + 4 * c : 4 * (m & 3)), of[c]);
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) {
-                        if (b < (t >> 1)) continue;
+                    for (int t = 0; t < TV; ++t) {
+                        if (b < ((tv0 + t) >> 1)) continue;
                         bf16x8 pf[PP];
-                        tri_cols(lp, b, g, m, t, pf);
-#pragma unroll
-                        for (int c = 0; c < CT; ++c) mma(dv[c][t], of[c], pf);
+                        tri_cols(lp, b, g, m, tv0 + t, pf);
+                        mma(dv[t], of, pf);
                     }
                 }
-                const int col = v0 + vw + 4 * CT * g;
+                const int col = v0 + v_col + 4 * g;
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    if (16 * t + m >= rem) continue;
-                    E* p = static_cast<E*>(a.dv) + ((s.b * a.T + t0 + 16 * t + m) * a.Hv + h) * int64_t(a.V) + col;
-                    float x[4 * CT];
-#pragma unroll
-                    for (int c = 0; c < CT; ++c)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[4 * c + i] = dv[c][t][i];
+                for (int t = 0; t < TV; ++t) {
+                    const int token = 16 * (tv0 + t) + m;
+                    if (token >= rem) continue;
+                    E* p = static_cast<E*>(a.dv) + ((s.b * a.T + t0 + token) * a.Hv + h) * int64_t(a.V) + col;
+                    const float x[4] = {dv[t][0], dv[t][1], dv[t][2], dv[t][3]};
                     if (a.vec_o) {
-                        if (col < a.V) store_floats<4 * CT>(p, x);
+                        if (col < a.V) store_floats<4>(p, x);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 4 * CT; ++i)
+                        for (int i = 0; i < 4; ++i)
                             if (col + i < a.V) p[i] = E(x[i]);
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        __syncthreads();                                  // P and the cotangents are done with
-        if (wave < TT) {
+        // gamma and eta of them, and what dg needs: q and k with their shares of dQ and dK.
+        float reads[TW], writes[TW];
+        {
             const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
-            f32x4 before[TT];                             // [t][i]: sum over j < t of M_ij
 #pragma unroll
-            for (int t = 0; t < TT; ++t) before[t] = zero4();
+            for (int t = 0; t < TW; ++t) {
+                const int token = 16 * (tt0 + t) + m;
+                const float gamma = dec.gamma[token] * a.scale, eta = dec.eta[token];
+                reads[t] = writes[t] = 0.f;
 #pragma unroll
-            for (int b = 0; b < JB; ++b) {
-                if (b > (wave >> 1)) continue;
-                float x[8];
-                decayed_pairs(dec, ov[b], wave, b, g, m, a.scale, x);
-                bf16x8 p[PP];
-                split<PP, 8>(x, p);
+                for (int e = 0; e < KW; ++e) {
+                    const int kacc = k0 + 16 * e + 4 * g, at = lds_piece<KP>(token, kacc >> 3) + (kacc & 7) * 2;
+                    rd[e][t] *= gamma;
+                    wr[e][t] *= eta;
+                    dq[e][t] += rd[e][t];
+                    dk[e][t] += wr[e][t];
+                    if (want_dg) {
+                        float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < PP; ++i) lp[tri_of(wave, b)][i][lane] = p[i];
-                if (want_dg) {
-                    bf16x8 mf[kParts];
+                        for (int p = NP - 1; p >= 0; --p) {
+                            const bf16x4 qp = *reinterpret_cast<const bf16x4*>(lq + at + p * (C * KP * 2));
+                            const bf16x4 kp = *reinterpret_cast<const bf16x4*>(lk + at + p * (C * KP * 2));
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] *= 32 * b + 8 * g + i < 16 * wave + m ? qk[b][i >> 2][i & 3] : 0.f;
-                    split<kParts, 8>(x, mf);
+                            for (int i = 0; i < 4; ++i) {
+                                x[i] += float(qp[i]);
+                                y[i] += float(kp[i]);
+                            }
+                        }
 #pragma unroll
-                    for (int t = 0; t < TT; ++t) {
-                        if (t > wave) continue;
-                        bf16x8 one[1];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) one[0][i] = __bf16(32 * b + 8 * g + i < 16 * t + m ? 1.f : 0.f);
-                        mma(before[t], one, mf);
+                        for (int i = 0; i < 4; ++i) {
+                            reads[t] += x[i] * rd[e][t][i];
+                            writes[t] += y[i] * wr[e][t][i];
+                        }
                     }
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();                                      // P is done with
+        float across[TT];                                     // of token 16 t + m: its pairs' M, by rows 4 g + ..
+#pragma unroll
+        for (int t = 0; t < TT; ++t) across[t] = 0.f;
+#pragma unroll
+        for (int p = 0; p < PW; ++p) {
+            int i, b;
+            if (!pair(p, i, b)) continue;
+            const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
+            float x[8];
+            decayed_pairs(dec, ov[p], i, b, g, m, a.scale, x);
+            bf16x8 f[PP];
+            split<PP, 8>(x, f);
+#pragma unroll
+            for (int q = 0; q < PP; ++q) lp[tri_of(i, b)][q][l] = f[q];
             if (want_dg) {
+                // M_ij of this pair; its sum over j < t <= i, for each t: over j with a matrix of ones.
+                f32x4 qk[2] = {zero4(), zero4()};
+                products(lq, lk, i, b, l, qk, std::integral_constant<int, KP>{});
+                bf16x8 mf[kParts];
 #pragma unroll
-                for (int t = 0; t < TT; ++t)
+                for (int c = 0; c < 8; ++c) x[c] *= 32 * b + 8 * g + c < 16 * i + m ? qk[c >> 2][c & 3] : 0.f;
+                split<kParts, 8>(x, mf);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int token = 16 * t + 4 * g + i;
-                        const float x = sum16(16 * wave + m >= token ? before[t][i] : 0.f);
-                        if (m == 0) sum.pairs[wave][token] = x;
-                    }
+                for (int t = 0; t < TT; ++t) {
+                    if (t < 2 * b || t > i) continue;
+                    bf16x8 one[1];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) one[0][c] = __bf16(32 * b + 8 * g + c < 16 * t + m ? 1.f : 0.f);
+                    f32x4 before = zero4();
+                    mma(before, mf, one);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) across[t] += 16 * i + 4 * g + c >= 16 * t + m ? before[c] : 0.f;
+                }
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (want_dg) {
-            if constexpr (TW < TT) {
-                for (int i = lane; i < C; i += 64) sum.reads[wave][i] = sum.writes[wave][i] = 0.f;
-                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const float p = sum_over_rows(across[t]);
+                if (g == 0) sum.pairs[wave][16 * t + m] = p;
+                if (TW < TT && (t < tt0 || t >= tt0 + TW) && g == 0) sum.reads[wave][16 * t + m] = sum.writes[wave][16 * t + m] = 0.f;
             }
 #pragma unroll
             for (int t = 0; t < TW; ++t) {
-                float x = reads[t], y = writes[t];
-                x += __shfl_xor(x, 16, 64);
-                y += __shfl_xor(y, 16, 64);
-                x += __shfl_xor(x, 32, 64);
-                y += __shfl_xor(y, 32, 64);
+                const float x = sum_over_rows(reads[t]), y = sum_over_rows(writes[t]);
                 if (g == 0) {
                     sum.reads[wave][16 * (tt0 + t) + m] = x;
                     sum.writes[wave][16 * (tt0 + t) + m] = y;
                 }
             }
-            float x = tt0 == 0 ? dot : 0.f;               // (each row of S0 once)
-#pragma unroll
-            for (int i = 1; i < 64; i *= 2) x += __shfl_xor(x, i, 64);
-            if (lane == 0) sum.dot[wave] = x;
+            const float x = sum_over_rows(sum_over_columns(tt0 == 0 ? dot : 0.f));      // (each row of S0 once)
+            if (lane == 0) {
+                sum.dot[wave] = x;
+                if (wave == 0) sum.last = dec.gamma[C - 1];
+            }
         }
-        __syncthreads();
+        __syncthreads();                                      // Phi and the sums are there
         if (a.dq || a.dk) {
             const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
 #pragma unroll
@@ -342,9 +406,8 @@ __global__ void __launch_bounds__(256, DT == 0 ? 1 : 2) dca_grad_kernel(DcaArgs 
                 bf16x8 kf[KW][NP], qf[KW][NP];
 #pragma unroll
                 for (int e = 0; e < KW; ++e) {
-                    const int col = KW == 2 ? k0 + 8 * (m & 3) + 4 * e : k0 + 4 * (m & 3);
-                    col_fragment<C, KP>(lk, b, g, m, col, kf[e]);
-                    col_fragment<C, KP>(lq, b, g, m, col, qf[e]);
+                    col_fragment<C, KP>(lk, b, g, m, k0 + 16 * e + 4 * (m & 3), kf[e]);
+                    col_fragment<C, KP>(lq, b, g, m, k0 + 16 * e + 4 * (m & 3), qf[e]);
                 }
 #pragma unroll
                 for (int t = 0; t < TW; ++t) {
@@ -352,7 +415,7 @@ __global__ void __launch_bounds__(256, DT == 0 ? 1 : 2) dca_grad_kernel(DcaArgs 
                     bf16x8 pf[PP];
                     if (b <= (tile >> 1)) {
 #pragma unroll
-                        for (int i = 0; i < PP; ++i) pf[i] = lp[tri_of(tile, b)][i][lane];
+                        for (int i = 0; i < PP; ++i) pf[i] = lp[tri_of(tile, b)][i][l];
 #pragma unroll
                         for (int e = 0; e < KW; ++e) mma(dq[e][t], kf[e], pf);
                     }
@@ -363,62 +426,32 @@ __global__ void __launch_bounds__(256, DT == 0 ? 1 : 2) dca_grad_kernel(DcaArgs 
                     }
                 }
             }
-        }
-        if (want_dg && wave == 0) {
-            // A lane's token t: what it and later tokens read of S0, what earlier ones leave in S1, and the pairs across it.
-            float d = 0.f, z = 0.f, pairs = 0.f, x = 0.f;
-            if (lane < C) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    d += sum.reads[c][lane];
-                    z += sum.writes[c][lane];
-                    if (c < TT) pairs += sum.pairs[c][lane];
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) x += sum.dot[c];
-#pragma unroll
-            for (int i = 1; i < C; i *= 2) {
-                const float y = __shfl_down(d, i, 64), w = __shfl_up(z, i, 64);
-                d += lane + i < C ? y : 0.f;
-                z += lane >= i ? w : 0.f;
-            }
-            z = __shfl_up(z, 1, 64);
-            float dg = dec.gamma[C - 1] * x + d + (lane ? z : 0.f) + pairs;
-            if (a.dg && lane < C && lane < rem) a.dg[(s.b * a.T + t0 + lane) * a.Hv + h] = dg;
-            if (a.dg_part) {
-                dg = lane < C && lane < rem ? dg : 0.f;
-#pragma unroll
-                for (int i = 1; i < 64; i *= 2) dg += __shfl_xor(dg, i, 64);
-                if (lane == 0) a.dg_part[slot * a.Hv + h] = dg;
-            }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
+    if (want_dg && wave == NW - 1) finish(a.group - 1);
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
         const int token = 16 * (tt0 + t) + m;
         if (token >= rem) continue;
-        const int64_t at = ((s.b * a.T + t0 + token) * a.Hk + hk) * a.K + kacc;
-        float x[4 * KW], y[4 * KW];
 #pragma unroll
-        for (int e = 0; e < KW; ++e)
+        for (int e = 0; e < KW; ++e) {
+            const int kacc = k0 + 16 * e + 4 * g;
+            const int64_t at = ((s.b * a.T + t0 + token) * a.Hk + hk) * a.K + kacc;
+            const float x[4] = {dq[e][t][0], dq[e][t][1], dq[e][t][2], dq[e][t][3]}, y[4] = {dk[e][t][0], dk[e][t][1], dk[e][t][2], dk[e][t][3]};
+            E* pq = static_cast<E*>(a.dq) + at;
+            E* pk = static_cast<E*>(a.dk) + at;
+            if (a.vec_qk) {
+                if (kacc >= a.K) continue;
+                if (a.dq) store_floats<4>(pq, x);
+                if (a.dk) store_floats<4>(pk, y);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[4 * e + i] = dq[e][t][i];
-                y[4 * e + i] = dk[e][t][i];
-            }
-        E* pq = static_cast<E*>(a.dq) + at;
-        E* pk = static_cast<E*>(a.dk) + at;
-        if (a.vec_qk) {
-            if (kacc >= a.K) continue;
-            if (a.dq) store_floats<4 * KW>(pq, x);
-            if (a.dk) store_floats<4 * KW>(pk, y);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4 * KW; ++i) {
-                if (kacc + i >= a.K) continue;
-                if (a.dq) pq[i] = E(x[i]);
-                if (a.dk) pk[i] = E(y[i]);
+                for (int i = 0; i < 4; ++i) {
+                    if (kacc + i >= a.K) continue;
+                    if (a.dq) pq[i] = E(x[i]);
+                    if (a.dk) pk[i] = E(y[i]);
+                }
             }
         }
     }
@@ -441,10 +474,10 @@ __global__ void __launch_bounds__(256) dca_heads_kernel(const float* part, int64
 
 }  // namespace
 
-hipError_t launch_dca_grad(int dt, int kb, int ct, const DcaArgs& a, hipStream_t st) {
+hipError_t launch_dca_grad(int dt, int kb, const DcaArgs& a, hipStream_t st) {
     if (!a.slots) return hipSuccess;
-    return by_dca_shape(dt, kb, ct, [&](auto d, auto k, auto c) {
-        const void* fn = reinterpret_cast<const void*>(&dca_grad_kernel<decltype(d)::value, decltype(k)::value, decltype(c)::value>);
+    return by_dtype_kb(dt, kb, [&](auto d, auto k) {
+        const void* fn = reinterpret_cast<const void*>(&dca_grad_kernel<decltype(d)::value, decltype(k)::value>);
         DcaArgs args = a;
         void* params[] = {&args};
         return hipLaunchKernel(fn, dim3(unsigned(a.slots * a.Hk)), dim3(256), params, 0, st);

@@ -9,13 +9,13 @@ namespace {
 // K, V, eta; REV, from the last chunk to the first, dS with Q, dO, scale gamma.
 // SUM: from zero, what a segment adds, stored at the segment that takes it.
 // Otherwise from the segment's state, which it leaves before each chunk (REV
-// alone: dS1), and at the end of the sequence as the gradient of s0.  A block
+// alone: dS1 of every block of dca_grad), and at the end of the sequence as the gradient of s0.  A block
 // has 64 CT columns of V, a wave 16 CT of them, held as [columns of V, KP] so
 // that a lane's accumulators are consecutive in memory, [KP][VP].
 template <int DT, int KB, int CT, bool REV, bool SUM>
 __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
     using E = typename Storage<DT>::type;
-    constexpr int C = dca_chunk(DT), NP = parts_of(DT), JB = C / 32, KP = 32 * KB, VW = 64 * CT, KT = 2 * KB;
+    constexpr int C = dca_chunk(DT), BL = dca_block(DT, KB), NP = parts_of(DT), JB = C / 32, KP = 32 * KB, VW = 64 * CT, KT = 2 * KB;
     __shared__ __align__(16) char lx[NP * C * KP * 2], ly[NP * C * VW * 2];
     __shared__ __align__(16) Decays<C> dec;
     constexpr bool kTight = DT == 1 && KB == 4 && CT == 2 && !SUM;
@@ -23,8 +23,8 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
     int64_t u;
     int part;
     if (!dca_unit(a.seg_slots * a.Hk, a.group * a.tiles, u, part)) return;
-    const int64_t seg_slot = u / a.Hk, n = owner<C, true>(a, seg_slot);
-    const Span s = span_of<C>(a, n);
+    const int64_t seg_slot = u / a.Hk, n = owner<BL, true>(a, seg_slot);
+    const Span s = span_of<BL>(a, n);
     const int hk = int(u % a.Hk), h = hk * a.group + part / a.tiles, v0 = part % a.tiles * VW;
     const int64_t seg = seg_slot - s.seg;
     const int segs = segments_of(a, s);
@@ -60,14 +60,14 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
     const float* gd = a.g + s.b * a.gs[0] + s.t0 * a.gs[1] + h * a.gs[2];
     Rows<DT, C, KP> rx;
     Rows<DT, C, VW> ry;
-    float rg = 0.f;
+    float rg[1] = {0.f};
     auto load = [&](int c) {
         const int64_t t = int64_t(c) * C;
         const int rem = int(s.len - t);
         const int id = fresh<kTight>(tid);
         rx.load(x + t * xs[1], xs[1], rem, a.K, a.vec_qk, id);
         ry.load(y + t * ys, ys, rem, a.V - v0, REV ? a.vec_o : a.vec_v, id);
-        rg = lane < C && lane < rem ? gd[(t + lane) * a.gs[1]] : 0.f;
+        rg[0] = lane < C && lane < rem ? gd[(t + lane) * a.gs[1]] : 0.f;
     };
     double decay = 0.;
     if (first < last) load(REV ? last - 1 : first);
@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
         rx.store(lx, id);
         ry.store(ly, id);
         if (wave == 0) decay += put_decays<C>(dec, rg, lane);
-        if constexpr (!SUM) {
-            float* dst = a.ds + ((s.slot + chunk) * a.Hv + h) * size + int64_t(m) * a.VP + v0 + wave * 16 * CT + 4 * CT * g;
+        if (!SUM && (chunk % (BL / C) == BL / C - 1 || chunk == all - 1)) {
+            float* dst = a.ds + ((s.slot + chunk / (BL / C)) * a.Hv + h) * size + int64_t(m) * a.VP + v0 + wave * 16 * CT + 4 * CT * g;
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -139,12 +139,12 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
 
 // The states at segments' starts (REV: dS at their ends) from what dca_state left there: one after the other, 1024
 // elements of a state to a block, eight segments' loads at once.
-template <int C, bool REV>
+template <bool REV>
 __global__ void __launch_bounds__(256) dca_join_kernel(DcaArgs a, int KP) {
     const int per = int((int64_t(KP) * a.VP + 1023) / 1024);
     const int64_t n = blockIdx.x / (int64_t(per) * a.Hv);
     const int h = int(blockIdx.x / per % a.Hv);
-    const Span s = span_of<C>(a, n);
+    const Span s = span_of<64>(a, n);         // (its blocks do not matter here)
     const int segs = segments_of(a, s);
     if (segs < 2) return;
     const int64_t size = int64_t(KP) * a.VP;
@@ -194,10 +194,8 @@ hipError_t launch_dca_state(int dt, int kb, int ct, bool rev, bool sum, const Dc
     });
 }
 
-hipError_t launch_dca_join(int dt, int kb, bool rev, const DcaArgs& a, hipStream_t st) {
-    const bool wide = dca_chunk(dt) == 64;
-    const void* fn = wide ? (rev ? reinterpret_cast<const void*>(&dca_join_kernel<64, true>) : reinterpret_cast<const void*>(&dca_join_kernel<64, false>))
-                          : (rev ? reinterpret_cast<const void*>(&dca_join_kernel<32, true>) : reinterpret_cast<const void*>(&dca_join_kernel<32, false>));
+hipError_t launch_dca_join(int kb, bool rev, const DcaArgs& a, hipStream_t st) {
+    const void* fn = rev ? reinterpret_cast<const void*>(&dca_join_kernel<true>) : reinterpret_cast<const void*>(&dca_join_kernel<false>);
     DcaArgs args = a;
     int KP = 32 * kb;
     void* params[] = {&args, &KP};
