@@ -1071,11 +1071,25 @@ def qkn_bwd(query, key, query_weight, key_weight, cos, sin, positions, d_query_o
 # Linear attention with a decay for each head (include/decay_attention.h) and
 # layer norm (include/layer_norm.h), with the same conventions.
 
+# What a call from Python costs is most of a decoding step's: the current
+# stream's handle without a Stream object (0.1 us, and 1.9 with one), outputs
+# made like an input where it is dense (1.2 us, and 2.3 from a shape).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _lm_like(t, shape):
+    """A new contiguous tensor of t's type and device."""
+    return torch.empty_like(t) if t.shape == shape and t.is_contiguous() else t.new_empty(shape)
+
+
 def _dca_dims(query, key, value, n, scale, head_decay):
     like = _gdr_dims(query, key, value, n, scale)          # the gated delta rule's shapes and checks
     d = DcaDims(*[getattr(like, x) for x in ("B", "T", "Hk", "Hv", "K", "V", "N")])
     d.q_stride, d.k_stride, d.v_stride = like.q_stride, like.k_stride, like.v_stride
     d.dtype, d.scale, d.packed, d.head_decay = like.dtype, like.scale, like.packed, int(head_decay)
+    lib = load()
+    d.workspace_bytes = [int(lib.dca_workspace_bytes(d, i)) for i in range(2)]      # (kept with the plan)
+    d.saved_bytes = int(lib.dca_saved_bytes(d))
     return d
 
 
@@ -1112,20 +1126,20 @@ def dca_fwd(query, key, value, log_decay, initial_state=None, *, scale=None, off
     if initial_state is not None:
         _lm_dense("initial_state", initial_state, states, torch.float32, device)
     lib = load()
-    ws_bytes = lib.dca_workspace_bytes(d, 0)
+    ws_bytes = d.workspace_bytes[0]
     if ws_bytes == 0:
         raise QuatCumprodError(-2, "dca_fwd")
     shape, given = (d.B, d.T, d.Hv, d.V), out
     if out is None:
-        out = (torch.empty if offsets is None else torch.zeros)(shape, dtype=query.dtype, device=device)
+        out = _lm_like(value, shape) if offsets is None else torch.zeros(shape, dtype=query.dtype, device=device)
     else:
         _lm_dense("out", out, shape, query.dtype, device)
     fin = torch.empty(states, dtype=torch.float32, device=device)
-    saved = torch.empty(lib.dca_saved_bytes(d), dtype=torch.uint8, device=device) if want_saved else None
+    saved = torch.empty(d.saved_bytes, dtype=torch.uint8, device=device) if want_saved else None
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
     rc = lib.dca_fwd(d, query.data_ptr(), key.data_ptr(), value.data_ptr(), log_decay.data_ptr(), _data_ptr(offsets),
                      _data_ptr(initial_state), out.data_ptr(), fin.data_ptr(), _data_ptr(saved), ws.data_ptr(), ws_bytes,
-                     torch.cuda.current_stream(device).cuda_stream)
+                     _raw_stream(device.index))
     _check(rc, "dca_fwd")
     _lm_written(given)
     return out, fin, saved
@@ -1146,16 +1160,15 @@ def dca_bwd(query, key, value, log_decay, saved, d_out, d_final_state=None, *, s
     if d_final_state is not None:
         _lm_dense("d_final_state", d_final_state, states, torch.float32, device)
     lib = load()
-    _lm_dense("saved", saved, (lib.dca_saved_bytes(d),), torch.uint8, device)
-    new = torch.empty if offsets is None else torch.zeros
-    grads = [new(t.shape, dtype=t.dtype, device=device) if w else None
-             for t, w in zip((query, key, value, log_decay), want)]
+    _lm_dense("saved", saved, (d.saved_bytes,), torch.uint8, device)
+    new = _lm_like if offsets is None else lambda t, shape: torch.zeros(shape, dtype=t.dtype, device=device)
+    grads = [new(t, t.shape) if w else None for t, w in zip((query, key, value, log_decay), want)]
     grads.append(torch.empty(states, dtype=torch.float32, device=device) if want[4] else None)
-    ws_bytes = lib.dca_workspace_bytes(d, 1)
+    ws_bytes = d.workspace_bytes[1]
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
     rc = lib.dca_bwd(d, query.data_ptr(), key.data_ptr(), value.data_ptr(), log_decay.data_ptr(), _data_ptr(offsets),
                      saved.data_ptr(), d_out.data_ptr(), _data_ptr(d_final_state), *[_data_ptr(g) for g in grads],
-                     ws.data_ptr(), ws_bytes, torch.cuda.current_stream(device).cuda_stream)
+                     ws.data_ptr(), ws_bytes, _raw_stream(device.index))
     _check(rc, "dca_bwd")
     return tuple(grads)
 
@@ -1179,12 +1192,12 @@ def dca_step(query, key, value, log_decay, state, slots=None, *, scale=None, out
         raise ValueError(f"state must have a slot for each of {d.B} rows, got {state.shape[0]}")
     shape, given = (d.B, d.T, d.Hv, d.V), out
     if out is None:
-        out = torch.empty(shape, dtype=query.dtype, device=device)
+        out = _lm_like(value, shape)
     else:
         _lm_dense("out", out, shape, query.dtype, device)
     rc = load().dca_step(d, query.data_ptr(), key.data_ptr(), value.data_ptr(), log_decay.data_ptr(), state.data_ptr(),
                          state.shape[0], state.stride(0) if state.shape[0] > 1 else d.Hv * d.K * d.V, _data_ptr(slots),
-                         out.data_ptr(), torch.cuda.current_stream(device).cuda_stream)
+                         out.data_ptr(), _raw_stream(device.index))
     _check(rc, "dca_step")
     _lm_written(state, given)
     return out
@@ -1214,6 +1227,7 @@ def _lnm_dims(x, by_head, eps):
     d = LnmDims(*lead, x.shape[-1])
     d.x_stride[:] = st
     d.dtype, d.by_head, d.eps = _LM_DTYPES[x.dtype], int(by_head), eps
+    d.workspace_bytes = int(load().lnm_workspace_bytes(d))      # (kept with the plan)
     return d
 
 
@@ -1238,12 +1252,12 @@ def lnm_fwd(x, weight=None, bias=None, *, eps=1e-5, want_stats=False, out=None, 
     d = _lnm_plan(x, weight, bias, eps)
     given = out
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        out = _lm_like(x, x.shape)
     else:
         _lm_dense("out", out, x.shape, x.dtype, device)
     stats = torch.empty((d.B * d.T * d.H, 4), dtype=torch.float32, device=device) if want_stats else None
     rc = load().lnm_fwd(d, x.data_ptr(), _data_ptr(weight), _data_ptr(bias), out.data_ptr(), _data_ptr(stats),
-                        torch.cuda.current_stream(device).cuda_stream)
+                        _raw_stream(device.index))
     _check(rc, "lnm_fwd")
     _lm_written(given)
     return out, stats
@@ -1259,13 +1273,12 @@ def lnm_bwd(x, weight, bias, stats, d_out, *, eps=1e-5, want=(True, True, True),
     d = _lnm_plan(x, weight, bias, eps)
     _lm_dense("d_out", d_out, x.shape, x.dtype, device)
     _lm_dense("stats", stats, (d.B * d.T * d.H, 4), torch.float32, device)
-    grads = [torch.empty(t.shape, dtype=t.dtype, device=device) if t is not None and w else None
-             for t, w in zip((x, weight, bias), want)]
+    grads = [_lm_like(t, t.shape) if t is not None and w else None for t, w in zip((x, weight, bias), want)]
     ws, nbytes = None, 0
     if grads[1] is not None or grads[2] is not None:
-        nbytes = int(load().lnm_workspace_bytes(d))
+        nbytes = d.workspace_bytes
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     rc = load().lnm_bwd(d, x.data_ptr(), _data_ptr(weight), stats.data_ptr(), d_out.data_ptr(),
-                        *[_data_ptr(g) for g in grads], _data_ptr(ws), nbytes, torch.cuda.current_stream(device).cuda_stream)
+                        *[_data_ptr(g) for g in grads], _data_ptr(ws), nbytes, _raw_stream(device.index))
     _check(rc, "lnm_bwd")
     return tuple(grads)

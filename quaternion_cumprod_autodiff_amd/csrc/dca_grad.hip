@@ -5,26 +5,6 @@
 namespace qc {
 namespace {
 
-// x added over the lanes that share lane % 16, and over those that share lane / 16, in each of them.
-__device__ __forceinline__ float sum_over_rows(float x) {
-    const uint32_t u = __float_as_uint(x);
-    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    const float y = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const uint32_t w = __float_as_uint(y);
-    const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-template <int N>
-__device__ __forceinline__ float turned(float x) {      // lane l's: that of lane l - N of its 16
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + N, 0xf, 0xf, true));
-}
-__device__ __forceinline__ float sum_over_columns(float x) {
-    x += turned<1>(x);
-    x += turned<2>(x);
-    x += turned<4>(x);
-    return x + turned<8>(x);
-}
-
 // One block of C = dca_block tokens and one key head to a thread block, its value
 // heads one after the other, so that a shared head's gradients are summed in
 // registers in one order, and 32 columns of V at a time.  P and Phi: pairs of a
@@ -158,7 +138,7 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
             }
         }
         if (a.dg_part) {
-            all = sum_over_rows(sum_over_columns(all));
+            all = lanes_sum<64>(all);
             if (lane == 0) a.dg_part[slot * a.Hv + h] = all;
         }
     };
@@ -380,19 +360,19 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
         if (want_dg) {
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
-                const float p = sum_over_rows(across[t]);
+                const float p = rows_of_lanes_sum(across[t]);
                 if (g == 0) sum.pairs[wave][16 * t + m] = p;
                 if (TW < TT && (t < tt0 || t >= tt0 + TW) && g == 0) sum.reads[wave][16 * t + m] = sum.writes[wave][16 * t + m] = 0.f;
             }
 #pragma unroll
             for (int t = 0; t < TW; ++t) {
-                const float x = sum_over_rows(reads[t]), y = sum_over_rows(writes[t]);
+                const float x = rows_of_lanes_sum(reads[t]), y = rows_of_lanes_sum(writes[t]);
                 if (g == 0) {
                     sum.reads[wave][16 * (tt0 + t) + m] = x;
                     sum.writes[wave][16 * (tt0 + t) + m] = y;
                 }
             }
-            const float x = sum_over_rows(sum_over_columns(tt0 == 0 ? dot : 0.f));      // (each row of S0 once)
+            const float x = lanes_sum<64>(tt0 == 0 ? dot : 0.f);      // (each row of S0 once)
             if (lane == 0) {
                 sum.dot[wave] = x;
                 if (wave == 0) sum.last = dec.gamma[C - 1];

@@ -34,8 +34,9 @@ struct LnArgs {
     float* part;                   // VJP: partial sums [blocks][heads][2][D] (null: no gradient of weight or bias)
     int64_t xs[3];
     int64_t T, H, rows;            // rows of a head (by_head), or all
-    int64_t blocks;                // of a head
+    int64_t blocks;                // that share the rows
     int D, heads, flat, small;     // heads: H with by_head, else 1
+    int side, sides;               // heads of a token to a block (a power of two), and blocks for all of them
     float eps, inv;
 };
 
@@ -47,9 +48,7 @@ __device__ __forceinline__ int64_t ln_quotient(int64_t n, int64_t d, bool small)
 template <int TR, int N>
 __device__ __forceinline__ void row_sums(float (&x)[N], float (*red)[N]) {
 #pragma unroll
-    for (int m = 1; m < (TR < 64 ? TR : 64); m *= 2)
-#pragma unroll
-        for (int n = 0; n < N; ++n) x[n] += __shfl_xor(x[n], m, 64);
+    for (int n = 0; n < N; ++n) x[n] = lanes_sum<(TR < 64 ? TR : 64)>(x[n]);
     if constexpr (TR > 64) {
         __syncthreads();
         if (threadIdx.x % 64 == 0)
@@ -66,181 +65,284 @@ __device__ __forceinline__ void row_sums(float (&x)[N], float (*red)[N]) {
     }
 }
 
-template <int DT, int W, int S, int TR, bool BWD>
+// R rows of a group of TR threads at once, so that their loads are under way together.
+template <int DT, int W, int S, int TR, int R, bool BWD>
 __global__ void __launch_bounds__(TR > kLnThreads ? TR : kLnThreads) ln_kernel(LnArgs a) {
     using E = typename Storage<DT>::type;
     constexpr int kBlock = TR > kLnThreads ? TR : kLnThreads, kGroups = kBlock / TR;
+    constexpr bool kHeld = S * W <= 16;        // weight and bias in registers, or read again for every row (from L1)
     const int lane = threadIdx.x % TR, group = threadIdx.x / TR;
-    const int D = a.D, head = int(blockIdx.x % a.heads);
-    const int64_t block = blockIdx.x / a.heads;
+    // Groups of a block: `side` heads of a token next to each other, then tokens; without heads, rows.
+    const int head = int(blockIdx.x % a.sides) * a.side + group % a.side, first = group / a.side, step = kGroups / a.side;
+    const bool on_head = head < a.heads;
+    const int D = a.D, h = on_head ? head : 0;
+    const int64_t block = blockIdx.x / a.sides;
     const bool small = a.small != 0;
-    __shared__ float red1[kBlock / 64][1], red2[kBlock / 64][2];
-    float w[S][W], b[S][W];                    // forward: weight and bias; VJP: weight, and sums of g
-    float sw[BWD ? S : 1][W];
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
+    const E *pw = a.w ? static_cast<const E*>(a.w) + int64_t(h) * D : nullptr, *pb = a.b ? static_cast<const E*>(a.b) + int64_t(h) * D : nullptr;
+    __shared__ float red1[kBlock / 64][R], red2[kBlock / 64][2 * R];
+    float hw[kHeld ? S : 1][W], hb[kHeld && !BWD ? S : 1][W];
+    float sw[BWD ? S : 1][W], sb[BWD ? S : 1][W];
+    auto get = [&](const E* p, int s, float none, float (&x)[W]) {
         const int at = (s * TR + lane) * W;
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            w[s][j] = 1.f;
-            b[s][j] = 0.f;
-            if constexpr (BWD) sw[s][j] = 0.f;
+        for (int j = 0; j < W; ++j) x[j] = none;
+        if (p && at < D) load_floats<W>(p + at, x);
+    };
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        if constexpr (kHeld) {
+            get(pw, s, 1.f, hw[s]);
+            if constexpr (!BWD) get(pb, s, 0.f, hb[s]);
         }
-        if (at < D) {
-            if (a.w) load_floats<W>(static_cast<const E*>(a.w) + int64_t(head) * D + at, w[s]);
-            if (!BWD && a.b) load_floats<W>(static_cast<const E*>(a.b) + int64_t(head) * D + at, b[s]);
-        }
+        if constexpr (BWD)
+#pragma unroll
+            for (int j = 0; j < W; ++j) sw[s][j] = sb[s][j] = 0.f;
     }
     // (Every group of a block takes as many turns as the first: the sums over more than a wave are the block's.)
-    for (int64_t r0 = block * kGroups; r0 < a.rows; r0 += a.blocks * kGroups) {
-        const bool in = r0 + group < a.rows;
-        const int64_t i = in ? r0 + group : a.rows - 1;
-        // Row i of a head is token i; without heads, row i is head i % H of token i / H.
-        int64_t row = i, src;
-        if (a.heads > 1) {
-            row = i * a.H + head;
-            if (a.flat) {
-                src = i * a.xs[1] + head * a.xs[2];
-            } else {
-                const int64_t bt = ln_quotient(i, a.T, small);
-                src = bt * a.xs[0] + (i - bt * a.T) * a.xs[1] + head * a.xs[2];
-            }
-        } else if (a.flat) {
-            src = i * a.xs[2];
-        } else {
-            const int64_t token = ln_quotient(i, a.H, small), bt = ln_quotient(token, a.T, small);
-            src = bt * a.xs[0] + (token - bt * a.T) * a.xs[1] + (i - token * a.H) * a.xs[2];
-        }
-        const E* px = static_cast<const E*>(a.x) + src;
-        float x[S][W], g[BWD ? S : 1][W];
+    for (int64_t r0 = block * (step * R); r0 < a.rows; r0 += a.blocks * (step * R)) {
+        // Rows stay as they lie in memory, half the registers of floats, and are taken apart in each pass over them.
+        Held<E, W, (W > 1)> hx[R][S], hg[BWD ? R : 1][S];
+        int64_t row[R];
+        bool in[R];
+        f32x4 st[R];
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int at = (s * TR + lane) * W;
-            if (at < D) {
-                load_floats<W>(px + at, x[s]);
-                if constexpr (BWD) load_floats<W>(static_cast<const E*>(a.gy) + row * D + at, g[s]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    x[s][j] = 0.f;
-                    if constexpr (BWD) g[s][j] = 0.f;
+        for (int k = 0; k < R; ++k) {
+            in[k] = on_head && r0 + first + k * step < a.rows;
+            const int64_t i = in[k] ? r0 + first + k * step : a.rows - 1;
+            // Row i of a head is token i; without heads, row i is head i % H of token i / H.
+            int64_t src;
+            row[k] = i;
+            if (a.heads > 1) {
+                row[k] = i * a.H + h;
+                if (a.flat) {
+                    src = i * a.xs[1] + h * a.xs[2];
+                } else {
+                    const int64_t bt = ln_quotient(i, a.T, small);
+                    src = bt * a.xs[0] + (i - bt * a.T) * a.xs[1] + h * a.xs[2];
                 }
+            } else if (a.flat) {
+                src = i * a.xs[2];
+            } else {
+                const int64_t token = ln_quotient(i, a.H, small), bt = ln_quotient(token, a.T, small);
+                src = bt * a.xs[0] + (token - bt * a.T) * a.xs[1] + (i - token * a.H) * a.xs[2];
             }
-        }
-        if constexpr (!BWD) {
-            float one[1] = {0.f}, two[2] = {0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-#pragma unroll
-                for (int j = 0; j < W; ++j) one[0] += x[s][j];
-            row_sums<TR, 1>(one, red1);
-            const float mean = one[0] * a.inv;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const bool on = (s * TR + lane) * W < D;
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    x[s][j] = on ? x[s][j] - mean : 0.f;
-                    two[0] += x[s][j];
-                    two[1] += x[s][j] * x[s][j];
-                }
-            }
-            row_sums<TR, 2>(two, red2);
-            const float m = two[0] * a.inv;
-            const float v = two[1] * a.inv - m * m, r = 1.f / sqrtf((v > 0.f ? v : v == v ? 0.f : v) + a.eps);
-            if (in && a.stats && lane == 0) *reinterpret_cast<f32x4*>(a.stats + row * 4) = f32x4{mean, m, r, 0.f};
+            if constexpr (BWD) st[k] = *reinterpret_cast<const f32x4*>(a.stats + row[k] * 4);
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 const int at = (s * TR + lane) * W;
-#pragma unroll
-                for (int j = 0; j < W; ++j) x[s][j] = (x[s][j] - m) * r * w[s][j] + b[s][j];
-                if (in && at < D) store_floats<W>(static_cast<E*>(a.y) + row * D + at, x[s]);
+                hx[k][s].load(static_cast<const E*>(a.x) + src + at, D - at);
+                if constexpr (BWD) hg[k][s].load(static_cast<const E*>(a.gy) + row[k] * D + at, D - at);
             }
-        } else {
-            const f32x4 st = *reinterpret_cast<const f32x4*>(a.stats + row * 4);
-            const float mean = st[0], m = st[1], r = st[2];
-            float two[2] = {0.f, 0.f};
+        }
+        auto renew = [&] {
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    hx[k][s].renew();
+                    if constexpr (BWD) hg[k][s].renew();
+                }
+        };
+        if constexpr (!BWD) {
+            float one[R], two[2 * R];
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                one[k] = two[2 * k] = two[2 * k + 1] = 0.f;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    float x[W];
+                    hx[k][s].get(x);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) one[k] += x[j];
+                }
+            }
+            row_sums<TR, R>(one, red1);
+            renew();
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                one[k] *= a.inv;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    if ((s * TR + lane) * W >= D) continue;
+                    float x[W];
+                    hx[k][s].get(x);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        x[j] -= one[k];
+                        two[2 * k] += x[j];
+                        two[2 * k + 1] += x[j] * x[j];
+                    }
+                }
+            }
+            row_sums<TR, 2 * R>(two, red2);
+            renew();
+            float r[R];
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const float m = two[2 * k] * a.inv, v = two[2 * k + 1] * a.inv - m * m;
+                two[2 * k] = m;
+                r[k] = 1.f / sqrtf((v > 0.f ? v : v == v ? 0.f : v) + a.eps);
+                if (in[k] && a.stats && lane == 0) *reinterpret_cast<f32x4*>(a.stats + row[k] * 4) = f32x4{one[k], m, r[k], 0.f};
+            }
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                const bool on = (s * TR + lane) * W < D;
+                const int at = (s * TR + lane) * W;
+                float w[W], b[W];
+                if constexpr (kHeld) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        w[j] = hw[s][j];
+                        b[j] = hb[s][j];
+                    }
+                } else {
+                    get(pw, s, 1.f, w);
+                    get(pb, s, 0.f, b);
+                }
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    float x[W];
+                    hx[k][s].get(x);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) x[j] = (x[j] - one[k] - two[2 * k]) * r[k] * w[j] + b[j];
+                    if (in[k] && at < D) store_floats<W>(static_cast<E*>(a.y) + row[k] * D + at, x);
+                }
+            }
+        } else {
+            float two[2 * R];
+#pragma unroll
+            for (int k = 0; k < R; ++k) two[2 * k] = two[2 * k + 1] = 0.f;
+            // h = (x - mean) r and the cotangent, 0 outside the row and the rows.
+            auto pass = [&](int k, int s, float (&h)[W], float (&g)[W]) {
+                const bool on = in[k] && (s * TR + lane) * W < D;
+                hx[k][s].get(h);
+                hg[k][s].get(g);
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
-                    x[s][j] = on ? (x[s][j] - mean - m) * r : 0.f;
-                    if (in) {
-                        sw[s][j] += g[s][j] * x[s][j];
-                        b[s][j] += g[s][j];
+                    h[j] = on ? (h[j] - st[k][0] - st[k][1]) * st[k][2] : 0.f;
+                    g[j] = on ? g[j] : 0.f;
+                }
+            };
+            auto weight = [&](int s, float (&w)[W]) {
+                if constexpr (kHeld) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) w[j] = hw[s][j];
+                } else {
+                    get(pw, s, 1.f, w);
+                }
+            };
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                float w[W];
+                weight(s, w);
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    float h[W], g[W];
+                    pass(k, s, h, g);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        sw[s][j] += g[j] * h[j];
+                        sb[s][j] += g[j];
+                        g[j] *= w[j];
+                        two[2 * k] += g[j];
+                        two[2 * k + 1] += g[j] * h[j];
                     }
-                    g[s][j] *= w[s][j];
-                    two[0] += g[s][j];
-                    two[1] += g[s][j] * x[s][j];
                 }
             }
             if (!a.y) continue;
-            row_sums<TR, 2>(two, red2);
-            const float c0 = two[0] * a.inv, c1 = two[1] * a.inv;
+            row_sums<TR, 2 * R>(two, red2);
+            renew();
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 const int at = (s * TR + lane) * W;
+                float w[W];
+                weight(s, w);
 #pragma unroll
-                for (int j = 0; j < W; ++j) x[s][j] = r * (g[s][j] - c0 - x[s][j] * c1);
-                if (in && at < D) store_floats<W>(static_cast<E*>(a.y) + row * D + at, x[s]);
+                for (int k = 0; k < R; ++k) {
+                    float h[W], g[W];
+                    pass(k, s, h, g);
+                    const float c0 = two[2 * k] * a.inv, c1 = two[2 * k + 1] * a.inv;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) h[j] = st[k][2] * (g[j] * w[j] - c0 - h[j] * c1);
+                    if (in[k] && at < D) store_floats<W>(static_cast<E*>(a.y) + row[k] * D + at, h);
+                }
             }
         }
     }
     if constexpr (BWD) {
         if (!a.part) return;
-        // The block's sums in a fixed order: groups of a wave by shuffles, waves through LDS.
-        float* part = a.part + (block * a.heads + head) * 2 * int64_t(D);
-        if constexpr (kGroups == 1) {
+        // The sums, in a fixed order.  Heads: a group's own.  Else the block's: groups of a wave by shuffles, waves through LDS.
+        if (kGroups == 1 || a.heads > 1) {
+            if (!on_head) return;
+            float* part = a.part + ((block * step + first) * a.heads + head) * 2 * int64_t(D);
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 const int at = (s * TR + lane) * W;
-                if (at < D)
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        part[at + j] = sw[s][j];
-                        part[D + at + j] = b[s][j];
-                    }
+                if (at < D) {
+                    store_floats<W>(part + at, sw[s]);
+                    store_floats<W>(part + D + at, sb[s]);
+                }
             }
         } else {
+            float* part = a.part + block * 2 * int64_t(D);
             constexpr int kSum = TR < 64 ? TR : 64, kWaves = kBlock / 64, kPer = TR < 64 ? kWaves : kBlock / TR;
-            __shared__ float red[kWaves][S * W * 2][kSum];
+            __shared__ float red[kWaves][W * 2][kSum];
 #pragma unroll
-            for (int s = 0; s < S; ++s)
+            for (int s = 0; s < S; ++s) {
+                if (s) __syncthreads();
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
 #pragma unroll
                     for (int m = TR; m < 64; m *= 2) {
                         sw[s][j] += __shfl_xor(sw[s][j], m, 64);
-                        b[s][j] += __shfl_xor(b[s][j], m, 64);
+                        sb[s][j] += __shfl_xor(sb[s][j], m, 64);
                     }
                     if (threadIdx.x % 64 < kSum) {
-                        red[threadIdx.x / 64][(s * W + j) * 2][threadIdx.x % 64] = sw[s][j];
-                        red[threadIdx.x / 64][(s * W + j) * 2 + 1][threadIdx.x % 64] = b[s][j];
+                        red[threadIdx.x / 64][j * 2][threadIdx.x % 64] = sw[s][j];
+                        red[threadIdx.x / 64][j * 2 + 1][threadIdx.x % 64] = sb[s][j];
                     }
                 }
-            __syncthreads();
-            if (threadIdx.x < TR) {
-                constexpr int kStep = TR < 64 ? 1 : TR / 64;       // waves that hold the same elements are kStep apart
+                __syncthreads();
+                const int at = (s * TR + lane) * W;
+                if (threadIdx.x < TR && at < D) {
+                    constexpr int kStep = TR < 64 ? 1 : TR / 64;       // waves that hold the same elements are kStep apart
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    const int at = (s * TR + lane) * W;
-                    if (at < D)
+                    for (int j = 0; j < W; ++j) {
+                        float tw = 0.f, tb = 0.f;
 #pragma unroll
-                        for (int j = 0; j < W; ++j) {
-                            float tw = 0.f, tb = 0.f;
-#pragma unroll
-                            for (int c = 0; c < kPer; ++c) {
-                                tw += red[threadIdx.x / 64 + c * kStep][(s * W + j) * 2][threadIdx.x % 64];
-                                tb += red[threadIdx.x / 64 + c * kStep][(s * W + j) * 2 + 1][threadIdx.x % 64];
-                            }
-                            part[at + j] = tw;
-                            part[D + at + j] = tb;
+                        for (int c = 0; c < kPer; ++c) {
+                            tw += red[threadIdx.x / 64 + c * kStep][j * 2][threadIdx.x % 64];
+                            tb += red[threadIdx.x / 64 + c * kStep][j * 2 + 1][threadIdx.x % 64];
                         }
+                        part[at + j] = tw;
+                        part[D + at + j] = tb;
+                    }
                 }
             }
         }
     }
+}
+
+struct LnShape {
+    bool wide;          // W = 8
+    int tr, s, r;       // threads of a row, runs of a thread, rows at once
+};
+
+// A row's threads and runs go by its length alone, so that its result does not depend on the rows it comes with: a wave
+// has up to 8 runs to a lane (VJP: 4) before a row gets another, since waves that wait for each other cost more than the
+// loads of one.  Where there are rows for two waves on each of 1024 SIMDs and four to spare, short ones come four to a group.
+LnShape ln_shape(int64_t D, int64_t all, bool wide, bool bwd) {
+    LnShape sh{wide, 4, 1, 1};
+    if (wide) {
+        const int64_t runs = (D + 7) / 8;
+        while (sh.tr < 64 && sh.tr < runs) sh.tr *= 2;
+        while (sh.s < (bwd ? 4 : 8) && sh.tr * sh.s < runs) sh.s *= 2;
+        while (sh.tr * sh.s < runs) sh.tr *= 2;
+        if (sh.s == 1 && all * sh.tr >= int64_t(64) * 2048 * 4) sh.r = 4;
+    } else {
+        sh.tr = D <= 1024 ? 64 : D <= 4096 ? 256 : 1024;
+        while (sh.tr * sh.s < D) sh.s *= 2;
+    }
+    return sh;
 }
 
 // The weights' gradients from the blocks' partial sums: 16 columns and 64 runs
@@ -271,30 +373,6 @@ __global__ void __launch_bounds__(16 * kLnRuns) ln_weight_kernel(const float* pa
     }
 }
 
-struct LnShape {
-    bool wide;          // W = 8
-    int tr, s;          // threads of a row, runs of a thread
-};
-
-LnShape ln_shape(int64_t D, bool wide) {
-    LnShape sh{wide, 4, 1};
-    if (wide) {
-        const int64_t runs = (D + 7) / 8;
-        while (sh.tr < 1024 && sh.tr < runs) sh.tr *= 2;
-        if (sh.tr >= 128) {          // two runs to a thread: half as many waves to join
-            sh.tr /= 2;
-            sh.s = 2;
-        }
-        if (sh.tr * sh.s < runs) sh.tr *= 2;
-    } else {
-        sh.tr = D <= 1024 ? 64 : D <= 4096 ? 256 : 1024;
-        while (sh.tr * sh.s < D) sh.s *= 2;
-    }
-    return sh;
-}
-
-int ln_groups(const LnShape& sh) { return sh.tr > kLnThreads ? 1 : kLnThreads / sh.tr; }
-
 template <class F>
 hipError_t ln_by_dtype(int dt, F&& f) {
     if (dt == 0) return f(std::integral_constant<int, 0>{});
@@ -304,12 +382,18 @@ hipError_t ln_by_dtype(int dt, F&& f) {
 
 template <int DT, bool BWD>
 const void* ln_kernel_of(const LnShape& sh) {
-#define LN_WIDE(s_, tr_) \
-    if (sh.wide && sh.s == s_ && sh.tr == tr_) return reinterpret_cast<const void*>(&ln_kernel<DT, 8, s_, tr_, BWD>);
+#define LN_WIDE(s_, tr_, r_) \
+    if (sh.wide && sh.s == s_ && sh.tr == tr_ && sh.r == r_) return reinterpret_cast<const void*>(&ln_kernel<DT, 8, s_, tr_, r_, BWD>);
 #define LN_NARROW(s_, tr_) \
-    if (!sh.wide && sh.s == s_ && sh.tr == tr_) return reinterpret_cast<const void*>(&ln_kernel<DT, 1, s_, tr_, BWD>);
-    LN_WIDE(1, 4) LN_WIDE(1, 8) LN_WIDE(1, 16) LN_WIDE(1, 32) LN_WIDE(1, 64)
-    LN_WIDE(2, 64) LN_WIDE(2, 128) LN_WIDE(2, 256) LN_WIDE(2, 512) LN_WIDE(2, 1024)
+    if (!sh.wide && sh.s == s_ && sh.tr == tr_) return reinterpret_cast<const void*>(&ln_kernel<DT, 1, s_, tr_, 1, BWD>);
+    LN_WIDE(1, 4, 1) LN_WIDE(1, 8, 1) LN_WIDE(1, 16, 1) LN_WIDE(1, 32, 1) LN_WIDE(1, 64, 1)
+    LN_WIDE(1, 4, 4) LN_WIDE(1, 8, 4) LN_WIDE(1, 16, 4) LN_WIDE(1, 32, 4) LN_WIDE(1, 64, 4)
+    LN_WIDE(2, 64, 1) LN_WIDE(4, 64, 1)
+    if constexpr (BWD) {
+        LN_WIDE(4, 128, 1) LN_WIDE(4, 256, 1) LN_WIDE(4, 512, 1)
+    } else {
+        LN_WIDE(8, 64, 1) LN_WIDE(8, 128, 1) LN_WIDE(8, 256, 1)
+    }
     LN_NARROW(1, 64) LN_NARROW(2, 64) LN_NARROW(4, 64) LN_NARROW(8, 64) LN_NARROW(16, 64)
     LN_NARROW(8, 256) LN_NARROW(16, 256) LN_NARROW(8, 1024) LN_NARROW(16, 1024)
 #undef LN_WIDE
@@ -324,7 +408,7 @@ hipError_t ln_launch(int dt, const LnShape& sh, const LnArgs& a, hipStream_t st)
         if (!fn) return hipErrorInvalidConfiguration;
         LnArgs args = a;
         void* params[] = {&args};
-        return hipLaunchKernel(fn, dim3(unsigned(a.blocks * a.heads)), dim3(unsigned(sh.tr > kLnThreads ? sh.tr : kLnThreads)), params, 0, st);
+        return hipLaunchKernel(fn, dim3(unsigned(a.blocks * a.sides)), dim3(unsigned(sh.tr > kLnThreads ? sh.tr : kLnThreads)), params, 0, st);
     });
 }
 
@@ -342,10 +426,27 @@ int ln_check(const lnm_dims* d) {
 int64_t ln_heads(const lnm_dims& d) { return d.by_head && d.H ? d.H : 1; }
 int64_t ln_rows(const lnm_dims& d) { return d.by_head ? d.B * d.T : d.B * d.T * d.H; }
 
-// Blocks of a head whose partial sums are kept: no more than there are rows, nor than fill the card.
+// Partial sums of a head: no more than fill the card.
 int64_t ln_partials(const lnm_dims& d) {
-    const int64_t share = kLnPartials / ln_heads(d), most = share > 1 ? share : 1, rows = ln_rows(d);
-    return rows < most ? rows : most;
+    int64_t groups = 1;              // of a block, the most that ln_shape makes of such rows
+    if (ln_heads(d) > 1)
+        while (groups < 64 && groups * 2 * ((d.D + 7) / 8) <= kLnThreads) groups *= 2;
+    const int64_t share = kLnPartials * groups / ln_heads(d);
+    return share > 1 ? share : 1;
+}
+
+// Grid of a call: heads to a block, blocks for the heads, and blocks that share the rows, at most `most` groups of them
+// for a head.  Returns a head's groups, of which each leaves partial sums.
+int64_t ln_grid(LnArgs& a, const LnShape& sh, int64_t most) {
+    const int groups = sh.tr > kLnThreads ? 1 : kLnThreads / sh.tr;
+    a.side = 1;
+    if (a.heads > 1)
+        while (a.side * 2 <= groups && a.side * 2 <= a.heads) a.side *= 2;
+    a.sides = (a.heads + a.side - 1) / a.side;
+    const int64_t step = groups / a.side, per = step * sh.r, n = (a.rows + per - 1) / per, cap = a.heads > 1 ? most / step : most;
+    a.blocks = n < cap ? n : cap > 1 ? cap : 1;
+    if (!a.rows) a.blocks = 0;
+    return a.blocks * (a.heads > 1 ? step : 1);
 }
 
 LnArgs ln_arguments(const lnm_dims& d, const void* x, const void* w) {
@@ -387,9 +488,8 @@ int lnm_fwd(const lnm_dims* dims, const void* x, const void* weight, const void*
     qc::LnArgs a = qc::ln_arguments(d, x, weight);
     a.b = bias; a.y = y; a.stats = stats;
     const bool wide = d.D % 8 == 0 && qc::rows_on_16(x, d.x_stride, e) && qc::aligned_to(y, 16) && qc::aligned_to(weight, 16) && qc::aligned_to(bias, 16);
-    const qc::LnShape sh = qc::ln_shape(d.D, wide);
-    const int64_t groups = qc::ln_groups(sh), most = (int64_t(1) << 20) / a.heads + 1, n = (a.rows + groups - 1) / groups;
-    a.blocks = n < most ? n : most;
+    const qc::LnShape sh = qc::ln_shape(d.D, rows, wide, false);
+    qc::ln_grid(a, sh, (int64_t(1) << 20) / a.heads + 1);
     const hipError_t err = qc::ln_launch<false>(d.dtype, sh, a, static_cast<hipStream_t>(stream));
     return err == hipSuccess ? QC_OK : qc::record_hip_error(err);
 }
@@ -425,16 +525,15 @@ int lnm_bwd(const lnm_dims* dims, const void* x, const void* weight, const float
     qc::LnArgs a = qc::ln_arguments(d, x, weight);
     a.gy = d_y; a.y = d_x; a.stats = const_cast<float*>(stats);
     a.part = sums ? static_cast<float*>(workspace) : nullptr;
-    const qc::LnShape sh = qc::ln_shape(d.D, wide);
-    const int64_t groups = qc::ln_groups(sh), n = (a.rows + groups - 1) / groups, most = sums ? qc::ln_partials(d) : (int64_t(1) << 20) / a.heads + 1;
-    a.blocks = n < most ? n : most;
+    const qc::LnShape sh = qc::ln_shape(d.D, rows, wide, true);
+    const int64_t partials = qc::ln_grid(a, sh, sums ? qc::ln_partials(d) : (int64_t(1) << 20) / a.heads + 1);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t err = hipSuccess;
-    if (a.blocks * a.heads) err = qc::ln_launch<true>(d.dtype, sh, a, st);
+    if (a.blocks) err = qc::ln_launch<true>(d.dtype, sh, a, st);
     if (err == hipSuccess && sums) {
         err = qc::ln_by_dtype(d.dtype, [&](auto t) {
             const float* part = a.part;
-            int64_t blocks = a.blocks;
+            int64_t blocks = partials;
             int heads = a.heads, D = a.D;
             void *dw = d_weight, *db = d_bias;
             void* params[] = {&part, &blocks, &heads, &D, &dw, &db};

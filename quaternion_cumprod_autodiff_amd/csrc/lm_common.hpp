@@ -81,7 +81,53 @@ struct Held {
 #pragma unroll
         for (int i = 0; i < N; ++i) y[i] = float(x[i / kPer][i % kPer]);
     }
+    // The compiler takes them for new ones: what get makes of them is made again after this, not kept in registers.
+    __device__ __forceinline__ void renew() {
+        if constexpr (N * sizeof(E) >= 4) {
+#pragma unroll
+            for (int i = 0; i < N / kPer; ++i) {
+                typedef uint32_t Words __attribute__((ext_vector_type(sizeof(Vec) / 4)));
+                Words w = __builtin_bit_cast(Words, x[i]);
+#pragma unroll
+                for (int j = 0; j < int(sizeof(Vec) / 4); ++j) {
+                    uint32_t u = w[j];
+                    asm volatile("" : "+v"(u));
+                    w[j] = u;
+                }
+                x[i] = __builtin_bit_cast(Vec, w);
+            }
+        }
+    }
 };
+
+// x added over groups of G consecutive lanes (a power of two), in each of them: in registers alone, without LDS.
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+template <int G>
+__device__ __forceinline__ float lanes_sum(float x) {
+    if constexpr (G >= 2) x += moved<0xb1>(x);        // lane l ^ 1
+    if constexpr (G >= 4) x += moved<0x4e>(x);        // l ^ 2
+    if constexpr (G >= 8) x += moved<0x141>(x);       // 7 - l of eight: the other four's sum
+    if constexpr (G >= 16) x += moved<0x140>(x);      // 15 - l of sixteen
+    if constexpr (G >= 32) {
+        const auto y = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(y[0]) + __uint_as_float(y[1]);
+    }
+    if constexpr (G >= 64) {
+        const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(y[0]) + __uint_as_float(y[1]);
+    }
+    return x;
+}
+// Over the four lanes that share lane % 16.
+__device__ __forceinline__ float rows_of_lanes_sum(float x) {
+    const auto y = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(y[0]) + __uint_as_float(y[1]);
+    const auto z = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(z[0]) + __uint_as_float(z[1]);
+}
 
 // Host checks -----------------------------------------------------------------
 
