@@ -81,8 +81,8 @@ DcaArgs arguments(const dca_dims& d, const DcaPlan& p, const void* q, const void
     a.tiles = int(p.vp / (64 * p.ct));
     a.scale = d.scale;
     const size_t e = dtype_bytes(d.dtype);
-    a.vec_v = d.V % 8 == 0 && rows_on_16(v, d.v_stride, e);
-    a.vec_qk = d.K % 8 == 0 && rows_on_16(q, d.q_stride, e) && rows_on_16(k, d.k_stride, e);
+    a.vec_v = d.V % 8 == 0 && rows_on_16(v, d.v_stride, e) && rows_near(d.v_stride[1], e);
+    a.vec_qk = d.K % 8 == 0 && rows_on_16(q, d.q_stride, e) && rows_on_16(k, d.k_stride, e) && rows_near(d.q_stride[1], e) && rows_near(d.k_stride[1], e);
     return a;
 }
 
@@ -178,7 +178,7 @@ int dca_bwd(const dca_dims* dims, const void* query, const void* key, const void
     const bool heads = d.head_decay && d_log_decay;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     qc::DcaArgs a = qc::arguments(d, p, query, key, value, log_decay, offsets);
-    a.vec_o = d.V % 8 == 0 && qc::aligned_to(d_out, 16) && qc::aligned_to(d_value, 16);
+    a.vec_o = d.V % 8 == 0 && qc::aligned_to(d_out, 16) && qc::aligned_to(d_value, 16) && qc::rows_near(d.Hv * d.V, e);
     a.vec_qk = a.vec_qk && qc::aligned_to(d_query, 16) && qc::aligned_to(d_key, 16);
     char* ws = static_cast<char*>(workspace);
     a.ds = reinterpret_cast<float*>(ws);

@@ -84,6 +84,9 @@ hipError_t launch_dca_join(int kb, bool rev, const DcaArgs& a, hipStream_t st);
 hipError_t launch_dca_grad(int dt, int kb, const DcaArgs& a, hipStream_t st);
 hipError_t launch_dca_heads(const DcaArgs& a, float* out, hipStream_t st);
 
+// Whether 64 tokens of this stride lie within 2^31 bytes.
+inline bool rows_near(int64_t stride, size_t e) { return stride < (int64_t(1) << 24) / int64_t(e); }
+
 // Calls f(dtype, blocks of K, column tiles of a wave) with all as constants.
 template <class F>
 hipError_t by_dca_shape(int dt, int kb, int ct, F&& f) {
@@ -202,7 +205,8 @@ __device__ __forceinline__ void tri_cols(const bf16x8 (*p)[NP][64], int b, int g
 
 // C tokens of W columns on their way from memory to LDS, by NT threads: loaded
 // in one place, taken apart and stored in a later one.  Tokens from `rem` on and
-// columns from `width` on are zero.  vec: rows on 16 bytes, width a multiple of 8.
+// columns from `width` on are zero.  p is the same in all lanes.  vec: rows on 16
+// bytes, width a multiple of 8, and C tokens within 2^31 bytes (rows_near).
 template <int DT, int C, int W, int NT = 256>
 struct Rows {
     using E = typename Storage<DT>::type;
@@ -211,20 +215,28 @@ struct Rows {
     Piece x[kMine][kWords];
 
     __device__ __forceinline__ void load(const E* p, int64_t stride, int rem, int width, bool vec, int tid) {
+        constexpr int kStep = NT / (W / 8);      // tokens from one of a thread's pieces to the next
+        if (vec) {
+            const int t0 = tid / (W / 8), c = tid % (W / 8) * 8;
+            const uint32_t off = (uint32_t(t0) * uint32_t(stride) + uint32_t(c)) * uint32_t(sizeof(E));
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const bool in = (kAll % NT == 0 || tid + i * NT < kAll) && t0 + i * kStep < rem && c < width;
+                const char* s = reinterpret_cast<const char*>(p + i * kStep * stride);
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) x[i][w] = in ? *reinterpret_cast<const Piece*>(s + off + 16 * w) : Piece(E(0.f));
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int at = tid + i * NT, token = at / (W / 8), c = at % (W / 8) * 8;
-            const bool in = (kAll % NT == 0 || at < kAll) && token < rem && c < width;
+            const bool in = (kAll % NT == 0 || at < kAll) && token < rem;
             const E* s = p + token * stride + c;
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                if (vec) {
-                    x[i][w] = in ? reinterpret_cast<const Piece*>(s)[w] : Piece(E(0.f));
-                } else {
+            for (int w = 0; w < kWords; ++w)
 #pragma unroll
-                    for (int j = 0; j < kPer; ++j) x[i][w][j] = in && c + w * kPer + j < width ? s[w * kPer + j] : E(0.f);
-                }
-            }
+                for (int j = 0; j < kPer; ++j) x[i][w][j] = in && c + w * kPer + j < width ? s[w * kPer + j] : E(0.f);
         }
     }
 
@@ -249,6 +261,13 @@ struct Rows {
     }
 };
 
+template <class T>
+__device__ __forceinline__ const T* same_in_all_lanes(const T* p) {
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(u)), hi = __builtin_amdgcn_readfirstlane(uint32_t(u >> 32));
+    return reinterpret_cast<const T*>(uint64_t(hi) << 32 | lo);
+}
+
 // A chunk's decays, in LDS.  cum is in units of log 2, for exp2.
 template <int C>
 struct Decays {
@@ -258,29 +277,38 @@ struct Decays {
 
 __device__ __forceinline__ float exp2_of(double x) { return __builtin_amdgcn_exp2f(float(x)); }
 
-// One wave: lane l has the log decays of tokens l and, with C = 128, 64 + l (none: zero).  Returns the chunk's whole log2 decay.
+template <int CTRL>
+__device__ __forceinline__ double moved64(double x) {      // by a DPP control, zero where there is no lane
+    typedef int Pair __attribute__((ext_vector_type(2)));
+    const Pair p = __builtin_bit_cast(Pair, x);
+    return __builtin_bit_cast(double, Pair{__builtin_amdgcn_update_dpp(0, p[0], CTRL, 0xf, 0xf, true), __builtin_amdgcn_update_dpp(0, p[1], CTRL, 0xf, 0xf, true)});
+}
+__device__ __forceinline__ double lane64(double x, int l) {
+    typedef int Pair __attribute__((ext_vector_type(2)));
+    const Pair p = __builtin_bit_cast(Pair, x);
+    return __builtin_bit_cast(double, Pair{__builtin_amdgcn_readlane(p[0], l), __builtin_amdgcn_readlane(p[1], l)});
+}
+
+// One wave: lane l has the log decay of token l (from C on, and where there is no token: zero).  Returns the chunk's
+// whole log2 decay.  The sums run within 16 lanes, then over their totals, in registers alone.
 template <int C>
-__device__ __forceinline__ double put_decays(Decays<C>& d, const float (&g)[C > 64 ? 2 : 1], int lane) {
-    constexpr int N = C > 64 ? 2 : 1, kLanes = C < 64 ? C : 64;
-    double x[N], last = 0.;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        x[n] = double(g[n] < -1e4f ? -1e4f : g[n]) * 1.4426950408889634;
-#pragma unroll
-        for (int i = 1; i < kLanes; i *= 2) {
-            const double y = __shfl_up(x[n], i, 64);
-            if (lane >= i) x[n] += y;
-        }
-        x[n] += last;
-        last = __shfl(x[n], kLanes - 1, 64);
-    }
-    if (lane < kLanes) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            d.cum[64 * n + lane] = x[n];
-            d.gamma[64 * n + lane] = exp2_of(x[n]);
-            d.eta[64 * n + lane] = exp2_of(last - x[n]);
-        }
+__device__ __forceinline__ double put_decays(Decays<C>& d, float g, int lane) {
+    double x = double(g < -1e4f ? -1e4f : g) * 1.4426950408889634;
+    x += moved64<0x111>(x);
+    x += moved64<0x112>(x);
+    x += moved64<0x114>(x);
+    x += moved64<0x118>(x);
+    const double a = lane64(x, 15), b = lane64(x, 31), c = lane64(x, 47);
+    double before = 0.;
+    if (lane >= 16) before = a;
+    if (lane >= 32) before += b;
+    if (lane >= 48) before += c;
+    x += before;
+    const double last = lane64(x, C - 1);
+    if (lane < C) {
+        d.cum[lane] = x;
+        d.gamma[lane] = exp2_of(x);
+        d.eta[lane] = exp2_of(last - x);
     }
     return last;
 }

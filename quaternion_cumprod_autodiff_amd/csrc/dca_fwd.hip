@@ -39,28 +39,55 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
     auto column = [&](int c) { return vw + (CT == 2 ? 8 * (m >> 2) + 4 * c + (m & 3) : m); };
     f32x4 S[KT][CT];
     {
+        // As S0 is saved, the other way round: rows of memory through LDS to columns of lanes.
+        constexpr int kStep = 36, kLanes = 4 * CT, kPasses = 32 * kLanes / 64;
+        static_assert(4 * 16 * CT * kStep * 4 <= sizeof(rows), "the columns' place");
         const bool own = seg > 0;
         const float* src = own ? a.seg + (seg_slot * a.Hv + h) * int64_t(KP) * a.VP : a.s0 ? a.s0 + (n * a.Hv + h) * int64_t(a.K) * a.V : nullptr;
-        const int rows = own ? KP : a.K, cols = own ? a.VP : a.V;
+        const int nk = own ? KP : a.K, nv = own ? a.VP : a.V, row = lane / kLanes, col = vw + lane % kLanes * 4;
+        const bool vec = own || (a.V % 4 == 0 && reinterpret_cast<uintptr_t>(a.s0) % 16 == 0);
+        float* t = reinterpret_cast<float*>(rows) + wave * (16 * CT * kStep);
+        f32x4 x[KB][kPasses];
 #pragma unroll
-        for (int r = 0; r < KT; ++r)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
+            for (int p = 0; p < kPasses; ++p) {
+                const int k = 32 * kb + p * (64 / kLanes) + row;
+                const float* at = src + int64_t(k) * nv + col;
+                x[kb][p] = zero4();
+                if (src && k < nk) {
+                    if (vec) {
+                        if (col < nv) x[kb][p] = *reinterpret_cast<const f32x4*>(at);
+                    } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = acc_index(r, g) + i, v = column(c);
-                    S[r][c][i] = src && k < rows && v < cols ? src[int64_t(k) * cols + v] : 0.f;
+                        for (int i = 0; i < 4; ++i)
+                            if (col + i < nv) x[kb][p][i] = at[i];
+                    }
                 }
+            }
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[(lane % kLanes * 4 + i) * kStep + p * (64 / kLanes) + row] = x[kb][p][i];
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int c = 0; c < CT; ++c) S[2 * kb + e][c] = *reinterpret_cast<const f32x4*>(t + (column(c) - vw) * kStep + 8 * g + 4 * e);
+            __builtin_amdgcn_wave_barrier();
+        }
     }
 
-    const E* q = static_cast<const E*>(a.q) + s.b * a.qs[0] + s.t0 * a.qs[1] + hk * a.qs[2];
-    const E* k = static_cast<const E*>(a.k) + s.b * a.ks[0] + s.t0 * a.ks[1] + hk * a.ks[2];
-    const E* v = static_cast<const E*>(a.v) + s.b * a.vs[0] + s.t0 * a.vs[1] + h * a.vs[2] + v0;
-    const float* gd = a.g + s.b * a.gs[0] + s.t0 * a.gs[1] + h * a.gs[2];
+    const E* q = same_in_all_lanes(static_cast<const E*>(a.q) + s.b * a.qs[0] + s.t0 * a.qs[1] + hk * a.qs[2]);
+    const E* k = same_in_all_lanes(static_cast<const E*>(a.k) + s.b * a.ks[0] + s.t0 * a.ks[1] + hk * a.ks[2]);
+    const E* v = same_in_all_lanes(static_cast<const E*>(a.v) + s.b * a.vs[0] + s.t0 * a.vs[1] + h * a.vs[2] + v0);
+    const float* gd = same_in_all_lanes(a.g + s.b * a.gs[0] + s.t0 * a.gs[1] + h * a.gs[2]);
     E* out = static_cast<E*>(a.out) + ((s.b * a.T + s.t0) * a.Hv + h) * int64_t(a.V);
     Rows<DT, C, KP> rq, rk;
     Rows<DT, C, VW> rv;
-    float rg[1] = {0.f};
+    float rg = 0.f;
     auto load = [&](int c) {
         const int64_t t = int64_t(c) * C;
         const int rem = int(s.len - t);
@@ -68,7 +95,7 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
         rq.load(q + t * a.qs[1], a.qs[1], rem, a.K, a.vec_qk, id);
         rk.load(k + t * a.ks[1], a.ks[1], rem, a.K, a.vec_qk, id);
         rv.load(v + t * a.vs[1], a.vs[1], rem, a.V - v0, a.vec_v, id);
-        rg[0] = lane < C && lane < rem ? gd[(t + lane) * a.gs[1]] : 0.f;
+        rg = lane < C && lane < rem ? gd[(t + lane) * a.gs[1]] : 0.f;
     };
     if (first < last) load(first);
     for (int chunk = first; chunk < last; ++chunk) {

@@ -22,7 +22,6 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
     constexpr int KW = KT / 4 > 0 ? KT / 4 : 1;                // a wave's tiles of K rows
     constexpr int TW = KT / 4 > 0 ? TT : TT / 2, TV = TT / 2;  // and of tokens, of dQ and dK, and of dV
     constexpr int kPairs = dca_tri(C), PW = (kPairs + NW - 1) / NW;
-    constexpr int kHalves = C > 64 ? 2 : 1;                    // of 64 tokens
     struct Sums {
         float reads[NW][C], writes[NW][C], pairs[NW][C], dot[NW], last;
     };
@@ -76,8 +75,8 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
     f32x4 sr[KW][2], dr[KW][2];
     auto load_rows = [&](int j, int v0) {
         const int h = hk * a.group + j, id = fresh<kTight>(tid);
-        rv.load(static_cast<const E*>(a.v) + s.b * a.vs[0] + t0 * a.vs[1] + h * a.vs[2] + v0, a.vs[1], rem, a.V - v0, a.vec_v, id);
-        ro.load(static_cast<const E*>(a.d_out) + ((s.b * a.T + t0) * a.Hv + h) * int64_t(a.V) + v0, int64_t(a.Hv) * a.V, rem, a.V - v0, a.vec_o, id);
+        rv.load(same_in_all_lanes(static_cast<const E*>(a.v) + s.b * a.vs[0] + t0 * a.vs[1] + h * a.vs[2] + v0), a.vs[1], rem, a.V - v0, a.vec_v, id);
+        ro.load(same_in_all_lanes(static_cast<const E*>(a.d_out) + ((s.b * a.T + t0) * a.Hv + h) * int64_t(a.V) + v0), int64_t(a.Hv) * a.V, rem, a.V - v0, a.vec_o, id);
     };
     auto load_states = [&](int j, int v0) {
         const int l = fresh<kTight>(lane);
@@ -92,61 +91,42 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
     };
     auto make_decays = [&](int j) {
         const int h = hk * a.group + j;
-        float x[kHalves];
-#pragma unroll
-        for (int i = 0; i < kHalves; ++i) {
-            const int t = 64 * i + lane;
-            x[i] = t < C && t < rem ? a.g[s.b * a.gs[0] + (t0 + t) * a.gs[1] + h * a.gs[2]] : 0.f;
-        }
-        put_decays<C>(decays[j & 1], x, lane);
+        put_decays<C>(decays[j & 1], lane < C && lane < rem ? a.g[s.b * a.gs[0] + (t0 + lane) * a.gs[1] + h * a.gs[2]] : 0.f, lane);
     };
     // dg of value head j from its sums: what a token and later ones read of S0, what earlier ones leave in S1, and the
-    // pairs across it; a lane has tokens 64 i + lane.
+    // pairs across it; a lane has a token.
     auto finish = [&](int j) {
-        const int h = hk * a.group + j;
-        constexpr int kLanes = C < 64 ? C : 64;
-        float d[kHalves], z[kHalves], pairs[kHalves], x = 0.f;
+        float d = 0.f, z = 0.f, pairs = 0.f, x = 0.f;
 #pragma unroll
         for (int c = 0; c < NW; ++c) x += sum.dot[c];
+        if (lane < C)
 #pragma unroll
-        for (int i = 0; i < kHalves; ++i) {
-            d[i] = z[i] = pairs[i] = 0.f;
-            if (lane < kLanes)
-#pragma unroll
-                for (int c = 0; c < NW; ++c) {
-                    d[i] += sum.reads[c][64 * i + lane];
-                    z[i] += sum.writes[c][64 * i + lane];
-                    pairs[i] += sum.pairs[c][64 * i + lane];
-                }
-#pragma unroll
-            for (int k = 1; k < kLanes; k *= 2) {
-                const float y = __shfl_down(d[i], k, 64), w = __shfl_up(z[i], k, 64);
-                d[i] += lane + k < kLanes ? y : 0.f;
-                z[i] += lane >= k ? w : 0.f;
+            for (int c = 0; c < NW; ++c) {
+                d += sum.reads[c][lane];
+                z += sum.writes[c][lane];
+                pairs += sum.pairs[c][lane];
             }
-        }
-        const float later = kHalves > 1 ? __shfl(d[kHalves - 1], 0, 64) : 0.f, sooner = __shfl(z[0], kLanes - 1, 64);
-        float all = 0.f;
 #pragma unroll
-        for (int i = 0; i < kHalves; ++i) {
-            const int t = 64 * i + lane;
-            const float y = __shfl_up(z[i], 1, 64);
-            const float dg = sum.last * x + (d[i] + (i + 1 < kHalves ? later : 0.f)) + ((lane ? y : 0.f) + (i ? sooner : 0.f)) + pairs[i];
-            if (t < C && t < rem) {
-                if (a.dg) a.dg[(s.b * a.T + t0 + t) * a.Hv + h] = dg;
-                all += dg;
-            }
+        for (int k = 1; k < C; k *= 2) {
+            const float y = __shfl_down(d, k, 64), w = __shfl_up(z, k, 64);
+            d += lane + k < C ? y : 0.f;
+            z += lane >= k ? w : 0.f;
         }
+        z = __shfl_up(z, 1, 64);
+        const bool in = lane < C && lane < rem;
+        const float dg = sum.last * x + d + (lane ? z : 0.f) + pairs;
+        const int h = hk * a.group + j;
+        if (a.dg && in) a.dg[(s.b * a.T + t0 + lane) * a.Hv + h] = dg;
         if (a.dg_part) {
-            all = lanes_sum<64>(all);
+            const float all = lanes_sum<64>(in ? dg : 0.f);
             if (lane == 0) a.dg_part[slot * a.Hv + h] = all;
         }
     };
 
     {
         Rows<DT, C, KP, NT> rq, rk;
-        rq.load(static_cast<const E*>(a.q) + s.b * a.qs[0] + t0 * a.qs[1] + hk * a.qs[2], a.qs[1], rem, a.K, a.vec_qk, tid);
-        rk.load(static_cast<const E*>(a.k) + s.b * a.ks[0] + t0 * a.ks[1] + hk * a.ks[2], a.ks[1], rem, a.K, a.vec_qk, tid);
+        rq.load(same_in_all_lanes(static_cast<const E*>(a.q) + s.b * a.qs[0] + t0 * a.qs[1] + hk * a.qs[2]), a.qs[1], rem, a.K, a.vec_qk, tid);
+        rk.load(same_in_all_lanes(static_cast<const E*>(a.k) + s.b * a.ks[0] + t0 * a.ks[1] + hk * a.ks[2]), a.ks[1], rem, a.K, a.vec_qk, tid);
         load_rows(0, 0);
         load_states(0, 0);
         if (wave == 0) make_decays(0);

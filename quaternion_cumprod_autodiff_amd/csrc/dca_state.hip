@@ -54,20 +54,20 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
 
     const int64_t* xs = REV ? a.qs : a.ks;
     const int64_t ys = REV ? int64_t(a.Hv) * a.V : a.vs[1];
-    const E* x = static_cast<const E*>(REV ? a.q : a.k) + s.b * xs[0] + s.t0 * xs[1] + hk * xs[2];
-    const E* y = REV ? static_cast<const E*>(a.d_out) + ((s.b * a.T + s.t0) * a.Hv + h) * int64_t(a.V) + v0
-                     : static_cast<const E*>(a.v) + s.b * a.vs[0] + s.t0 * a.vs[1] + h * a.vs[2] + v0;
-    const float* gd = a.g + s.b * a.gs[0] + s.t0 * a.gs[1] + h * a.gs[2];
+    const E* x = same_in_all_lanes(static_cast<const E*>(REV ? a.q : a.k) + s.b * xs[0] + s.t0 * xs[1] + hk * xs[2]);
+    const E* y = same_in_all_lanes(REV ? static_cast<const E*>(a.d_out) + ((s.b * a.T + s.t0) * a.Hv + h) * int64_t(a.V) + v0
+                                       : static_cast<const E*>(a.v) + s.b * a.vs[0] + s.t0 * a.vs[1] + h * a.vs[2] + v0);
+    const float* gd = same_in_all_lanes(a.g + s.b * a.gs[0] + s.t0 * a.gs[1] + h * a.gs[2]);
     Rows<DT, C, KP> rx;
     Rows<DT, C, VW> ry;
-    float rg[1] = {0.f};
+    float rg = 0.f;
     auto load = [&](int c) {
         const int64_t t = int64_t(c) * C;
         const int rem = int(s.len - t);
         const int id = fresh<kTight>(tid);
         rx.load(x + t * xs[1], xs[1], rem, a.K, a.vec_qk, id);
         ry.load(y + t * ys, ys, rem, a.V - v0, REV ? a.vec_o : a.vec_v, id);
-        rg[0] = lane < C && lane < rem ? gd[(t + lane) * a.gs[1]] : 0.f;
+        rg = lane < C && lane < rem ? gd[(t + lane) * a.gs[1]] : 0.f;
     };
     double decay = 0.;
     if (first < last) load(REV ? last - 1 : first);
