@@ -301,9 +301,8 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
             __builtin_amdgcn_sched_barrier(0);
         }
         __syncthreads();                                      // P is done with
-        float across[TT];                                     // of token 16 t + m: its pairs' M, by rows 4 g + ..
-#pragma unroll
-        for (int t = 0; t < TT; ++t) across[t] = 0.f;
+        if (want_dg && lane < C) sum.pairs[wave][lane] = 0.f;
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int p = 0; p < PW; ++p) {
             int i, b;
@@ -316,23 +315,39 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
 #pragma unroll
             for (int q = 0; q < PP; ++q) lp[tri_of(i, b)][q][l] = f[q];
             if (want_dg) {
-                // M_ij of this pair; its sum over j < t <= i, for each t: over j with a matrix of ones.
+                // M_ij of this pair, i > j, and its sums over j < t <= i, for each t.
                 f32x4 qk[2] = {zero4(), zero4()};
                 products(lq, lk, i, b, l, qk, std::integral_constant<int, KP>{});
-                bf16x8 mf[kParts];
+                const int row = 16 * i + m, col = 32 * b + 8 * g;
+                float all = 0.f;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) x[c] *= 32 * b + 8 * g + c < 16 * i + m ? qk[c >> 2][c & 3] : 0.f;
-                split<kParts, 8>(x, mf);
+                for (int c = 0; c < 8; ++c) all += x[c] *= col + c < row ? qk[c >> 2][c & 3] : 0.f;
+                // t in the block's 32 tokens, col + c here: what is left of it in its row, then over the rows from it on.
+                float left = all, y = __shfl_up(left, 16, 64);
+                left += g >= 1 ? y : 0.f;
+                y = __shfl_up(left, 32, 64);
+                left += g >= 2 ? y : 0.f;
+                left = __shfl_up(left, 16, 64);
+                left = g >= 1 ? left : 0.f;
+                float* to = sum.pairs[wave] + col;
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    if (t < 2 * b || t > i) continue;
-                    bf16x8 one[1];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) one[0][c] = __bf16(32 * b + 8 * g + c < 16 * t + m ? 1.f : 0.f);
-                    f32x4 before = zero4();
-                    mma(before, mf, one);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) across[t] += 16 * i + 4 * g + c >= 16 * t + m ? before[c] : 0.f;
+                for (int c = 0; c < 8; ++c) {
+                    const float z = lanes_sum<16>(row >= col + c ? left : 0.f);
+                    if (m == c) to[c] += z;
+                    left += x[c];
+                }
+                // t behind them, in the rows' tile or (two blocks of 32) between: whole rows.
+                if (2 * b + 2 <= i) {
+                    const float total = rows_of_lanes_sum(all);
+                    float from = total + moved<0x101>(total);
+                    from += moved<0x102>(from);
+                    from += moved<0x104>(from);
+                    from += moved<0x108>(from);
+                    if (g == 0) sum.pairs[wave][16 * i + m] += from;
+                    if (i == 2 * b + 3) {
+                        const float z = lanes_sum<16>(total);
+                        if (g == 0) sum.pairs[wave][16 * i - 16 + m] += z;
+                    }
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -340,8 +355,6 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
         if (want_dg) {
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
-                const float p = rows_of_lanes_sum(across[t]);
-                if (g == 0) sum.pairs[wave][16 * t + m] = p;
                 if (TW < TT && (t < tt0 || t >= tt0 + TW) && g == 0) sum.reads[wave][16 * t + m] = sum.writes[wave][16 * t + m] = 0.f;
             }
 #pragma unroll
