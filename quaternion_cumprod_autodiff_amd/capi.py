@@ -1074,7 +1074,7 @@ def qkn_bwd(query, key, query_weight, key_weight, cos, sin, positions, d_query_o
 # What a call from Python costs is most of a decoding step's: the current
 # stream's handle without a Stream object (0.1 us, and 1.9 with one), outputs
 # made like an input where it is dense (1.2 us, and 2.3 from a shape).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _lm_like(t, shape):

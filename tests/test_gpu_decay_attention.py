@@ -206,6 +206,27 @@ def test_scale_strides_shared_and_absent_inputs():
     assert np.abs(f64(got) - want).max() <= 3 * 2.0 ** -8 * top + 1e-5 * top
 
 
+def test_rows_far_apart():
+    """Tokens and heads 16 MiB apart: offsets pass 32 bits, within a chunk too."""
+    args, cot = inputs(1, 70, 2, 2, 32, 40, BF16, seed=23)
+    room = torch.zeros(150 * 2 ** 23, device=DEV, dtype=BF16)
+    far = []
+    for i, t in enumerate(args[:3]):
+        view = room[i * 2 ** 10:].as_strided(t.shape, (0, 2 ** 24, 2 ** 23, 1))
+        view.copy_(t)
+        far.append(view)
+    want = decay_attention(*args)
+    got = decay_attention(*far, *args[3:])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    leaves, there = [t.clone().requires_grad_() for t in args], [t.detach().requires_grad_() for t in far + args[3:]]
+    a = torch.autograd.grad(decay_attention(*leaves), leaves, cot)
+    b = torch.autograd.grad(decay_attention(*there), there, cot)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    step = [t[:, :1] for t in far] + [args[3][:, :1].contiguous()]
+    near = [t[:, :1].contiguous() for t in args[:4]]
+    assert torch.equal(decay_attention_step(*step, args[4].clone()), decay_attention_step(*near, args[4].clone()))
+
+
 @pytest.mark.parametrize("head", [False, True])
 def test_gradients_of_some_inputs_and_of_one_output(head):
     args, cot = inputs(1, 100, 1, 2, 48, 40, F32, seed=16, head=head)
@@ -282,6 +303,11 @@ def test_with_nothing_to_do(head):
         leaf = args[3].clone().requires_grad_()
         out = decay_attention(*empty[:3], leaf, empty[4])
         assert not torch.autograd.grad(out, [leaf], [t.detach() for t in out])[0].any()
+    long, _ = inputs(1, 300, 1, 2, 16, 8, BF16, seed=24, head=head)          # no sequence among many rows
+    leaves = [t.clone().requires_grad_() for t in long[:4]] + [long[4][:0].clone().requires_grad_()]
+    out, state = decay_attention(*leaves, offsets=torch.zeros(1, dtype=torch.int32, device=DEV))
+    grads = torch.autograd.grad([out, state], leaves, [torch.ones_like(out), torch.ones_like(state)])
+    assert not out.any() and state.shape == (0, 2, 16, 8) and not any(g.any() for g in grads)
     none = torch.zeros(1, dtype=torch.int32, device=DEV)
     out, state = decay_attention(*[t[:1] for t in args[:3]], args[3] if head else args[3][:1], args[4][:0], offsets=none)
     assert not out.any() and state.shape == (0, 2, 16, 8)
@@ -581,6 +607,19 @@ def test_a_decoding_step_captured_and_replayed():
         torch.cuda.synchronize()
         assert torch.equal(got, w)
     assert torch.equal(args[4], end)
+
+
+def test_a_result_does_not_depend_on_the_sequences_beside_it():
+    """As long as the segments are the same, a sequence of a batch has the bits that it has alone."""
+    args, cot = inputs(9, 90, 2, 4, 64, 48, BF16, seed=25)
+    leaves = [t.clone().requires_grad_() for t in args]
+    whole = decay_attention(*leaves)
+    grads = torch.autograd.grad(whole, leaves, cot)
+    for n in (0, 4, 8):
+        one = [t[n:n + 1].clone().requires_grad_() for t in args]
+        part = decay_attention(*one)
+        for a, b in zip((*whole, *grads), (*part, *torch.autograd.grad(part, one, [c[n:n + 1] for c in cot]))):
+            assert torch.equal(a[n:n + 1], b)
 
 
 def test_a_scale_in_a_tensor_is_read_at_each_call():

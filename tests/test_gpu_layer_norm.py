@@ -137,6 +137,27 @@ def test_rows_far_from_zero_constant_and_of_all_sizes():
     assert torch.equal(y, torch.arange(64.0, device=DEV).expand(3, 64))        # no variance: the bias alone
 
 
+@pytest.mark.parametrize("D", [24, 128, 500, 1032, 4096, 9000])
+def test_a_row_does_not_depend_on_the_rows_beside_it(D):
+    """One row, a few, and so many that they come several to a group: the same bits, gradients of x among them."""
+    x, w, b, dy = inputs((40000 if D < 512 else 3000, D), "both", BF16, D)
+
+    def run(n):
+        leaf = x[:n].clone().requires_grad_()
+        y = layer_norm(leaf, w, b)
+        return y.detach(), torch.autograd.grad(y, [leaf], dy[:n])[0]
+
+    every = run(len(x))
+    for n in (1, 7, 300):
+        assert all(torch.equal(a[:n], c) for a, c in zip(every, run(n)))
+
+
+def test_heads_that_fill_no_block():
+    for H, D in ((3, 16), (5, 128), (17, 64), (33, 8), (2, 600), (70, 24)):
+        check(*inputs((3, 11, H, D), "both", F32, H, heads=True))
+        check(*inputs((2, 400, H, D), "both", BF16, H, heads=True))
+
+
 def test_not_finite_rows_stay_their_own():
     x, w, b, dy = inputs((70, 96), "both", BF16, 9)
     want = layer_norm(x, w, b)
