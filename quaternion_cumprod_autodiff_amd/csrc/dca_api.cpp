@@ -15,8 +15,13 @@ struct DcaPlan {
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// Blocks that a pass over a sequence wants: two to each of 256 CUs.
+// Blocks that a pass over a sequence wants: two to each of 256 CUs (prompt of 8192 tokens of 32 heads of 128: 155 us with
+// 512, 193 with 256, 180 with 1024, whose states pass through memory for more than they gain).
 constexpr int64_t kBlocks = 512;
+// The backward states' pass does without segments from these blocks of 64 columns on: it is bound by the states that it
+// stores, and a block to each CU stores as fast (4 x 4096 tokens of 32 heads of 128: 179 us, and 283 with segments of
+// 128 columns, their sums and joins among them; the forward pass 398, and 332).
+constexpr int64_t kNarrow = 256;
 // Tokens to a segment, at least: shorter ones cost more in states through memory than they gain.
 constexpr int64_t kLeast = 128;
 
@@ -190,11 +195,18 @@ int dca_bwd(const dca_dims* dims, const void* query, const void* key, const void
     a.dq = d_query; a.dk = d_key; a.dv = d_value; a.dg = heads ? nullptr : d_log_decay; a.ds0 = d_initial_state;
     hipError_t err = hipSuccess;
     if (d.N) {
-        if (p.segs > 1) {
-            err = qc::launch_dca_state(d.dtype, p.kb, p.ct, true, true, a, st);
+        int ct = p.ct;
+        if (p.segs > 1 && !d.packed && d.N * d.Hv * (p.vp / 64) >= qc::kNarrow) {
+            ct = 1;
+            a.tiles = int(p.vp / 64);
+            a.segs = 1;
+            a.seg_slots = d.N;
+            a.seg_tokens = a.blocks * p.block;
+        } else if (p.segs > 1) {
+            err = qc::launch_dca_state(d.dtype, p.kb, ct, true, true, a, st);
             if (err == hipSuccess) err = qc::launch_dca_join(p.kb, true, a, st);
         }
-        if (err == hipSuccess) err = qc::launch_dca_state(d.dtype, p.kb, p.ct, true, false, a, st);
+        if (err == hipSuccess) err = qc::launch_dca_state(d.dtype, p.kb, ct, true, false, a, st);
         if (err == hipSuccess && (d_query || d_key || d_value || d_log_decay)) err = qc::launch_dca_grad(d.dtype, p.kb, a, st);
     }
     // (Without tokens there are no sums, and a head's decay has a gradient of zero.)

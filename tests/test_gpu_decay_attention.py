@@ -94,10 +94,12 @@ def test_sequences_in_segments(size, head, dtype):
     check(*inputs(*size, dtype, seed=size[1], head=head))
 
 
-@pytest.mark.parametrize("size", [(5, 300, 16, 32, 32, 40), (2, 513, 8, 128, 64, 128)], ids=str)
-def test_many_heads_and_sequences(size):
-    print(f"[many {size}]", flush=True)
-    check(*inputs(*size, BF16, seed=size[1]))
+@pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=str)
+@pytest.mark.parametrize("size", [(5, 300, 16, 32, 32, 40), (2, 333, 8, 128, 64, 128), (4, 450, 4, 24, 100, 130), (9, 290, 30, 30, 24, 50)], ids=str)
+def test_many_heads_and_sequences(size, dtype):
+    """Enough of them that the forward pass or the backward states' pass goes without segments, or both do."""
+    print(f"[many {size} {dtype}]", flush=True)
+    check(*inputs(*size, dtype, seed=size[1]))
 
 
 PACKED = [([5, 0, 1, 64, 65, 0, 130], 0), ([1], 3), ([0, 0], 5), ([63, 1, 1, 63, 128], 70), ([1] * 9, 0), ([200, 7], 1), ([900, 0, 3, 640, 257], 30)]
