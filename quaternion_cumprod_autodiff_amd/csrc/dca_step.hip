@@ -7,7 +7,9 @@
 // owns 32 columns of one state, in registers: lane l holds rows (l / 8) NR .. of
 // columns 4 (l % 8) .. + 3 (NR = K / 8 rounded up to 4, 8 or 16), so a row's
 // piece is one 128-byte line, all of a state's loads are in flight at once, and
-// the reduction stays inside the wave.
+// the reduction stays inside the wave.  810 MB of states (read and written): 152
+// us, 5.3 TB/s, a copy's rate; one row of 32 heads of 128 x 128: 6.7 us, the loads,
+// the reduction and the stores in a row.
 #include "dca_internal.hpp"
 
 #include <type_traits>
@@ -160,7 +162,8 @@ const void* step_kernel(int nr, bool vec, bool many, bool stream) {
 }
 
 // From how many bytes of states on a call streams them: a model calls for one layer after another, so that a layer's
-// states are gone from the 256 MB cache when its turn comes again.
+// states are gone from the 256 MB cache when its turn comes again.  (The rule of gdr_step, whose states move alike and
+// where both sides were measured: three pools of 134 MB in turn 60.7 us, streamed 53.6; one of 100 MB alone 37, and 42.)
 constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
 }  // namespace

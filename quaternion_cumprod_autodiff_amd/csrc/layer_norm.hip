@@ -10,7 +10,13 @@
 // Bound by memory: every element is read once (twice as x and g in the VJP) and
 // written once, so TR threads hold a row in registers between the sums and the
 // result, S runs of W consecutive elements each: W = 8 where rows lie on 16
-// bytes, else 1.  Rows of up to 512 elements (W = 8) share a wave with others.
+// bytes, else 1.  Rows of up to 512 elements (W = 8) share a wave with others,
+// next to each other in memory: heads of a token, or rows.  What is under way
+// counts, so rows stay as they lie, in half the registers of floats, and sums
+// are made without LDS.  16384 rows of 4096 in bfloat16: 58 us, 4.6 TB/s (as
+// floats, by four waves to a row, 71); 4 x 4096 tokens of 32 heads of 128 with
+// weights of each head: forward 50 us, 5.5 TB/s (one row at a time, heads apart,
+// 64), VJP 81 us, 5.0 TB/s (92), and 4 us for the weights' sums.
 #include "layer_norm.h"
 #include "lm_common.hpp"
 #include "qc_internal.hpp"
