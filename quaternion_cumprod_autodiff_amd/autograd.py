@@ -471,7 +471,7 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
     x, eps = _last_dense(x), float(eps)
     shape = x.shape
     if x.dim() > 4:
-        x = x.reshape(-1, *shape[-3:])
+        x = x.reshape(shape[:-3].numel(), *shape[-3:])
     if _grads_wanted(x, weight, bias):
         y = LayerNormFunction.apply(x, weight, bias, eps)
     else:

@@ -180,6 +180,15 @@ def test_no_rows():
         assert y.shape == shape and all(g.shape == t.shape and not g.any() for g, t in zip(grads, leaves))
 
 
+@pytest.mark.parametrize("shape", [(2, 3, 0, 4, 8), (0, 2, 3, 4, 8), (2, 2, 3, 4, 0, 8)], ids=str)
+def test_no_rows_of_many_axes(shape):
+    x, w, b, dy = inputs(shape, "both", F32, 1)
+    leaves = [t.requires_grad_() for t in (x, w, b)]
+    y = layer_norm(*leaves)
+    grads = torch.autograd.grad(y, leaves, dy)
+    assert y.shape == shape and all(g.shape == t.shape and not g.any() for g, t in zip(grads, leaves))
+
+
 def test_some_gradients_alone():
     x, w, b, dy = inputs((40, 200), "both", F32, 10)
     leaves = [t.clone().requires_grad_() for t in (x, w, b)]

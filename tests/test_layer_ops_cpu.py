@@ -286,6 +286,12 @@ def test_python_refuses_host_tensors_and_gradients():
         autograd.layer_norm(torch.zeros(()))
 
 
+@pytest.mark.parametrize("shape", [(2, 3, 0, 4, 5), (0, 2, 3, 4, 5), (2, 2, 3, 4, 0, 5)], ids=str)
+def test_empty_rows_of_many_axes_reach_the_checks(shape):
+    with pytest.raises(ValueError, match="GPU"):
+        autograd.layer_norm(cpu(*shape))
+
+
 @pytest.mark.parametrize("tracked", [False, True])
 def test_forward_mode_is_refused_and_not_dropped(tracked):
     q, v, g, s = cpu(1, 2, 1, 4), cpu(1, 2, 1, 4), cpu(1, 2, 1), cpu(1, 1, 4, 4)
