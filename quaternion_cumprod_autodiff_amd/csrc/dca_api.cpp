@@ -7,9 +7,9 @@ namespace {
 
 struct DcaPlan {
     int rc;
-    int kb, ct, block;
+    int kb, ct, chunk;
     int64_t slots, seg_slots, segs, seg_tokens, tokens, vp;
-    int64_t states, seg, decays, part;         // bytes of S0 (or dS1) of every block, and of the workspace's parts
+    int64_t states, seg, decays, part;         // bytes of S0 (or dS1) of every chunk, and of the workspace's parts
     int64_t q_bytes, out, gates, fin;
 };
 
@@ -39,19 +39,19 @@ DcaPlan dca_plan(const dca_dims* dims) {
     if (blocks < 0 || blocks >= (int64_t(1) << 23)) return p;
     p.kb = d.K <= 32 ? 1 : d.K <= 64 ? 2 : 4;
     p.ct = d.V <= 64 ? 1 : 2;
-    p.block = dca_block(d.dtype, p.kb);
+    p.chunk = dca_chunk(d.dtype);
     p.vp = (d.V + 64 * p.ct - 1) / (64 * p.ct) * (64 * p.ct);
-    const int64_t per = (d.T + p.block - 1) / p.block;
-    p.slots = !d.T || !d.N ? 0 : d.packed ? d.T / p.block + d.N : d.N * per;
+    const int64_t per = (d.T + p.chunk - 1) / p.chunk;
+    p.slots = !d.T || !d.N ? 0 : d.packed ? d.T / p.chunk + d.N : d.N * per;
     // Segments: as many as fill the card where sequences, heads and columns do not.
     const int64_t wide = d.Hv * (p.vp / (64 * p.ct));
     int64_t len = per > 0 ? per : 1;
     if (d.N && d.N * wide < kBlocks) {
         const int64_t share = (d.packed ? per : d.N * per) * wide / kBlocks + 1;
-        len = share * p.block > kLeast ? share : kLeast / p.block;
+        len = share * p.chunk > kLeast ? share : kLeast / p.chunk;
         if (len > per) len = per > 0 ? per : 1;
     }
-    p.seg_tokens = len * p.block;
+    p.seg_tokens = len * p.chunk;
     p.segs = per > len ? (per + len - 1) / len : 1;
     p.seg_slots = d.packed ? d.T / p.seg_tokens + d.N : d.N * p.segs;
     p.tokens = d.B * d.T;
@@ -80,7 +80,7 @@ DcaArgs arguments(const dca_dims& d, const DcaPlan& p, const void* q, const void
     a.gs[0] = d.head_decay ? 0 : d.T * d.Hv;
     a.gs[1] = d.head_decay ? 0 : d.Hv;
     a.gs[2] = 1;
-    a.T = d.T; a.N = d.N; a.blocks = (d.T + p.block - 1) / p.block; a.segs = p.segs;
+    a.T = d.T; a.N = d.N; a.chunks = (d.T + p.chunk - 1) / p.chunk; a.segs = p.segs;
     a.slots = p.slots; a.seg_slots = p.seg_slots; a.seg_tokens = p.seg_tokens;
     a.Hk = int(d.Hk); a.Hv = int(d.Hv); a.group = int(d.Hv / d.Hk); a.K = int(d.K); a.V = int(d.V); a.VP = int(p.vp);
     a.tiles = int(p.vp / (64 * p.ct));
@@ -201,7 +201,7 @@ int dca_bwd(const dca_dims* dims, const void* query, const void* key, const void
             a.tiles = int(p.vp / 64);
             a.segs = 1;
             a.seg_slots = d.N;
-            a.seg_tokens = a.blocks * p.block;
+            a.seg_tokens = a.chunks * p.chunk;
         } else if (p.segs > 1) {
             err = qc::launch_dca_state(d.dtype, p.kb, ct, true, true, a, st);
             if (err == hipSuccess) err = qc::launch_dca_join(p.kb, true, a, st);

@@ -51,8 +51,6 @@
 namespace qc {
 
 constexpr int dca_chunk(int dt) { return dt == 1 ? 64 : 32; }
-// Tokens to a block of dca_grad, with the states at whose ends the other passes leave to it: whole chunks.
-constexpr int dca_block(int dt, int) { return dca_chunk(dt); }
 constexpr int dca_parts(int dt) { return dt == 0 ? 3 : 2; }        // of operands computed on the way to an output
 
 struct DcaArgs {
@@ -61,17 +59,17 @@ struct DcaArgs {
     const int32_t* offsets;
     void* out;
     float* fin;
-    float* save;                        // S0 of every block of dca_block tokens: [slots][Hv][KP][VP] (or null)
+    float* save;                        // S0 of every chunk: [slots][Hv][KP][VP] (or null)
     float* seg;                         // workspace: states at segments' starts (backward: dS at their ends), as save
     float* seg_decay;                   // workspace: [segment slots][Hv]
     const void* d_out;
     const float* d_fin;
     void *dq, *dk, *dv;
     float *dg, *ds0;
-    float* ds;                          // workspace: dS1 of every block
-    float* dg_part;                     // workspace: sums of dg over blocks [slots][Hv], for decays of the head alone
+    float* ds;                          // workspace: dS1 of every chunk
+    float* dg_part;                     // workspace: sums of dg over chunks [slots][Hv], for decays of the head alone
     int64_t qs[3], ks[3], vs[3], gs[3]; // gs: of log_decay, zeros for batch and token where it is of the head alone
-    int64_t T, N, blocks, segs;         // blocks, segs: per sequence, without offsets
+    int64_t T, N, chunks, segs;         // chunks, segs: per sequence, without offsets
     int64_t slots, seg_slots, seg_tokens;
     int Hk, Hv, group, K, V, VP, tiles; // tiles: blocks of 64 CT columns of V
     int vec_qk, vec_v, vec_o;           // rows on 16 bytes and sizes multiples of 8
@@ -98,19 +96,18 @@ hipError_t by_dca_shape(int dt, int kb, int ct, F&& f) {
 // Device helpers ----------------------------------------------------------------
 
 struct Span {
-    int64_t b, t0, slot, seg;          // first token, first block's slot, first segment's slot
+    int64_t b, t0, slot, seg;          // first token, first chunk's slot, first segment's slot
     int len;
 };
 
-// BL: tokens to a block.
-template <int BL>
+template <int C>
 __device__ __forceinline__ Span span_of(const DcaArgs& a, int64_t n) {
-    if (!a.offsets) return {n, 0, n * a.blocks, n * a.segs, int(a.T)};
+    if (!a.offsets) return {n, 0, n * a.chunks, n * a.segs, int(a.T)};
     int64_t lo = a.offsets[n], hi = a.offsets[n + 1];
     lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
     hi = hi < lo ? lo : hi > a.T ? a.T : hi;
     // Consecutive sequences' slots cannot meet: floor((lo + len) / s) + 1 >= floor(lo / s) + max(1, ceil(len / s)).
-    return {0, lo, lo / BL + n, lo / a.seg_tokens + n, int(hi - lo)};
+    return {0, lo, lo / C + n, lo / a.seg_tokens + n, int(hi - lo)};
 }
 
 __device__ __forceinline__ int segments_of(const DcaArgs& a, const Span& s) {
@@ -118,14 +115,14 @@ __device__ __forceinline__ int segments_of(const DcaArgs& a, const Span& s) {
     return n > 1 ? n : 1;
 }
 
-// The last sequence whose first slot (of blocks, or of segments) is at or before this one.
-template <int BL, bool SEG>
+// The last sequence whose first slot (of chunks, or of segments) is at or before this one.
+template <int C, bool SEG>
 __device__ __forceinline__ int64_t owner(const DcaArgs& a, int64_t slot) {
-    if (!a.offsets) return slot / (SEG ? a.segs : a.blocks);
+    if (!a.offsets) return slot / (SEG ? a.segs : a.chunks);
     int64_t lo = 0, hi = a.N - 1;
     while (lo < hi) {
         const int64_t mid = (lo + hi + 1) / 2;
-        const Span s = span_of<BL>(a, mid);
+        const Span s = span_of<C>(a, mid);
         if ((SEG ? s.seg : s.slot) <= slot) lo = mid;
         else hi = mid - 1;
     }

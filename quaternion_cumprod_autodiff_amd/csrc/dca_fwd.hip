@@ -20,7 +20,7 @@ namespace {
 template <int DT, int KB, int CT, bool SAVE>
 __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
     using E = typename Storage<DT>::type;
-    constexpr int C = dca_chunk(DT), BL = dca_block(DT, KB), NP = parts_of(DT), PP = dca_parts(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 64 * CT, KT = 2 * KB;
+    constexpr int C = dca_chunk(DT), NP = parts_of(DT), PP = dca_parts(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 64 * CT, KT = 2 * KB;
     // Rows of Q, K and V; between chunks, a wave's columns of S on their way to memory.
     __shared__ __align__(16) char rows[NP * C * (2 * KP + VW) * 2];
     char *lq = rows, *lk = lq + NP * C * KP * 2, *lv = lk + NP * C * KP * 2;
@@ -31,8 +31,8 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
     int64_t u;
     int part;
     if (!dca_unit(a.seg_slots * a.Hk, a.group * a.tiles, u, part)) return;
-    const int64_t seg_slot = u / a.Hk, n = owner<BL, true>(a, seg_slot);
-    const Span s = span_of<BL>(a, n);
+    const int64_t seg_slot = u / a.Hk, n = owner<C, true>(a, seg_slot);
+    const Span s = span_of<C>(a, n);
     const int hk = int(u % a.Hk), h = hk * a.group + part / a.tiles, v0 = part % a.tiles * VW;
     const int64_t seg = seg_slot - s.seg;
     const int segs = segments_of(a, s);
@@ -107,14 +107,14 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
     for (int chunk = first; chunk < last; ++chunk) {
         const int rem = s.len - chunk * C;
         __syncthreads();
-        if (SAVE && chunk % (BL / C) == 0) {
+        if constexpr (SAVE) {
             // S0, 32 rows at a time: lanes hold a column's, memory wants a row's.  (Stored as they are, four bytes a lane,
             // 4 x 4096 tokens of 32 heads of 128 took 563 us instead of 240.)
             constexpr int kStep = 36, kLanes = 4 * CT;
             static_assert(4 * 16 * CT * kStep * 4 <= sizeof(rows), "the columns' place");
             const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
             float* t = reinterpret_cast<float*>(rows) + wave * (16 * CT * kStep);
-            float* dst = a.save + ((s.slot + chunk / (BL / C)) * a.Hv + h) * int64_t(KP) * a.VP + int64_t(l / kLanes) * a.VP + vw + l % kLanes * 4;
+            float* dst = a.save + ((s.slot + chunk) * a.Hv + h) * int64_t(KP) * a.VP + int64_t(l / kLanes) * a.VP + vw + l % kLanes * 4;
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll

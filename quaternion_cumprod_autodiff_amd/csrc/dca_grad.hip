@@ -1,18 +1,18 @@
-// dca_grad.hip -- gradients of linear attention with decays, block by block of tokens
+// dca_grad.hip -- gradients of linear attention with decays, chunk by chunk
 // (include/decay_attention.h; formulas and layouts in dca_chunk.hpp).
 #include "dca_chunk.hpp"
 
 namespace qc {
 namespace {
 
-// One block of C = dca_block tokens and one key head to a thread block, its value
-// heads one after the other, so that a shared head's gradients are summed in
-// registers in one order, and 32 columns of V at a time.  P and Phi: pairs of a
-// 16-token tile of rows and a 32-token block of columns, each wave every fourth.
-// dQ^T and dK^T [KP, tokens]: a wave has a quarter of the rows (of 32 in all:
-// half, and half of the tokens).  dV^T [32, tokens]: 16 columns of V and half of
-// the tokens.  S0 and dS1 come from memory as rows, the next 32 columns' while
-// these are worked on; dV takes dS1's columns from LDS.
+// One chunk and one key head to a block, its value heads one after the other, so
+// that a shared head's gradients are summed in registers in one order, and 32
+// columns of V at a time.  P and Phi: pairs of a 16-token tile of rows and a
+// 32-token block of columns, each wave every fourth.  dQ^T and dK^T [KP, tokens]:
+// a wave has a quarter of the rows (of 32 in all: half, and half of the tokens).
+// dV^T [32, tokens]: 16 columns of V and half of the tokens.  S0 and dS1 come from
+// memory as rows, the next 32 columns' while these are worked on; dV takes dS1's
+// columns from LDS.
 //
 // 4 x 4096 tokens of 32 heads of 128, bfloat16: 570 us, 1.75 GB of inputs, states
 // and gradients (340 us at the rate of a copy), 41% of the time in vector
@@ -25,7 +25,7 @@ namespace {
 template <int DT, int KB>
 __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kernel(DcaArgs a) {
     using E = typename Storage<DT>::type;
-    constexpr int C = dca_block(DT, KB), NP = parts_of(DT), PP = dca_parts(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 32, KT = 2 * KB;
+    constexpr int C = dca_chunk(DT), NP = parts_of(DT), PP = dca_parts(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 32, KT = 2 * KB;
     constexpr int NW = 4, NT = 64 * NW;
     constexpr bool kTight = DT == 1 ? KB > 1 : DT == 2 && KB == 4;
     constexpr int KW = KT / 4 > 0 ? KT / 4 : 1;                // a wave's tiles of K rows
@@ -43,14 +43,14 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
     const int hk = int(blockIdx.x % a.Hk);
     const int64_t n = owner<C, false>(a, slot);
     const Span s = span_of<C>(a, n);
-    const int64_t block = slot - s.slot;
-    if (block < 0 || block * C >= s.len) {
+    const int64_t chunk = slot - s.slot;
+    if (chunk < 0 || chunk * C >= s.len) {
         if (a.dg_part)
             for (int j = tid; j < a.group; j += NT) a.dg_part[slot * a.Hv + hk * a.group + j] = 0.f;
         return;
     }
-    const int rem = int(s.len - block * C);
-    const int64_t t0 = s.t0 + block * C, size = int64_t(KP) * a.VP;
+    const int rem = int(s.len - chunk * C);
+    const int64_t t0 = s.t0 + chunk * C, size = int64_t(KP) * a.VP;
     const bool want_dg = a.dg || a.dg_part;
     const int vtiles = a.VP / VW;
 

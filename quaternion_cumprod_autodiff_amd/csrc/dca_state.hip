@@ -8,8 +8,8 @@ namespace {
 // X = gamma_last X + A^T (w B) over a segment's chunks: forward S with A, B, w =
 // K, V, eta; REV, from the last chunk to the first, dS with Q, dO, scale gamma.
 // SUM: from zero, what a segment adds, stored at the segment that takes it.
-// Otherwise from the segment's state, which it leaves before each chunk (REV
-// alone: dS1 of every block of dca_grad), and at the end of the sequence as the gradient of s0.  A block
+// Otherwise (REV alone) from the segment's state, which it leaves before each
+// chunk as dS1, and at the end of the sequence as the gradient of s0.  A block
 // has 64 CT columns of V, a wave 16 CT of them, held as [columns of V, KP] so
 // that a lane's accumulators are consecutive in memory, [KP][VP].  Bound, where it
 // stores, by memory: 4 x 4096 tokens of 32 heads of 128, bfloat16, 740 MB in 185 us,
@@ -18,7 +18,7 @@ namespace {
 template <int DT, int KB, int CT, bool REV, bool SUM>
 __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
     using E = typename Storage<DT>::type;
-    constexpr int C = dca_chunk(DT), BL = dca_block(DT, KB), NP = parts_of(DT), JB = C / 32, KP = 32 * KB, VW = 64 * CT, KT = 2 * KB;
+    constexpr int C = dca_chunk(DT), NP = parts_of(DT), JB = C / 32, KP = 32 * KB, VW = 64 * CT, KT = 2 * KB;
     __shared__ __align__(16) char lx[NP * C * KP * 2], ly[NP * C * VW * 2];
     __shared__ __align__(16) Decays<C> dec;
     constexpr bool kTight = DT == 1 && KB == 4 && CT == 2 && !SUM;
@@ -26,8 +26,8 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
     int64_t u;
     int part;
     if (!dca_unit(a.seg_slots * a.Hk, a.group * a.tiles, u, part)) return;
-    const int64_t seg_slot = u / a.Hk, n = owner<BL, true>(a, seg_slot);
-    const Span s = span_of<BL>(a, n);
+    const int64_t seg_slot = u / a.Hk, n = owner<C, true>(a, seg_slot);
+    const Span s = span_of<C>(a, n);
     const int hk = int(u % a.Hk), h = hk * a.group + part / a.tiles, v0 = part % a.tiles * VW;
     const int64_t seg = seg_slot - s.seg;
     const int segs = segments_of(a, s);
@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
         rx.store(lx, id);
         ry.store(ly, id);
         if (wave == 0) decay += put_decays<C>(dec, rg, lane);
-        if (!SUM && (chunk % (BL / C) == BL / C - 1 || chunk == all - 1)) {
-            float* dst = a.ds + ((s.slot + chunk / (BL / C)) * a.Hv + h) * size + int64_t(m) * a.VP + v0 + wave * 16 * CT + 4 * CT * g;
+        if constexpr (!SUM) {
+            float* dst = a.ds + ((s.slot + chunk) * a.Hv + h) * size + int64_t(m) * a.VP + v0 + wave * 16 * CT + 4 * CT * g;
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(256) dca_join_kernel(DcaArgs a, int KP) {
     const int per = int((int64_t(KP) * a.VP + 1023) / 1024);
     const int64_t n = blockIdx.x / (int64_t(per) * a.Hv);
     const int h = int(blockIdx.x / per % a.Hv);
-    const Span s = span_of<64>(a, n);         // (its blocks do not matter here)
+    const Span s = span_of<64>(a, n);         // (its chunks do not matter here)
     const int segs = segments_of(a, s);
     if (segs < 2) return;
     const int64_t size = int64_t(KP) * a.VP;
