@@ -8,7 +8,7 @@ namespace {
 struct DcaPlan {
     int rc;
     int kb, ct, chunk;
-    int64_t slots, seg_slots, segs, seg_tokens, tokens, vp;
+    int64_t slots, seg_slots, segs, seg_tokens, cuts, tokens, vp;
     int64_t states, seg, decays, part;         // bytes of S0 (or dS1) of every chunk, and of the workspace's parts
     int64_t q_bytes, out, gates, fin;
 };
@@ -22,6 +22,8 @@ constexpr int64_t kBlocks = 512;
 // stores, and a block to each CU stores as fast (4 x 4096 tokens of 32 heads of 128: 179 us, and 283 with segments of
 // 128 columns, their sums and joins among them; the forward pass 398, and 332).
 constexpr int64_t kNarrow = 256;
+// Packed sequences may be of unlike length, so they are always cut, at a length that none has where equal ones fill the
+// card: one of 8192 tokens and 63 of 64, 16 heads of 128, without: 822 us, and 144 with; 64 of 192: 87 us, and 115.
 // Tokens to a segment, at least: shorter ones cost more in states through memory than they gain.
 constexpr int64_t kLeast = 128;
 
@@ -46,7 +48,7 @@ DcaPlan dca_plan(const dca_dims* dims) {
     // Segments: as many as fill the card where sequences, heads and columns do not.
     const int64_t wide = d.Hv * (p.vp / (64 * p.ct));
     int64_t len = per > 0 ? per : 1;
-    if (d.N && d.N * wide < kBlocks) {
+    if (d.N && (d.packed || d.N * wide < kBlocks)) {
         const int64_t share = (d.packed ? per : d.N * per) * wide / kBlocks + 1;
         len = share * p.chunk > kLeast ? share : kLeast / p.chunk;
         if (len > per) len = per > 0 ? per : 1;
@@ -54,11 +56,12 @@ DcaPlan dca_plan(const dca_dims* dims) {
     p.seg_tokens = len * p.chunk;
     p.segs = per > len ? (per + len - 1) / len : 1;
     p.seg_slots = d.packed ? d.T / p.seg_tokens + d.N : d.N * p.segs;
+    p.cuts = d.packed ? (d.T + p.seg_tokens - 1) / p.seg_tokens : d.N * p.segs;
     p.tokens = d.B * d.T;
     const int64_t state = int64_t(32) * p.kb * p.vp * 4;
     p.states = up256(p.slots * d.Hv * state);
-    p.seg = p.segs > 1 ? up256(p.seg_slots * d.Hv * state) : 0;
-    p.decays = p.segs > 1 ? up256(p.seg_slots * d.Hv * 4) : 0;
+    p.seg = p.segs > 1 ? up256(p.cuts * d.Hv * state) : 0;
+    p.decays = p.segs > 1 ? up256(p.cuts * d.Hv * 4) : 0;
     p.part = d.head_decay ? up256(p.slots * d.Hv * 4) : 0;
     const size_t e = dtype_bytes(d.dtype);
     p.q_bytes = p.tokens * d.Hk * d.K * e;
@@ -82,6 +85,7 @@ DcaArgs arguments(const dca_dims& d, const DcaPlan& p, const void* q, const void
     a.gs[2] = 1;
     a.T = d.T; a.N = d.N; a.chunks = (d.T + p.chunk - 1) / p.chunk; a.segs = p.segs;
     a.slots = p.slots; a.seg_slots = p.seg_slots; a.seg_tokens = p.seg_tokens;
+    a.cuts = p.cuts;
     a.Hk = int(d.Hk); a.Hv = int(d.Hv); a.group = int(d.Hv / d.Hk); a.K = int(d.K); a.V = int(d.V); a.VP = int(p.vp);
     a.tiles = int(p.vp / (64 * p.ct));
     a.scale = d.scale;

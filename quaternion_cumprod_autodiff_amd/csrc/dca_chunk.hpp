@@ -60,8 +60,8 @@ struct DcaArgs {
     void* out;
     float* fin;
     float* save;                        // S0 of every chunk: [slots][Hv][KP][VP] (or null)
-    float* seg;                         // workspace: states at segments' starts (backward: dS at their ends), as save
-    float* seg_decay;                   // workspace: [segment slots][Hv]
+    float* seg;                         // workspace: states where two segments meet (backward: dS), [cuts][Hv][KP][VP]
+    float* seg_decay;                   // workspace: of the segment that the state passes to get there, [cuts][Hv]
     const void* d_out;
     const float* d_fin;
     void *dq, *dk, *dv;
@@ -71,6 +71,7 @@ struct DcaArgs {
     int64_t qs[3], ks[3], vs[3], gs[3]; // gs: of log_decay, zeros for batch and token where it is of the head alone
     int64_t T, N, chunks, segs;         // chunks, segs: per sequence, without offsets
     int64_t slots, seg_slots, seg_tokens;
+    int64_t cuts;                       // packed: multiples of seg_tokens in T; else N segs
     int Hk, Hv, group, K, V, VP, tiles; // tiles: blocks of 64 CT columns of V
     int vec_qk, vec_v, vec_o;           // rows on 16 bytes and sizes multiples of 8
     float scale;
@@ -127,6 +128,30 @@ __device__ __forceinline__ int64_t owner(const DcaArgs& a, int64_t slot) {
         else hi = mid - 1;
     }
     return lo;
+}
+
+// Of packed sequences: a whole segment holds one multiple of seg_tokens, the cut, so that as many blocks as there are
+// multiples find every segment that another follows, however many sequences there are.  The one that holds multiple j:
+// its sequence, or -1 if no other follows it.
+__device__ __forceinline__ int64_t cut_owner(const DcaArgs& a, int64_t j, int& seg) {
+    const int64_t token = j * a.seg_tokens;
+    int64_t lo = -1, hi = a.N - 1;                   // the last sequence that starts at or before the token
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) / 2;
+        if (a.offsets[mid] <= token) lo = mid;
+        else hi = mid - 1;
+    }
+    if (lo < 0) return -1;
+    const Span s = span_of<64>(a, lo);               // (its chunks do not matter here)
+    if (token < s.t0 || token >= s.t0 + s.len) return -1;
+    seg = int((token - s.t0) / a.seg_tokens);
+    return seg + 1 < segments_of(a, s) ? lo : -1;
+}
+
+// The slot of the state between segments `seg` and seg + 1 of a sequence; of packed ones, the multiple in the first of
+// them.  (Within the cuts: ceil(lo / s) + ceil(len / s) - 2 <= ceil((lo + len) / s) - 1.)
+__device__ __forceinline__ int64_t cut_slot(const DcaArgs& a, const Span& s, int64_t n, int64_t seg) {
+    return a.offsets ? (s.t0 + a.seg_tokens - 1) / a.seg_tokens + seg : n * a.segs + seg;
 }
 
 // Blocks that share a key head's rows run on one XCD (block % 8), next to each other in time.

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
         constexpr int kStep = 36, kLanes = 4 * CT, kPasses = 32 * kLanes / 64;
         static_assert(4 * 16 * CT * kStep * 4 <= sizeof(rows), "the columns' place");
         const bool own = seg > 0;
-        const float* src = own ? a.seg + (seg_slot * a.Hv + h) * int64_t(KP) * a.VP : a.s0 ? a.s0 + (n * a.Hv + h) * int64_t(a.K) * a.V : nullptr;
+        const float* src = own ? a.seg + (cut_slot(a, s, n, seg - 1) * a.Hv + h) * int64_t(KP) * a.VP : a.s0 ? a.s0 + (n * a.Hv + h) * int64_t(a.K) * a.V : nullptr;
         const int nk = own ? KP : a.K, nv = own ? a.VP : a.V, row = lane / kLanes, col = vw + lane % kLanes * 4;
         const bool vec = own || (a.V % 4 == 0 && reinterpret_cast<uintptr_t>(a.s0) % 16 == 0);
         float* t = reinterpret_cast<float*>(rows) + wave * (16 * CT * kStep);

@@ -7,7 +7,7 @@ namespace {
 
 // X = gamma_last X + A^T (w B) over a segment's chunks: forward S with A, B, w =
 // K, V, eta; REV, from the last chunk to the first, dS with Q, dO, scale gamma.
-// SUM: from zero, what a segment adds, stored at the segment that takes it.
+// SUM: from zero, what a segment adds, stored where the next one takes it.
 // Otherwise (REV alone) from the segment's state, which it leaves before each
 // chunk as dS1, and at the end of the sequence as the gradient of s0.  A block
 // has 64 CT columns of V, a wave 16 CT of them, held as [columns of V, KP] so
@@ -25,9 +25,17 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), g = lane / 16, m = lane % 16;
     int64_t u;
     int part;
-    if (!dca_unit(a.seg_slots * a.Hk, a.group * a.tiles, u, part)) return;
-    const int64_t seg_slot = u / a.Hk, n = owner<C, true>(a, seg_slot);
+    if (!dca_unit((SUM && a.offsets ? a.cuts : a.seg_slots) * a.Hk, a.group * a.tiles, u, part)) return;
+    int64_t seg_slot = u / a.Hk, n;
+    int cut = 0;
+    if (SUM && a.offsets) {
+        n = cut_owner(a, seg_slot, cut);
+        if (n < 0) return;
+    } else {
+        n = owner<C, true>(a, seg_slot);
+    }
     const Span s = span_of<C>(a, n);
+    if (SUM && a.offsets) seg_slot = s.seg + cut + REV;       // (from the end, a segment that one is before)
     const int hk = int(u % a.Hk), h = hk * a.group + part / a.tiles, v0 = part % a.tiles * VW;
     const int64_t seg = seg_slot - s.seg;
     const int segs = segments_of(a, s);
@@ -47,7 +55,7 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
             const int k = 16 * r + m, v = v0 + row + 4 * c;
             X[c][r] = zero4();
             if (own) {
-                X[c][r] = *reinterpret_cast<const f32x4*>(a.seg + (seg_slot * a.Hv + h) * size + int64_t(k) * a.VP + v);
+                X[c][r] = *reinterpret_cast<const f32x4*>(a.seg + (cut_slot(a, s, n, seg) * a.Hv + h) * size + int64_t(k) * a.VP + v);
             } else if (!SUM && a.d_fin && k < a.K) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -120,13 +128,13 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
         }
     }
     if constexpr (SUM) {
-        const int64_t to = REV ? seg_slot - 1 : seg_slot + 1;
+        const int64_t to = cut_slot(a, s, n, REV ? seg - 1 : seg);
         float* dst = a.seg + (to * a.Hv + h) * size + v0 + row;
 #pragma unroll
         for (int c = 0; c < CT; ++c)
 #pragma unroll
             for (int r = 0; r < KT; ++r) *reinterpret_cast<f32x4*>(dst + int64_t(16 * r + m) * a.VP + 4 * c) = X[c][r];
-        if (!v0 && tid == 0) a.seg_decay[seg_slot * a.Hv + h] = exp2_of(decay);
+        if (!v0 && tid == 0) a.seg_decay[to * a.Hv + h] = exp2_of(decay);
     } else if (a.ds0 && seg == 0) {
 #pragma unroll
         for (int c = 0; c < CT; ++c)
@@ -145,8 +153,13 @@ __global__ void __launch_bounds__(256, 2) dca_state_kernel(DcaArgs a) {
 template <bool REV>
 __global__ void __launch_bounds__(256) dca_join_kernel(DcaArgs a, int KP) {
     const int per = int((int64_t(KP) * a.VP + 1023) / 1024);
-    const int64_t n = blockIdx.x / (int64_t(per) * a.Hv);
+    int64_t n = blockIdx.x / (int64_t(per) * a.Hv);
     const int h = int(blockIdx.x / per % a.Hv);
+    if (a.offsets) {
+        int cut = 0;
+        n = cut_owner(a, n, cut);
+        if (n < 0 || cut) return;                 // (the sequence's first cut stands for it)
+    }
     const Span s = span_of<64>(a, n);         // (its chunks do not matter here)
     const int segs = segments_of(a, s);
     if (segs < 2) return;
@@ -161,8 +174,8 @@ __global__ void __launch_bounds__(256) dca_join_kernel(DcaArgs a, int KP) {
         for (int i = 0; i < 4; ++i)
             if (v + i < a.V) run[i] = start[((n * a.Hv + h) * a.K + k) * a.V + v + i];
     }
-    // Step i = 1 .. segs - 1 takes the state over segment i - 1 (REV: counted from the end) to i's place.
-    auto slot = [&](int i) { return s.seg + (REV ? segs - 1 - i : i); };
+    // Step i = 1 .. segs - 1 takes the state over segment i - 1 (REV: counted from the end), to where it meets the next.
+    auto slot = [&](int i) { return cut_slot(a, s, n, REV ? segs - 1 - i : i - 1); };
     constexpr int kAhead = 8;
     for (int i0 = 1; i0 < segs; i0 += kAhead) {
         f32x4 x[kAhead];
@@ -171,7 +184,7 @@ __global__ void __launch_bounds__(256) dca_join_kernel(DcaArgs a, int KP) {
         for (int j = 0; j < kAhead; ++j) {
             const int i = i0 + j < segs ? i0 + j : segs - 1;
             x[j] = *reinterpret_cast<const f32x4*>(a.seg + (slot(i) * a.Hv + h) * size + at);
-            d[j] = a.seg_decay[slot(i - 1) * a.Hv + h];
+            d[j] = a.seg_decay[slot(i) * a.Hv + h];
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
@@ -192,7 +205,7 @@ hipError_t launch_dca_state(int dt, int kb, int ct, bool rev, bool sum, const Dc
                                : reinterpret_cast<const void*>(&dca_state_kernel<DT, KB, CT, true, false>);
         DcaArgs args = a;
         void* params[] = {&args};
-        const int64_t blocks = (a.seg_slots * a.Hk + 7) / 8 * 8 * (a.group * a.tiles);
+        const int64_t blocks = ((sum && a.offsets ? a.cuts : a.seg_slots) * a.Hk + 7) / 8 * 8 * (a.group * a.tiles);
         return hipLaunchKernel(fn, dim3(unsigned(blocks)), dim3(256), params, 0, st);
     });
 }
@@ -202,7 +215,7 @@ hipError_t launch_dca_join(int kb, bool rev, const DcaArgs& a, hipStream_t st) {
     DcaArgs args = a;
     int KP = 32 * kb;
     void* params[] = {&args, &KP};
-    return hipLaunchKernel(fn, dim3(unsigned((int64_t(KP) * a.VP + 1023) / 1024 * a.N * a.Hv)), dim3(256), params, 0, st);
+    return hipLaunchKernel(fn, dim3(unsigned((int64_t(KP) * a.VP + 1023) / 1024 * (a.offsets ? a.cuts : a.N) * a.Hv)), dim3(256), params, 0, st);
 }
 
 }  // namespace qc

@@ -141,6 +141,16 @@ def test_packed(lengths, tail, dtype, head):
             assert torch.equal(state[n], args[4][n]) and torch.equal(grads[4][n], cot[1][n])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+@pytest.mark.parametrize("lengths", [[128, 256, 0, 129, 127, 1, 640, 0, 0, 383], [7] * 140 + [1000] + [5] * 40, [1] + [255] * 4 + [0] * 3 + [257, 513, 2],
+                                     [0, 700, 0] + [3] * 200], ids=lambda x: f"{len(x)} sequences")
+def test_packed_sequences_of_unlike_length(lengths, dtype):
+    """Ends at, before and behind the places where segments may meet; a long sequence among many short ones."""
+    print(f"[packed {len(lengths)} {dtype}]", flush=True)
+    args, cot = inputs(1, sum(lengths), 2, 4, 40, 24, dtype, N=len(lengths), seed=len(lengths))
+    check(args, cot, lengths)
+
+
 def test_packed_equals_a_batch_bit_for_bit():
     args, cot = inputs(3, 128, 1, 2, 64, 32, BF16, seed=11)
     leaves = [t.clone().requires_grad_() for t in args]
