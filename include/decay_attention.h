@@ -31,9 +31,8 @@
  *
  * Arithmetic: products run on bfloat16 MFMA with operands split into bfloat16
  * parts, summed in float32.  Inputs are held whole (three parts for float32).
- * States, their gradients, the gradient of log_decay and everything of float32
- * have float32 accuracy; on the way to an output that is rounded to 16 bits,
- * computed operands keep two parts (2^-18).  Decays are cumulated in float64;
+ * Computed operands keep three parts, whole significands, so that everything
+ * has float32 accuracy before its rounding.  Decays are cumulated in float64;
  * below -10^4 they count as -10^4 (their exponential is zero in float32).
  * log_decay of -inf clears a finite state, as exp(-inf) = 0 says.  A key,
  * decay (other than -inf) or value that is not finite reaches its own and later

@@ -31,8 +31,11 @@
 //
 // Arithmetic.  All products are v_mfma_f32_16x16x32_bf16 on operands split into
 // bfloat16 parts: inputs whole (one part for bfloat16, two for float16, three
-// for float32), computed operands in three, or in two on the way to an output
-// that is rounded to 16 bits.
+// for float32), computed operands in three, which hold a float32 whole.  Two on
+// the way to an output of 16 bits were 3 to 11% faster (prompt of 8192 tokens of
+// 32 heads of 128: 144 us, three 154; training step of 4 x 4096: 1036, 1147), but
+// put it 15 times as far from the value as float32 does before its rounding, and
+// lost the last bits of differences.
 //
 // Layouts.  A lane l = 16 g + m holds of an operand fragment row m (A) or column
 // m (B) and the 8 consecutive indices 32 b + 8 g + .. of the contracted axis'
@@ -51,7 +54,6 @@
 namespace qc {
 
 constexpr int dca_chunk(int dt) { return dt == 1 ? 64 : 32; }
-constexpr int dca_parts(int dt) { return dt == 0 ? 3 : 2; }        // of operands computed on the way to an output
 
 struct DcaArgs {
     const void *q, *k, *v;
@@ -353,6 +355,30 @@ __device__ __forceinline__ void whole(const bf16x8 (&p)[NP], float (&x)[8]) {
         x[j] = float(p[NP - 1][j]);
 #pragma unroll
         for (int n = NP - 2; n >= 0; --n) x[j] += float(p[n][j]);
+    }
+}
+
+// Eight floats as their upper and their lower 16 bits: whole in two planes of LDS that are read transposed like bfloat16,
+// where three parts take three planes.
+__device__ __forceinline__ void halves(const float (&x)[8], bf16x8 (&h)[2]) {
+    typedef uint32_t Words __attribute__((ext_vector_type(4)));
+    Words hi, lo;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t a = __float_as_uint(x[2 * j]), b = __float_as_uint(x[2 * j + 1]);
+        hi[j] = __builtin_amdgcn_perm(b, a, 0x07060302);
+        lo[j] = __builtin_amdgcn_perm(b, a, 0x05040100);
+    }
+    h[0] = __builtin_bit_cast(bf16x8, hi);
+    h[1] = __builtin_bit_cast(bf16x8, lo);
+}
+__device__ __forceinline__ void of_halves(const bf16x8 (&h)[2], float (&x)[8]) {
+    typedef uint32_t Words __attribute__((ext_vector_type(4)));
+    const Words hi = __builtin_bit_cast(Words, h[0]), lo = __builtin_bit_cast(Words, h[1]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float(__builtin_amdgcn_perm(hi[j], lo[j], 0x05040100));
+        x[2 * j + 1] = __uint_as_float(__builtin_amdgcn_perm(hi[j], lo[j], 0x07060302));
     }
 }
 

@@ -20,13 +20,13 @@ namespace {
 template <int DT, int KB, int CT, bool SAVE>
 __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
     using E = typename Storage<DT>::type;
-    constexpr int C = dca_chunk(DT), NP = parts_of(DT), PP = dca_parts(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 64 * CT, KT = 2 * KB;
+    constexpr int C = dca_chunk(DT), NP = parts_of(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 64 * CT, KT = 2 * KB;
     // Rows of Q, K and V; between chunks, a wave's columns of S on their way to memory.
     __shared__ __align__(16) char rows[NP * C * (2 * KP + VW) * 2];
     char *lq = rows, *lk = lq + NP * C * KP * 2, *lv = lk + NP * C * KP * 2;
-    __shared__ __align__(16) bf16x8 lp[dca_tri(C)][PP][64];
+    __shared__ __align__(16) bf16x8 lp[dca_tri(C)][kParts][64];
     __shared__ __align__(16) Decays<C> dec;
-    constexpr bool kTight = KB == 4 && CT == 2;
+    constexpr bool kTight = KB * CT == 8 || (DT == 1 && KB * CT == 4);
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), g = lane / 16, m = lane % 16;
     int64_t u;
     int part;
@@ -163,10 +163,10 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
                 }
                 float x[8];
                 decayed_pairs(dec, pt, wave, b, g, m, 1.f, x);
-                bf16x8 p[PP];
-                split<PP, 8>(x, p);
+                bf16x8 p[kParts];
+                split<kParts, 8>(x, p);
 #pragma unroll
-                for (int j = 0; j < PP; ++j) lp[tri_of(wave, b)][j][lane] = p[j];
+                for (int j = 0; j < kParts; ++j) lp[tri_of(wave, b)][j][lane] = p[j];
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -178,12 +178,12 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
         const int l1 = fresh<kTight>(lane), g1 = l1 / 16, m1 = l1 % 16;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-            bf16x8 sf[CT][PP];
+            bf16x8 sf[CT][kParts];
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 const float x[8] = {S[2 * kb][c][0], S[2 * kb][c][1], S[2 * kb][c][2], S[2 * kb][c][3],
                                     S[2 * kb + 1][c][0], S[2 * kb + 1][c][1], S[2 * kb + 1][c][2], S[2 * kb + 1][c][3]};
-                split<PP, 8>(x, sf[c]);
+                split<kParts, 8>(x, sf[c]);
             }
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
@@ -244,9 +244,9 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
 #pragma unroll
             for (int b = 0; b < JB; ++b) {
                 if (b > (t >> 1)) continue;
-                bf16x8 pf[PP];
+                bf16x8 pf[kParts];
 #pragma unroll
-                for (int j = 0; j < PP; ++j) pf[j] = lp[tri_of(t, b)][j][lane];
+                for (int j = 0; j < kParts; ++j) pf[j] = lp[tri_of(t, b)][j][lane];
 #pragma unroll
                 for (int c = 0; c < CT; ++c) mma(o[c][t], vf[c][b], pf);
             }

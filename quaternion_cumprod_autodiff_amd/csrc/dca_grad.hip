@@ -25,17 +25,21 @@ namespace {
 template <int DT, int KB>
 __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kernel(DcaArgs a) {
     using E = typename Storage<DT>::type;
-    constexpr int C = dca_chunk(DT), NP = parts_of(DT), PP = dca_parts(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 32, KT = 2 * KB;
+    constexpr int C = dca_chunk(DT), NP = parts_of(DT), TT = C / 16, JB = C / 32, KP = 32 * KB, VW = 32, KT = 2 * KB;
     constexpr int NW = 4, NT = 64 * NW;
     constexpr bool kTight = DT == 1 ? KB > 1 : DT == 2 && KB == 4;
     constexpr int KW = KT / 4 > 0 ? KT / 4 : 1;                // a wave's tiles of K rows
     constexpr int TW = KT / 4 > 0 ? TT : TT / 2, TV = TT / 2;  // and of tokens, of dQ and dK, and of dV
+    // dS1 in LDS as halves of floats, split where it is read, where its three parts would leave room for one block to a CU
+    // alone (89 KB of 80).  The third part later, in the place of V's rows and of the sums, after a barrier of its own: 674 us,
+    // and 668 so; elsewhere parts cost less (float32 64 x 128, whole step: 667 us, halves 675).
+    constexpr bool kHalves = DT == 1 && KB == 4;
     constexpr int kPairs = dca_tri(C), PW = (kPairs + NW - 1) / NW;
     struct Sums {
         float reads[NW][C], writes[NW][C], pairs[NW][C], dot[NW], last;
     };
-    __shared__ __align__(16) char lq[NP * C * KP * 2], lk[NP * C * KP * 2], lv[NP * C * VW * 2], lo[NP * C * VW * 2], ld[PP * KP * VW * 2];
-    __shared__ __align__(16) bf16x8 lp[kPairs][PP][64];
+    __shared__ __align__(16) char lq[NP * C * KP * 2], lk[NP * C * KP * 2], lv[NP * C * VW * 2], lo[NP * C * VW * 2], ld[(kHalves ? 2 : kParts) * KP * VW * 2];
+    __shared__ __align__(16) bf16x8 lp[kPairs][kParts][64];
     __shared__ __align__(16) Decays<C> decays[2];              // of this value head and the next
     __shared__ Sums sum;
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), g = lane / 16, m = lane % 16;
@@ -184,10 +188,10 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
                     products(lq, lk, i, b, l, pt, std::integral_constant<int, KP>{});
                     float x[8];
                     decayed_pairs(dec, pt, i, b, l / 16, l % 16, a.scale, x);
-                    bf16x8 f[PP];
-                    split<PP, 8>(x, f);
+                    bf16x8 f[kParts];
+                    split<kParts, 8>(x, f);
 #pragma unroll
-                    for (int q = 0; q < PP; ++q) lp[tri_of(i, b)][q][l] = f[q];
+                    for (int q = 0; q < kParts; ++q) lp[tri_of(i, b)][q][l] = f[q];
                 }
                 products(lo, lv, i, b, l, ov[p], std::integral_constant<int, VW>{});
                 __builtin_amdgcn_sched_barrier(0);
@@ -208,8 +212,16 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
                     const float y[8] = {lo4[0], lo4[1], lo4[2], lo4[3], hi4[0], hi4[1], hi4[2], hi4[3]};
                     split<kParts, 8>(y, sf[e]);
                     if (side && tt0 == 0) {
+                        char* to = ld + lds_piece<VW>(k0 + 16 * e + m, g);
+                        if constexpr (kHalves) {
+                            bf16x8 f[2];
+                            halves(y, f);
 #pragma unroll
-                        for (int p = 0; p < PP; ++p) *reinterpret_cast<bf16x8*>(ld + p * (KP * VW * 2) + lds_piece<VW>(k0 + 16 * e + m, g)) = sf[e][p];
+                            for (int p = 0; p < 2; ++p) *reinterpret_cast<bf16x8*>(to + p * (KP * VW * 2)) = f[p];
+                        } else {
+#pragma unroll
+                            for (int p = 0; p < kParts; ++p) *reinterpret_cast<bf16x8*>(to + p * (KP * VW * 2)) = sf[e][p];
+                        }
                     }
                 }
 #pragma unroll
@@ -230,8 +242,16 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
                 for (int t = 0; t < TV; ++t) dv[t] = zero4();
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
-                    bf16x8 df[PP];
-                    col_fragment<KP, VW>(ld, kb, g, m, v_col + 4 * (m & 3), df);
+                    bf16x8 df[kParts];
+                    if constexpr (kHalves) {
+                        bf16x8 f[2];
+                        col_fragment<KP, VW>(ld, kb, g, m, v_col + 4 * (m & 3), f);
+                        float x[8];
+                        of_halves(f, x);
+                        split<kParts, 8>(x, df);
+                    } else {
+                        col_fragment<KP, VW>(ld, kb, g, m, v_col + 4 * (m & 3), df);
+                    }
 #pragma unroll
                     for (int t = 0; t < TV; ++t) {
                         bf16x8 kf[NP];
@@ -248,7 +268,7 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
 #pragma unroll
                     for (int t = 0; t < TV; ++t) {
                         if (b < ((tv0 + t) >> 1)) continue;
-                        bf16x8 pf[PP];
+                        bf16x8 pf[kParts];
                         tri_cols(lp, b, g, m, tv0 + t, pf);
                         mma(dv[t], of, pf);
                     }
@@ -319,10 +339,10 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
             const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
             float x[8];
             decayed_pairs(dec, ov[p], i, b, g, m, a.scale, x);
-            bf16x8 f[PP];
-            split<PP, 8>(x, f);
+            bf16x8 f[kParts];
+            split<kParts, 8>(x, f);
 #pragma unroll
-            for (int q = 0; q < PP; ++q) lp[tri_of(i, b)][q][l] = f[q];
+            for (int q = 0; q < kParts; ++q) lp[tri_of(i, b)][q][l] = f[q];
             if (want_dg) {
                 // M_ij of this pair, i > j, and its sums over j < t <= i, for each t.
                 f32x4 qk[2] = {zero4(), zero4()};
@@ -394,10 +414,10 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
 #pragma unroll
                 for (int t = 0; t < TW; ++t) {
                     const int tile = tt0 + t;
-                    bf16x8 pf[PP];
+                    bf16x8 pf[kParts];
                     if (b <= (tile >> 1)) {
 #pragma unroll
-                        for (int i = 0; i < PP; ++i) pf[i] = lp[tri_of(tile, b)][i][l];
+                        for (int i = 0; i < kParts; ++i) pf[i] = lp[tri_of(tile, b)][i][l];
 #pragma unroll
                         for (int e = 0; e < KW; ++e) mma(dq[e][t], kf[e], pf);
                     }
