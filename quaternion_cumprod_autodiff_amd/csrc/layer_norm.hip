@@ -352,30 +352,36 @@ LnShape ln_shape(int64_t D, int64_t all, bool wide, bool bwd) {
 }
 
 // The weights' gradients from the blocks' partial sums: 16 columns and 64 runs
-// of blocks to a block of threads, the runs joined in order.
+// of blocks to a block of threads, the runs joined in order.  A launch holds
+// less than 2^32 threads, so blocks take every kLnColumns-th 16 columns.
 constexpr int kLnRuns = 64;
+constexpr int64_t kLnColumns = int64_t(1) << 20;
 
 template <int DT>
 __global__ void __launch_bounds__(16 * kLnRuns) ln_weight_kernel(const float* part, int64_t n, int heads, int D, void* dw, void* db) {
     using E = typename Storage<DT>::type;
     E* out = static_cast<E*>(blockIdx.y ? db : dw);
     if (!out) return;
-    const int64_t col = int64_t(blockIdx.x) * 16 + threadIdx.x % 16, all = int64_t(heads) * D;
+    const int64_t all = int64_t(heads) * D;
     const int run = threadIdx.x / 16;
     __shared__ float red[kLnRuns][17];
-    float s = 0.f;
-    if (col < all) {
-        const float* p = part + (col / D * 2 + blockIdx.y) * D + col % D;
+    for (int64_t first = int64_t(blockIdx.x) * 16; first < all; first += kLnColumns * 16) {
+        const int64_t col = first + threadIdx.x % 16;
+        float s = 0.f;
+        if (col < all) {
+            const float* p = part + (col / D * 2 + blockIdx.y) * D + col % D;
 #pragma unroll 4
-        for (int64_t i = run; i < n; i += kLnRuns) s += p[i * 2 * all];
-    }
-    red[run][threadIdx.x % 16] = s;
-    __syncthreads();
-    if (threadIdx.x < 16 && col < all) {
-        float t = 0.f;
+            for (int64_t i = run; i < n; i += kLnRuns) s += p[i * 2 * all];
+        }
+        red[run][threadIdx.x % 16] = s;
+        __syncthreads();
+        if (threadIdx.x < 16 && col < all) {
+            float t = 0.f;
 #pragma unroll 8
-        for (int i = 0; i < kLnRuns; ++i) t += red[i][threadIdx.x];
-        out[col] = E(t);
+            for (int i = 0; i < kLnRuns; ++i) t += red[i][threadIdx.x];
+            out[col] = E(t);
+        }
+        __syncthreads();
     }
 }
 
@@ -543,8 +549,9 @@ int lnm_bwd(const lnm_dims* dims, const void* x, const void* weight, const float
             int heads = a.heads, D = a.D;
             void *dw = d_weight, *db = d_bias;
             void* params[] = {&part, &blocks, &heads, &D, &dw, &db};
+            const int64_t columns = (int64_t(heads) * D + 15) / 16;
             return hipLaunchKernel(reinterpret_cast<const void*>(&qc::ln_weight_kernel<decltype(t)::value>),
-                                   dim3(unsigned((int64_t(heads) * D + 15) / 16), 2), dim3(16 * qc::kLnRuns), params, 0, st);
+                                   dim3(unsigned(columns < qc::kLnColumns ? columns : qc::kLnColumns), 2), dim3(16 * qc::kLnRuns), params, 0, st);
         });
     }
     return err == hipSuccess ? QC_OK : qc::record_hip_error(err);

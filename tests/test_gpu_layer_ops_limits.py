@@ -1,0 +1,46 @@
+"""Layer norm and linear attention with decays at the sizes that their headers allow and little reaches (needs an
+MI355X)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import layer_ops as ref
+from quaternion_cumprod_autodiff_amd import layer_norm
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def near(label, got, want, size):
+    """Half a step of bfloat16 for the one rounding, and 1e-5 of the terms' size for float32's sums over a row: by at most
+    14 levels of pairs and 32 in a row, 46 2^-24, and four products more."""
+    off = np.abs(f64(got) - want) - 2.0 ** -8 * np.abs(want) - 1e-5 * size
+    assert np.isfinite(f64(got)).all() and off.max() <= 1e-30, f"{label}: {off.max():.3e} too far"
+
+
+@pytest.mark.parametrize("heads,D", [(65535, 1024), (65536, 1024), (1 << 20, 2040)], ids=str)
+def test_norm_of_many_weights_of_heads(heads, D):
+    """Columns of weights on both sides of 2^26, and close to 2^31: their gradients' kernel takes them 16 to a block, and a
+    launch holds less than 2^32 threads.  One token, so a bias' gradient is its cotangent, bit for bit."""
+    print(f"[norm of {heads} heads of {D}]", flush=True)
+    gen = torch.Generator(device=DEV).manual_seed(heads)
+    x, dy = (torch.empty(1, heads, D, device=DEV, dtype=BF16).normal_(generator=gen) for _ in range(2))
+    w, b = (torch.empty(heads, D, device=DEV, dtype=BF16).normal_(1.0, 0.3, generator=gen) for _ in range(2))
+    leaves = [t.requires_grad_() for t in (x, w, b)]
+    y = layer_norm(*leaves)
+    dx, dw, db = torch.autograd.grad(y, leaves, dy)
+    assert torch.equal(db, dy[0])
+    edge = min(heads, 65536)
+    for at in (slice(0, 3), slice(edge - 2, edge + 1), slice(heads - 3, heads)):
+        fx, fw, fb, fd = (f64(t) for t in (x[:, at], w[at], b[at], dy[:, at]))
+        h = ref.lnm_fwd(fx, None, None, 1e-5)
+        near("y", y[:, at], ref.lnm_fwd(fx, fw, fb, 1e-5), np.abs(h).max(-1, keepdims=True) * np.abs(fw).max() + np.abs(fb))
+        rx, rw, _ = ref.lnm_bwd(fx, fw, 1e-5, fd, True)
+        near("gradient of weight", dw[at], rw, np.abs(fd[0]) * np.abs(h[0]).max())
+        big = (np.abs(fd) * np.abs(fw)).max(-1, keepdims=True) * (1 + np.abs(h).max(-1, keepdims=True))
+        near("gradient of x", dx[:, at], rx, big / np.sqrt(fx.var(-1, keepdims=True)))
