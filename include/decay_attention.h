@@ -49,7 +49,9 @@
  * B, T, N >= 0, T below 2^31, element counts at most 2^40.  dca_fwd, dca_bwd:
  * Hv ceil(V / 64) times the chunks of 32 tokens (N ceil(T / 32); with offsets
  * T / 32 + N) below 2^23, and N Hk rounded up to a multiple of 8, times
- * Hv / Hk ceil(V / 64), too.  dca_step: N Hv ceil(V / 32) up to 2^25.
+ * Hv / Hk ceil(V / 64), too.  dca_step: N Hv ceil(V / 32) up to 2^25, and with
+ * slots, N times that up to 2^40 (a row looks through the slots of those before
+ * it, once for each head and 32 columns).
  *
  * Conventions: as in gated_delta.h.  Device pointers are the caller's; the
  * library never allocates, frees or keeps one.  Validation is on the host,

@@ -198,6 +198,9 @@ extern "C" int dca_step(const dca_dims* dims, const void* query, const void* key
                                {value, size_t(qc::strided_bytes(d.B, d.T, d.Hv, d.V, d.v_stride, e))},
                                {log_decay, gates}, {slots, size_t(d.N) * 4}};
     if (qc::outputs_overlap(sp, 2, 7)) return QC_ERR_ALIAS;
+    // What the waves look through of the slots before their rows, at most: 2^40 take 127 ms (2^20 rows of one head of 8 x 16,
+    // 0.6 ms without slots), and 2^25 rows would take two minutes.
+    if (slots && qc::count(used, d.N) < 0) return QC_ERR_SHAPE;
     qc::StepArgs a{};
     a.q = query; a.k = key; a.v = value; a.g = log_decay; a.state = state; a.slots = slots; a.out = out;
     for (int i = 0; i < 3; ++i) {

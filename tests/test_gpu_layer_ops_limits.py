@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import layer_ops as ref
-from quaternion_cumprod_autodiff_amd import layer_norm
+from quaternion_cumprod_autodiff_amd import capi, decay_attention_step, layer_norm
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -44,3 +44,30 @@ def test_norm_of_many_weights_of_heads(heads, D):
         near("gradient of weight", dw[at], rw, np.abs(fd[0]) * np.abs(h[0]).max())
         big = (np.abs(fd) * np.abs(fw)).max(-1, keepdims=True) * (1 + np.abs(h).max(-1, keepdims=True))
         near("gradient of x", dx[:, at], rx, big / np.sqrt(fx.var(-1, keepdims=True)))
+
+
+def test_as_many_slots_as_a_step_looks_through():
+    """2^20 rows of one head and 32 columns, the last of them named by the first row already, and by its neighbour."""
+    N, K, V = 1 << 20, 2, 8
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    q, k = (torch.randn(N, 1, 1, K, generator=gen, device=DEV) for _ in range(2))
+    v, g = torch.randn(N, 1, 1, V, generator=gen, device=DEV), -torch.rand(N, 1, 1, generator=gen, device=DEV)
+    state = torch.randn(N, 1, K, V, generator=gen, device=DEV)
+    slots = torch.randperm(N, generator=gen, device=DEV).int()
+    slots[N - 1], slots[N - 2], slots[N // 2] = slots[0], slots[N - 3], slots[1]
+    before = state.clone()
+    out = decay_attention_step(q, k, v, g, state, slots=slots)
+    run = torch.ones(N, dtype=torch.bool, device=DEV)
+    run[[N - 1, N - 2, N // 2]] = False
+    rows = slots.long()[run]
+    want = g[run].double().exp()[:, :, :, None] * before[rows].double() + k[run, 0, :, :, None].double() * v[run, 0, :, None, :].double()
+    # Two roundings and an exponential's of terms, and float32 sums of two of them.
+    assert ((state[rows].double() - want).abs() <= 2.0 ** -21 * (1 + before[rows].double().abs() + (k[run, 0, :, :, None] * v[run, 0, :, None, :]).abs())).all()
+    assert not out[~run].any()
+    read = (want * q[run, 0, :, :, None].double()).sum(2) * K ** -0.5
+    assert ((out[run, 0].double() - read).abs() <= 2.0 ** -19 * (1 + (want.abs() * q[run, 0, :, :, None].abs()).sum(2))).all()
+    left = torch.ones(N, dtype=torch.bool, device=DEV)
+    left[rows] = False
+    assert torch.equal(state[left], before[left])
+    with pytest.raises(capi.QuatCumprodError):
+        decay_attention_step(*(torch.cat([t, t[:1]]) for t in (q, k, v, g)), state, slots=torch.cat([slots, slots[:1]]))
