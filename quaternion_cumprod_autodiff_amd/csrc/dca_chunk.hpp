@@ -32,8 +32,8 @@
 // Arithmetic.  All products are v_mfma_f32_16x16x32_bf16 on operands split into
 // bfloat16 parts: inputs whole (one part for bfloat16, two for float16, three
 // for float32), computed operands in three, which hold a float32 whole.  Two on
-// the way to an output of 16 bits were 3 to 11% faster (prompt of 8192 tokens of
-// 32 heads of 128: 144 us, three 154; training step of 4 x 4096: 1036, 1147), but
+// the way to an output of 16 bits were 3 to 7% faster (prompt of 8192 tokens of
+// 32 heads of 128: 144 us, three 154; training step of 4 x 4096: 1036, 1099), but
 // put it 15 times as far from the value as float32 does before its rounding, and
 // lost the last bits of differences.
 //
@@ -182,8 +182,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // TIGHT: a lane's number that the compiler takes for a new one.  Addresses made of it are made again in each phase of a
 // chunk, a few instructions, instead of being held over all of them, in registers that the state needs (bfloat16, 128 x
-// 128, forward: 272 bytes a lane spilled and 160 us, none and 97; but where nothing spills 142 us become 160, float32
-// 64 x 128).
+// 128, forward, with two parts of the state: 272 bytes a lane spilled and 160 us, none and 97; but where nothing spills
+// 142 us become 160, float32 64 x 128).
 template <bool TIGHT>
 __device__ __forceinline__ int fresh(int x) {
     if constexpr (TIGHT) asm volatile("" : "+v"(x));

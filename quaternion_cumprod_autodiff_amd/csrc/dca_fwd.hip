@@ -12,11 +12,13 @@ namespace {
 // before), P by tiles of 16 rows to a wave and shared through LDS, out^T = S^T
 // Q^T gamma + V^T P^T, S = gamma_last S + K^T (eta V).
 //
-// Bound by instructions: a wave's chunk of 64 x 128 x 128 in bfloat16 is 196 MFMA
-// (3100 cycles) and 1120 vector instructions (4500; splits, decays, scaling) in
-// five phases, and two waves to a SIMD, as many as the registers allow, take
-// 16000 cycles for both.  8192 tokens of 32 heads of 128: 98 us, 22 GFLOP of the
-// recurrence and 200 MB; with S0 saved, 4 x 4096 tokens, 240 us, 940 MB, 3.9 TB/s.
+// Bound by instructions: a wave's chunk of 64 x 128 x 128 in bfloat16 is 240 MFMA
+// (3840 cycles) and 1570 vector instructions (6280; splits, decays, scaling) in
+// five phases.  Two waves to a SIMD, as many as the registers allow, spend 22500
+// cycles on a chunk each, 20200 of them in the two kinds of instructions, which
+// so hardly run beside each other.  8192 tokens of 32 heads of 128: 110 us, 22
+// GFLOP of the recurrence and 200 MB; with S0 saved, 4 x 4096 tokens, 257 us, 940
+// MB, 3.7 TB/s.
 template <int DT, int KB, int CT, bool SAVE>
 __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
     using E = typename Storage<DT>::type;
@@ -26,7 +28,9 @@ __global__ void __launch_bounds__(256, 2) dca_fwd_kernel(DcaArgs a) {
     char *lq = rows, *lk = lq + NP * C * KP * 2, *lv = lk + NP * C * KP * 2;
     __shared__ __align__(16) bf16x8 lp[dca_tri(C)][kParts][64];
     __shared__ __align__(16) Decays<C> dec;
-    constexpr bool kTight = KB * CT == 8 || (DT == 1 && KB * CT == 4);
+    // (64 x 128 with S0 saved: 9 registers spilled and 248 us for 4 x 4096 tokens of 32 heads, 224 so; not saved, 4 of them and
+    // 118 us for 8192 tokens, 122 so; 128 x 64, saved or not: 2 to 4% slower so.)
+    constexpr bool kTight = KB * CT == 8 || (DT == 1 && KB == 2 && CT == 2 && SAVE);
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), g = lane / 16, m = lane % 16;
     int64_t u;
     int part;

@@ -14,14 +14,18 @@ namespace {
 // memory as rows, the next 32 columns' while these are worked on; dV takes dS1's
 // columns from LDS.
 //
-// 4 x 4096 tokens of 32 heads of 128, bfloat16: 570 us, 1.75 GB of inputs, states
-// and gradients (340 us at the rate of a copy), 41% of the time in vector
-// instructions and 15% in MFMA; with the states out of cache it takes 531 us, so
-// that memory is not what bounds it but the phases between barriers, of which
-// each alone is worth 16 to 90 us.  Tried: 128 tokens to a block of eight waves,
-// which halves the states' way through memory (1205 us: one block to a CU, every
-// phase's wait in full), 64 tokens and eight waves, everything a phase ahead (629
-// us), columns of dS1 read from memory as such (643 us).
+// 4 x 4096 tokens of 32 heads of 128, bfloat16: 629 us, 1.75 GB of inputs, states
+// and gradients (340 us at the rate of a copy), 47% of the time in vector
+// instructions and 15% in MFMA, one wave's hardly beside another's.  With two
+// parts of what is computed it took 566 us, of which 35 were the states' way from
+// memory (out of cache 531) and no phase between barriers more than 90; then were
+// tried 128 tokens to a block of eight waves, which halves the states' way (1205
+// us: one block to a CU, every phase's wait in full), 64 tokens and eight waves,
+// everything a phase ahead (629), columns of dS1 read from memory as such (643).
+// Two registers spill at K > 64 in bfloat16, once for a value head.  One key
+// head's value heads follow each other in a block: 2048 tokens of one key head and
+// 64 value heads of 128 x 64 are 32 blocks, and 1.19 ms with the states' pass,
+// where 64 key heads take 0.21.
 template <int DT, int KB>
 __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kernel(DcaArgs a) {
     using E = typename Storage<DT>::type;
@@ -31,8 +35,8 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
     constexpr int KW = KT / 4 > 0 ? KT / 4 : 1;                // a wave's tiles of K rows
     constexpr int TW = KT / 4 > 0 ? TT : TT / 2, TV = TT / 2;  // and of tokens, of dQ and dK, and of dV
     // dS1 in LDS as halves of floats, split where it is read, where its three parts would leave room for one block to a CU
-    // alone (89 KB of 80).  The third part later, in the place of V's rows and of the sums, after a barrier of its own: 674 us,
-    // and 668 so; elsewhere parts cost less (float32 64 x 128, whole step: 667 us, halves 675).
+    // alone (89 KB of 80).  The third part later, in the place of V's rows and of the sums, after a barrier of its own: 674 us
+    // where halves took 668; elsewhere parts cost less (float32 64 x 128, whole step: 667 us, halves 675).
     constexpr bool kHalves = DT == 1 && KB == 4;
     constexpr int kPairs = dca_tri(C), PW = (kPairs + NW - 1) / NW;
     struct Sums {
@@ -233,7 +237,8 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if (more) load_states(next_j, next_v);
+            // (Beside them what the halves take would spill accumulators, 360 MB written for 290 of results: 664 us, 629 so.)
+            if (more && !kHalves) load_states(next_j, next_v);
             __syncthreads();                                  // P and dS1 are there
             if (a.dv) {
                 const int l = fresh<kTight>(lane), g = l / 16, m = l % 16;
@@ -290,6 +295,7 @@ __global__ void __launch_bounds__(256, DT == 0 && KB == 4 ? 1 : 2) dca_grad_kern
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
+            if (more && kHalves) load_states(next_j, next_v);
         }
         // gamma and eta of them, and what dg needs: q and k with their shares of dQ and dK.
         float reads[TW], writes[TW];
