@@ -409,10 +409,12 @@ def decay_attention(query, key, value, log_decay, initial_state=None, *, scale=N
     (a value: in its column); a query its own token; what comes before is as
     without it.  Gradients: anywhere in its sequence.
 
-    With gradients, the float32 states of every chunk of 64 tokens (bfloat16;
-    32 for the other types) are kept from forward to backward:
-    N ceil(T / 64) Hv K' V' 4 bytes, K' = 32, 64 or 128 and V' a multiple of 64
-    (of 128 from 65 on); the backward pass takes as much again while it runs.
+    With gradients, the float32 states of every chunk of C = 64 tokens
+    (bfloat16; 32 for the other types) are kept from forward to backward, Hv K'
+    V' 4 bytes each, K' = 32, 64 or 128 and V' a multiple of 64 (of 128 from 65
+    on): N ceil(T / C) of them, with offsets floor(T / C) + N, so that a short
+    packed sequence costs a state as well; the backward pass takes as much again
+    while it runs.
 
     Forward and backward can be captured into a graph, as for
     :func:`gated_delta_rule`."""
