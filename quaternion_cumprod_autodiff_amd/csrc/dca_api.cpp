@@ -15,8 +15,10 @@ struct DcaPlan {
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// Blocks that a pass over a sequence wants: two to each of 256 CUs (prompt of 8192 tokens of 32 heads of 128: 155 us with
-// 512, 193 with 256, 180 with 1024, whose states pass through memory for more than they gain).
+// Blocks that a pass over a sequence wants: two to each of 256 CUs (bfloat16, heads of 128, calls: 8192 tokens of 32 heads
+// 162 us with 512, 203 with 256, 194 with 1024, whose states pass through memory for more than they gain; 4096 of 32 heads
+// 96, 114, 111; 2048 of 32 heads 69, 74, 66; 8 x 2048 of 16 heads of 64 x 128 in float32 168, 218, 191).  (dca_plan's
+// division leaves segments a chunk longer than an even cut has them, 9 for 8 at the first of these.)
 constexpr int64_t kBlocks = 512;
 // The backward states' pass does without segments from these blocks of 64 columns on: it is bound by the states that it
 // stores, and a block to each CU stores as fast (4 x 4096 tokens of 32 heads of 128: 179 us, and 283 with segments of
@@ -24,7 +26,9 @@ constexpr int64_t kBlocks = 512;
 constexpr int64_t kNarrow = 256;
 // Packed sequences may be of unlike length, so they are always cut, at a length that none has where equal ones fill the
 // card: one of 8192 tokens and 63 of 64, 16 heads of 128, without: 822 us, and 144 with; 64 of 192: 87 us, and 115.
-// Tokens to a segment, at least: shorter ones cost more in states through memory than they gain.
+// Tokens to a segment, at least (bfloat16, heads of 128, calls with 128, 64 and 256: 1024 tokens of one head 39, 31 and 57
+// us, of 16 heads 45, 39 and 60; 4096 of 4 heads 50, 49 and 62, of 16 heads 71, 70 and 70; 30 packed sequences of 64, 8
+// heads, 30.7, 32.8 and 29.5: shorter ones gain where heads are few, and cost states through memory).
 constexpr int64_t kLeast = 128;
 
 DcaPlan dca_plan(const dca_dims* dims) {

@@ -9,7 +9,9 @@
 // piece is one 128-byte line, all of a state's loads are in flight at once, and
 // the reduction stays inside the wave.  810 MB of states (read and written): 152
 // us, 5.3 TB/s, a copy's rate; one row of 32 heads of 128 x 128: 6.7 us, the loads,
-// the reduction and the stores in a row.
+// the reduction and the stores in a row.  Of several tokens one is loaded ahead,
+// which its predecessor's work does not cover: 33 rows of 6 heads of 72 x 100, 6.6
+// us for one token and 11.6 for five.
 #include "dca_internal.hpp"
 
 #include <type_traits>
@@ -162,8 +164,8 @@ const void* step_kernel(int nr, bool vec, bool many, bool stream) {
 }
 
 // From how many bytes of states on a call streams them: a model calls for one layer after another, so that a layer's
-// states are gone from the 256 MB cache when its turn comes again.  (The rule of gdr_step, whose states move alike and
-// where both sides were measured: three pools of 134 MB in turn 60.7 us, streamed 53.6; one of 100 MB alone 37, and 42.)
+// states are gone from the 256 MB cache when its turn comes again.  (Three pools of 134 MB in turn, a call: 61.5 us, streamed
+// 55.1; one alone, which the cache holds, 47.3 and 53.8; one of 403 MB 159.6 and 150; one of 101 MB alone 36.0 and 38.1.)
 constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
 }  // namespace

@@ -14,9 +14,15 @@
 // next to each other in memory: heads of a token, or rows.  What is under way
 // counts, so rows stay as they lie, in half the registers of floats, and sums
 // are made without LDS.  16384 rows of 4096 in bfloat16: 58 us, 4.6 TB/s (as
-// floats, by four waves to a row, 71); 4 x 4096 tokens of 32 heads of 128 with
-// weights of each head: forward 50 us, 5.5 TB/s (one row at a time, heads apart,
-// 64), VJP 81 us, 5.0 TB/s (92), and 4 us for the weights' sums.
+// floats, by four waves to a row, 71), and VJP 126 us, 3.2 TB/s: weight and bias of
+// long rows stay in no register and are read again for each, from the caches, as
+// many bytes as the rows.  4 x 4096 tokens of 32 heads of 128 with weights of each
+// head, held by their groups: forward 50 us, 5.5 TB/s (one row at a time, heads
+// apart, 64), VJP 82 us, 5.0 TB/s (92), and 4 us for the weights' sums.  Rows that
+// are not on 16 bytes go element by element: 16384 of 4100 in bfloat16 292 us, VJP
+// 360; the 4096 of a view that begins at the second element 211, 502.  The VJP
+// spills above 8192 elements: float32 on 16 bytes 100 bytes of scratch a lane, and
+// any type off them 212 to 220 (4096 rows of 16380 in bfloat16: 724 us).
 #include "layer_norm.h"
 #include "lm_common.hpp"
 #include "qc_internal.hpp"
