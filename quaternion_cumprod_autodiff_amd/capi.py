@@ -1224,6 +1224,16 @@ def _lnm_dims(x, by_head, eps):
         lead, st = lead + [1], st + [x.shape[-1]]
     while len(lead) < 3:
         lead, st = [1] + lead, [0] + st
+    if lead[2] > 1 << 20:
+        # More than the third axis holds: rows alike lie along the second too, where two axes are one.
+        if by_head:
+            raise ValueError(f"x may have 2^20 heads of weights of their own, got {lead[2]}")
+        if lead[1] == 1 or st[1] == lead[2] * st[2]:
+            lead, st = [lead[0], lead[1] * lead[2], 1], [st[0], st[2], x.shape[-1]]
+        elif lead[0] == 1 or st[0] == lead[1] * st[1]:
+            lead, st = [lead[0] * lead[1], lead[2], 1], [st[1], st[2], x.shape[-1]]
+        else:
+            raise ValueError(f"x's third axis of {lead[2]} is over 2^20 and no two axes before its rows are one: make it contiguous")
     d = LnmDims(*lead, x.shape[-1])
     d.x_stride[:] = st
     d.dtype, d.by_head, d.eps = _LM_DTYPES[x.dtype], int(by_head), eps

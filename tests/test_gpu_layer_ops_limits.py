@@ -46,6 +46,34 @@ def test_norm_of_many_weights_of_heads(heads, D):
         near("gradient of x", dx[:, at], rx, big / np.sqrt(fx.var(-1, keepdims=True)))
 
 
+@pytest.mark.parametrize("form", ["one token", "dense", "tokens apart", "batch apart", "apart"])
+def test_norm_of_more_rows_to_a_token_than_heads(form):
+    """A third axis above 2^20, of rows that are alike: as the same rows in two axes, bit for bit, gradients too."""
+    H, D = (1 << 20) + 3, 8
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    B, T = {"one token": (1, 1), "dense": (2, 2), "tokens apart": (1, 3), "batch apart": (2, 1), "apart": (2, 2)}[form]
+    x = torch.empty(B + 1, T + 1, H + 1, D, device=DEV, dtype=BF16).normal_(generator=gen)[:B, :T, :H]
+    if form in ("one token", "dense"):
+        x = x.contiguous()
+    w, b = (torch.empty(D, device=DEV, dtype=BF16).normal_(generator=gen) for _ in range(2))
+    if form == "apart":
+        with pytest.raises(ValueError, match="contiguous"):
+            layer_norm(x, w, b)
+        x = x.contiguous()
+    dy = torch.empty(B, T, H, D, device=DEV, dtype=BF16).normal_(generator=gen)
+    leaves = [t.detach().requires_grad_() for t in (x, w, b)]
+    y = layer_norm(*leaves)
+    grads = torch.autograd.grad(y, leaves, dy)
+    rows = [x.reshape(-1, D).requires_grad_(), *leaves[1:]]
+    want = layer_norm(*rows)
+    assert torch.equal(y, want.reshape(y.shape))
+    for got, same in zip(grads, torch.autograd.grad(want, rows, dy.reshape(-1, D))):
+        assert torch.equal(got, same.reshape(got.shape))
+    if form == "one token":
+        with pytest.raises(ValueError, match="2\\^20"):
+            layer_norm(x, torch.empty(H, D, device=DEV, dtype=BF16))
+
+
 def test_as_many_slots_as_a_step_looks_through():
     """2^20 rows of one head and 32 columns, the last of them named by the first row already, and by its neighbour."""
     N, K, V = 1 << 20, 2, 8
