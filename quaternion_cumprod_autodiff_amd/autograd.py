@@ -468,9 +468,9 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
     x: float32, bfloat16 or float16, any strides (views of a fused projection
     are read in place), rows of 1 to 16384 elements; weight and bias of the
     same dtype, [D], or [H, D] for an x [.., H, D] whose heads (up to 2^20) have
-    weights of their own (both alike); None: ones, zeros.  Statistics are float32, the
-    variance from the differences to the mean.  Capturing a backward pass: as
-    for :func:`gated_delta_rule`."""
+    weights of their own (both alike); None: ones, zeros.  Statistics are
+    float32, the variance from the differences to the mean.  Capturing a
+    backward pass: as for :func:`gated_delta_rule`."""
     _refuse_forward_mode("layer_norm", x, weight, bias)
     x, eps = _last_dense(x), float(eps)
     shape = x.shape

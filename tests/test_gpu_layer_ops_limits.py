@@ -1,11 +1,13 @@
 """Layer norm and linear attention with decays at the sizes that their headers allow and little reaches (needs an
 MI355X)."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 from oracle import layer_ops as ref
-from quaternion_cumprod_autodiff_amd import capi, decay_attention_step, layer_norm
+from quaternion_cumprod_autodiff_amd import capi, decay_attention, decay_attention_step, layer_norm
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -99,3 +101,78 @@ def test_as_many_slots_as_a_step_looks_through():
     assert torch.equal(state[left], before[left])
     with pytest.raises(capi.QuatCumprodError):
         decay_attention_step(*(torch.cat([t, t[:1]]) for t in (q, k, v, g)), state, slots=torch.cat([slots, slots[:1]]))
+
+
+def test_attention_beyond_2_to_the_31_elements():
+    """Values of 4.8 GB: a decay of -inf makes what is behind it, gradients too, what the tail alone gives, bit for bit."""
+    T, Hk, Hv, K, V = 131072, 16, 144, 16, 128
+    cut, tail = T - 1024, 3072         # whole chunks; segments differ, but decays forget a token within a chunk or two
+    assert T * Hv * V > 2 ** 31
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    q, k = (torch.empty(1, T, Hk, K, device=DEV, dtype=BF16).normal_(0, 0.5, generator=gen) for _ in range(2))
+    v = torch.empty(1, T, Hv, V, device=DEV, dtype=BF16).normal_(generator=gen)
+    g = -torch.rand(1, T, Hv, generator=gen, device=DEV)
+    g[:, cut] = -float("inf")
+    dy = torch.zeros_like(v)
+    dy[:, cut:].normal_(generator=gen)
+
+    def run(*args):
+        *leaves, cot = args
+        leaves = [t.requires_grad_() for t in leaves]
+        out, state = decay_attention(*leaves)
+        return (out.detach(), *torch.autograd.grad(out, leaves, cot)), state.detach()
+
+    whole, state = run(q, k, v, g, dy)
+    rows, last = run(*(t.detach()[:, T - tail:].clone() for t in (q, k, v, g, dy)))
+    assert torch.equal(state, last)
+    for name, a, b in zip(("out", "query", "key", "value", "log_decay"), whole, rows):
+        assert b[:, cut - T:].any() and torch.equal(a[:, cut:], b[:, cut - T:]), name
+
+
+def test_many_packed_sequences():
+    """70000 of them, of no to three tokens: as a padded batch, bit for bit."""
+    N, L, H = 70000, 3, 2
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    lengths = torch.randint(0, L + 1, (N,), generator=gen, device=DEV)
+    offsets = torch.cat([torch.zeros(1, device=DEV, dtype=torch.int32), lengths.cumsum(0).int()])
+    T = int(offsets[-1])
+    q, k = (torch.empty(1, T, 1, 32, device=DEV, dtype=BF16).normal_(generator=gen) for _ in range(2))
+    v = torch.empty(1, T, H, 32, device=DEV, dtype=BF16).normal_(generator=gen)
+    g = -torch.rand(1, T, H, generator=gen, device=DEV)
+    at = (offsets[:-1, None].long() + torch.arange(L, device=DEV)).clamp_max(T - 1)
+    inside = torch.arange(L, device=DEV) < lengths[:, None]
+    padded = lambda t: torch.where(inside.reshape(N, L, *[1] * (t.dim() - 2)), t[0][at], torch.zeros((), device=DEV, dtype=t.dtype))
+    out, state = decay_attention(q, k, v, g, offsets=offsets)
+    want, last = decay_attention(*(padded(t) for t in (q, k, v, g)))
+    assert torch.equal(out[0], want[inside]) and torch.equal(state, last)
+
+
+def test_calls_of_several_threads_and_streams():
+    """Plans are shared by a process' threads: each call's bits are what it gives alone."""
+    def inputs(seed):
+        gen = torch.Generator(device=DEV).manual_seed(seed)
+        q = torch.randn(1, 700, 4, 64, generator=gen, device=DEV).to(BF16)
+        return q, -torch.rand(1, 700, 4, generator=gen, device=DEV)
+
+    def call(q, g):
+        leaf = q.clone().requires_grad_()
+        out, _ = decay_attention(leaf, q, q, g)
+        return out.detach(), torch.autograd.grad(out, [leaf], q)[0], layer_norm(q)
+
+    seeds, got = range(4), {}
+    data = [inputs(s) for s in seeds]
+    want = [call(*d) for d in data]
+    torch.cuda.synchronize()
+
+    def work(seed):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got[seed] = [call(*data[seed]) for _ in range(10)]
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in seeds]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(torch.equal(a, b) for s in seeds for x in got[s] for a, b in zip(x, want[s]))
