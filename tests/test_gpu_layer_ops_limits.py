@@ -106,7 +106,7 @@ def test_as_many_slots_as_a_step_looks_through():
 def test_attention_beyond_2_to_the_31_elements():
     """Values of 4.8 GB: a decay of -inf makes what is behind it, gradients too, what the tail alone gives, bit for bit."""
     T, Hk, Hv, K, V = 131072, 16, 144, 16, 128
-    cut, tail = T - 1024, 3072         # whole chunks; segments differ, but decays forget a token within a chunk or two
+    cut, tail = T - 1024, 2880         # whole chunks; segments differ, but decays forget a token within a chunk or two
     assert T * Hv * V > 2 ** 31
     gen = torch.Generator(device=DEV).manual_seed(8)
     q, k = (torch.empty(1, T, Hk, K, device=DEV, dtype=BF16).normal_(0, 0.5, generator=gen) for _ in range(2))
